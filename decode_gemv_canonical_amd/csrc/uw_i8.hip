@@ -1,0 +1,384 @@
+// Product of 8-bit integer matrices with a scale per token and per channel,
+// on the gfx950 matrix cores:
+//
+//   Y[b, n] = x_scale[b] * w_scale[n] * sum_k X[b, k] W[n, k] (+ bias[n])
+//
+// The sum is exact: v_mfma_i32_16x16x64_i8 adds into 32-bit integers, and
+// cols <= 131071 keeps |sum| <= 131071 * 128 * 128 < 2^31.  So the result does
+// not depend on tiles, waves or splits of k; it is rounded to fp32, scaled
+// in fp32 and rounded once more where Y is bf16.
+//
+// W [rows, cols] and X [batch, cols] are both k-contiguous.  A = 16 weight
+// rows, B = 16 activation rows: lane (r = lane % 16, q = lane / 16) holds 16
+// consecutive bytes of row r, at the same k for both operands; lane (r, q) of
+// the result holds weight rows 4 q .. 4 q + 3 for activation row r, four
+// consecutive values of a row of Y.
+#include <algorithm>
+
+#include "uw_device.h"
+
+namespace uw {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kXcds = 8;
+
+struct I8Args {
+  const int8_t* W;
+  const float* sw;
+  const int8_t* X;
+  const float* sx;
+  const float* bias;  // may be null
+  char* Y;
+  int64_t rows, cols, ldw, batch, ldx, ldy;
+};
+
+__device__ __forceinline__ i32x4 mfma_i8(const u32x4& a, const u32x4& b, const i32x4& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ u32x4 load16_any(const int8_t* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
+// 16 bytes of a row at p, of which `left` lie inside it (may be <= 0); the
+// others read as zero and are not touched.
+__device__ __forceinline__ u32x4 load16_tail(const int8_t* p, int64_t left) {
+  if (left >= 16) return load16_any(p);
+  u32x4 v{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 15; ++e)
+    if (e < left) v[e / 4] |= uint32_t(uint8_t(p[e])) << (8 * (e & 3));
+  return v;
+}
+
+// Four consecutive values of row b of Y, weight rows n .. n + 3.
+template <bool YBF16>
+__device__ __forceinline__ void store_y4(const I8Args& a, int64_t b, int64_t n, const i32x4& acc) {
+  if (b >= a.batch || n >= a.rows) return;
+  const float sx = a.sx[b];
+  const int m = int(std::min<int64_t>(4, a.rows - n));
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (e >= m) continue;
+    v[e] = float(acc[e]) * (sx * a.sw[n + e]);
+    if (a.bias) v[e] += a.bias[n + e];
+  }
+  if (YBF16) {
+    uint16_t* y = reinterpret_cast<uint16_t*>(a.Y) + b * a.ldy + n;
+    uint16_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = e < m ? f32_to_bf16(v[e]) : 0;
+    if (m == 4) {
+      __builtin_memcpy(y, w, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < m) y[e] = w[e];
+    }
+  } else {
+    float* y = reinterpret_cast<float*>(a.Y) + b * a.ldy + n;
+    if (m == 4) {
+      __builtin_memcpy(y, v, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < m) y[e] = v[e];
+    }
+  }
+}
+
+// Operands straight from global memory into registers: RB blocks of 16 weight
+// rows and TB tiles of 16 activation rows per workgroup, whose waves split k:
+// wave w takes the 256-byte groups w, w + KS, ... and the partial tiles are
+// summed in LDS.  The next group's loads are issued before this group's
+// products.  Rows may start at any byte; nothing outside a row is read.
+template <int RB, int TB, bool YBF16>
+__global__ __launch_bounds__(512) void i8_direct_kernel(I8Args a, int n_groups, int ny) {
+  const int L = int(blockIdx.x);
+  const int grp = (L / (kXcds * ny)) * kXcds + L % kXcds;
+  const int y = (L / kXcds) % ny;
+  if (grp >= n_groups) return;  // whole workgroups
+  const int KS = int(blockDim.x) / kWave;
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int r = lane % 16, q = lane / 16;
+  const int64_t row0 = int64_t(grp) * 16 * RB, b0 = int64_t(y) * 16 * TB;
+  const int8_t* wr[RB];
+  const int8_t* xr[TB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) wr[i] = a.W + std::min<int64_t>(row0 + 16 * i + r, a.rows - 1) * a.ldw + 16 * q;
+#pragma unroll
+  for (int t = 0; t < TB; ++t) xr[t] = a.X + std::min<int64_t>(b0 + 16 * t + r, a.batch - 1) * a.ldx + 16 * q;
+  i32x4 acc[RB][TB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int t = 0; t < TB; ++t) acc[i][t] = i32x4{0, 0, 0, 0};
+  const int nfull = int(a.cols / 256);
+  u32x4 wc[RB][4], xc[TB][4], wn[RB][4], xn[TB][4];
+  auto load = [&](int g, u32x4 (&w)[RB][4], u32x4 (&x)[TB][4]) {
+    const int64_t k = int64_t(g) * 256;
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) w[i][s] = load16_any(wr[i] + k + 64 * s);
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) x[t][s] = load16_any(xr[t] + k + 64 * s);
+  };
+  auto mul = [&](const u32x4 (&w)[RB][4], const u32x4 (&x)[TB][4]) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[i][t] = mfma_i8(w[i][s], x[t][s], acc[i][t]);
+  };
+  int g = wave;
+  if (g < nfull) load(g, wc, xc);
+  while (g < nfull) {
+    const int next = g + KS;
+    if (next < nfull) load(next, wn, xn);
+    mul(wc, xc);
+    g = next;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i) wc[i][s] = wn[i][s];
+#pragma unroll
+      for (int t = 0; t < TB; ++t) xc[t][s] = xn[t][s];
+    }
+  }
+  if (a.cols % 256 && nfull % KS == wave) {
+    const int64_t k = int64_t(nfull) * 256, left = a.cols - k - 16 * q;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i) wc[i][s] = load16_tail(wr[i] + k + 64 * s, left - 64 * s);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) xc[t][s] = load16_tail(xr[t] + k + 64 * s, left - 64 * s);
+    }
+    mul(wc, xc);
+  }
+  if (KS == 1) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) store_y4<YBF16>(a, b0 + 16 * t + r, row0 + 16 * i + 4 * q, acc[i][t]);
+    return;
+  }
+  // partial tile (i, t) of wave w at ((w * RB + i) * TB + t) KB
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+      st128(uint32_t(((wave * RB + i) * TB + t) * 1024 + 16 * lane), __builtin_bit_cast(uint4, acc[i][t]));
+  __syncthreads();
+  for (int idx = wave; idx < RB * TB; idx += KS) {
+    i32x4 sum{0, 0, 0, 0};
+    for (int w = 0; w < KS; ++w)
+      sum += __builtin_bit_cast(i32x4, ld128(uint32_t((w * RB * TB + idx) * 1024 + 16 * lane)));
+    store_y4<YBF16>(a, b0 + 16 * (idx % TB) + r, row0 + 16 * (idx / TB) + 4 * q, sum);
+  }
+}
+
+// 16 bytes per lane from the buffer resource at byte voff + soff into LDS at
+// m0 + 16 * lane (all lanes active).
+__device__ __forceinline__ void stage_load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t m0) {
+  asm volatile(
+      "s_nop 4\n"
+      "s_mov_b32 m0, %[m]\n"
+      "s_nop 0\n"
+      "buffer_load_dwordx4 %[v], %[r], %[s] offen lds"
+      :
+      : [m] "s"(m0), [v] "v"(voff), [r] "s"(r), [s] "s"(soff)
+      : "memory");
+}
+
+// Both operands staged through LDS by direct loads (no registers), in a ring
+// of ST stages of 128 bytes of k: BW weight rows and BB activation rows per
+// workgroup, whose WGW x WGB waves each hold a BW / WGW by BB / WGB tile.  A
+// 16-byte chunk c of staged row r sits at chunk c ^ (r % 8) of its 128-byte
+// row, so that the 8 rows an operand read touches at a time lie in 8
+// different bank groups.  Needs both operands 16-byte aligned with strides
+// that are multiples of 16; the last cols % 128 bytes go through registers,
+// zero-filled, and nothing outside a row is read.
+template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16>
+__global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
+  constexpr int NW = WGW * WGB;
+  constexpr int WI = BW / WGW / 16, BJ = BB / WGB / 16;
+  constexpr int LW = BW / 8 / NW, LB = BB / 8 / NW;  // 1 KB loads per wave and stage
+  constexpr uint32_t kWBytes = BW * 128, kStage = (BW + BB) * 128;
+  static_assert(BW % (8 * NW) == 0 && BB % (8 * NW) == 0, "whole loads");
+  // workgroups are dealt to the XCDs round-robin: each XCD takes a run of
+  // tiles, 4 activation tiles deep, so that its L2 serves the rereads
+  const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
+  if (id >= nw_tiles * nb_tiles) return;  // whole workgroups
+  constexpr int kDeep = 4;
+  const int strip = id / (kDeep * nw_tiles);
+  const int deep = min(kDeep, nb_tiles - strip * kDeep);
+  const int in = id - strip * kDeep * nw_tiles;
+  const int64_t row0 = int64_t(in / deep) * BW, b0 = (int64_t(strip) * kDeep + in % deep) * BB;
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int lrow = lane / 8, lchunk = (lane % 8) ^ lrow;
+  const int8_t* Wt = a.W + row0 * a.ldw;
+  const int8_t* Xt = a.X + b0 * a.ldx;
+  const int wlast = int(std::min<int64_t>(BW, a.rows - row0)) - 1, blast = int(std::min<int64_t>(BB, a.batch - b0)) - 1;
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(Wt), int16_t(0), int(int64_t(wlast) * a.ldw + a.cols), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(Xt), int16_t(0), int(int64_t(blast) * a.ldx + a.cols), 0x00020000);
+  // staged row 8 (u NW + wave) + lrow of load u; rows past the last are the last one again
+  uint32_t wvo[LW], xvo[LB];
+#pragma unroll
+  for (int u = 0; u < LW; ++u) wvo[u] = uint32_t(min(8 * (u * NW + wave) + lrow, wlast)) * uint32_t(a.ldw) + 16 * lchunk;
+#pragma unroll
+  for (int u = 0; u < LB; ++u) xvo[u] = uint32_t(min(8 * (u * NW + wave) + lrow, blast)) * uint32_t(a.ldx) + 16 * lchunk;
+  auto issue = [&](int kb, int st) {
+    const uint32_t base = uint32_t(st) * kStage, k = uint32_t(kb) * 128;
+#pragma unroll
+    for (int u = 0; u < LW; ++u) stage_load(rw, wvo[u], k, base + uint32_t(u * NW + wave) * 1024);
+#pragma unroll
+    for (int u = 0; u < LB; ++u) stage_load(rx, xvo[u], k, base + kWBytes + uint32_t(u * NW + wave) * 1024);
+  };
+  const int r = lane % 16, q = lane / 16;
+  const int ww = wave / WGB, wb = wave % WGB;
+  const uint32_t arow = uint32_t(ww * WI * 16 + r) * 128, xrow = kWBytes + uint32_t(wb * BJ * 16 + r) * 128;
+  i32x4 acc[WI][BJ];
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  auto multiply = [&](uint32_t base) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t ch = uint32_t(((4 * s + q) ^ (r & 7)) * 16);
+      u32x4 x[BJ];
+#pragma unroll
+      for (int j = 0; j < BJ; ++j) x[j] = __builtin_bit_cast(u32x4, ld128(base + xrow + uint32_t(j) * 2048 + ch));
+#pragma unroll
+      for (int i = 0; i < WI; ++i) {
+        const u32x4 w = __builtin_bit_cast(u32x4, ld128(base + arow + uint32_t(i) * 2048 + ch));
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) acc[i][j] = mfma_i8(w, x[j], acc[i][j]);
+      }
+    }
+  };
+  const int nkb = int(a.cols / 128);
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i)
+    if (i < nkb) issue(i, i);
+  int st = 0;
+  for (int kb = 0; kb < nkb; ++kb) {
+    // this wave's loads of block kb have landed once only the younger
+    // blocks' (ST - 2 of them) may be pending
+    if (kb + ST - 2 < nkb) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((ST - 2) * (LW + LB)) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();  // every wave's loads of block kb have landed; block kb - 1 is no longer read
+    if (kb + ST - 1 < nkb) issue(kb + ST - 1, st == 0 ? ST - 1 : st - 1);
+    multiply(uint32_t(st) * kStage);
+    st = st + 1 == ST ? 0 : st + 1;
+  }
+  if (a.cols % 128) {
+    const int64_t k = int64_t(nkb) * 128 + 16 * lchunk;
+    lds_barrier();  // stage 0 may still be read
+#pragma unroll
+    for (int u = 0; u < LW; ++u)
+      st128(uint32_t(u * NW + wave) * 1024 + 16 * lane,
+            __builtin_bit_cast(uint4, load16_tail(Wt + int64_t(wvo[u]) - 16 * lchunk + k, a.cols - k)));
+#pragma unroll
+    for (int u = 0; u < LB; ++u)
+      st128(kWBytes + uint32_t(u * NW + wave) * 1024 + 16 * lane,
+            __builtin_bit_cast(uint4, load16_tail(Xt + int64_t(xvo[u]) - 16 * lchunk + k, a.cols - k)));
+    lds_barrier();
+    multiply(0);
+  }
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int j = 0; j < BJ; ++j)
+      store_y4<YBF16>(a, b0 + (wb * BJ + j) * 16 + r, row0 + (ww * WI + i) * 16 + 4 * q, acc[i][j]);
+}
+
+template <int RB, int TB>
+int run_direct(const I8Args& a, int yt, int ks, hipStream_t s) {
+  const int64_t n_groups = (a.rows + 16 * RB - 1) / (16 * RB), ny = (a.batch + 16 * TB - 1) / (16 * TB);
+  const int64_t grid = (n_groups + kXcds - 1) / kXcds * kXcds * ny;
+  if (grid * ks * kWave >= int64_t(1) << 32) return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
+  const size_t lds = ks > 1 ? size_t(ks) * RB * TB * 1024 : 0;
+  auto kern = yt == UW_BF16 ? i8_direct_kernel<RB, TB, true> : i8_direct_kernel<RB, TB, false>;
+  allow_full_lds(kern);
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(ks * kWave), lds, s, a, int(n_groups), int(ny));
+  return hip_check(hipGetLastError(), "i8_direct_kernel launch");
+}
+
+template <int BW, int BB, int WGW, int WGB, int ST>
+int run_stage(const I8Args& a, int yt, hipStream_t s) {
+  const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
+  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
+  constexpr int kThreads = 64 * WGW * WGB;
+  if (per_xcd * kXcds * kThreads >= int64_t(1) << 32)
+    return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
+  auto kern = yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, true> : i8_stage_kernel<BW, BB, WGW, WGB, ST, false>;
+  allow_full_lds(kern);
+  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * 128, s, a, int(nw),
+                     int(nb), int(per_xcd));
+  return hip_check(hipGetLastError(), "i8_stage_kernel launch");
+}
+
+constexpr int kShapes = 11;       // 0 = heuristic
+constexpr int kDirectShapes = 5;  // 1..5; the others are staged
+
+bool stage_ok(const I8Args& a) {
+  // 16-byte chunks, and 32-bit offsets inside a tile of 256 rows
+  return reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldw % 16 == 0 &&
+         a.ldx % 16 == 0 && a.ldw < (int64_t(1) << 22) && a.ldx < (int64_t(1) << 22);
+}
+
+}  // namespace
+
+int i8_gemm_shape_count() { return kShapes; }
+
+bool i8_gemm_shape_ok(const int8_t* W, int64_t rows, int64_t ldw, const int8_t* X, int64_t batch, int64_t ldx, int shape) {
+  I8Args a{};
+  a.W = W;
+  a.X = X;
+  a.ldw = rows > 1 ? ldw : 0;
+  a.ldx = batch > 1 ? ldx : 0;
+  return shape <= kDirectShapes || stage_ok(a);
+}
+
+int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, const float* sw, const int8_t* X,
+                   int64_t batch, int64_t ldx, const float* sx, const float* bias, void* Y, int64_t ldy, int yt,
+                   int shape, int ks, void* stream) {
+  // a single row has no stride
+  const I8Args a{W, sw, X, sx, bias, static_cast<char*>(Y), rows, cols, rows > 1 ? ldw : 0, batch, batch > 1 ? ldx : 0, ldy};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (shape <= 0) {
+    if (batch <= 16) shape = 1;
+    else if (batch <= 32) shape = 3;
+    else if (!stage_ok(a)) shape = 5;
+    else if (batch <= 64) shape = 6;
+    else shape = (rows + 255) / 256 * ((batch + 255) / 256) >= 256 ? 10 : (rows + 127) / 128 * ((batch + 127) / 128) >= 128 ? 8 : 6;
+  }
+  if (ks <= 0) ks = shape <= 3 ? 8 : 4;
+  switch (shape) {
+    case 1: return run_direct<1, 1>(a, yt, ks, s);
+    case 2: return run_direct<2, 1>(a, yt, ks, s);
+    case 3: return run_direct<1, 2>(a, yt, ks, s);
+    case 4: return run_direct<2, 2>(a, yt, ks, s);
+    case 5: return run_direct<2, 4>(a, yt, ks, s);
+    case 6: return run_stage<64, 64, 2, 2, 4>(a, yt, s);
+    case 7: return run_stage<128, 64, 4, 1, 4>(a, yt, s);
+    case 8: return run_stage<128, 128, 2, 2, 3>(a, yt, s);
+    case 9: return run_stage<256, 128, 4, 2, 3>(a, yt, s);
+    default: return run_stage<256, 256, 2, 4, 2>(a, yt, s);
+  }
+}
+
+}  // namespace uw

@@ -168,6 +168,24 @@ int launch_bf16_gemm(const uint16_t* W, int64_t rows, int64_t cols, int64_t ldw,
                      int ks = 0);
 bool bf16_gemm_supported(int64_t cols, int64_t batch, int xt, std::string* why);
 bool bf16_gemm_on_mfma(const void* X, int64_t batch, int64_t cols, int64_t ldx, int xt);
+// Row operators (uw_rows.hip) and the 8-bit product (uw_i8.hip).
+int launch_rmsnorm(const void* X, int64_t batch, int64_t cols, int64_t ldx, int xt, const void* R, int64_t ldr, int rt,
+                   void* H, int64_t ldh, const void* gain, int gt, float eps, void* Y, int64_t ldy, int yt,
+                   float* scale, void* stream);
+int launch_silu_mul(const void* G, int64_t ldg, const void* U, int64_t ldu, int xt, int64_t batch, int64_t cols,
+                    void* Y, int64_t ldy, int yt, float* scale, void* stream);
+int launch_i8_quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, int xt, int8_t* Q, int64_t ldq,
+                       float* scale, void* stream);
+int launch_i8_dequantize(const int8_t* Q, int64_t rows, int64_t cols, int64_t ldq, const float* scale, void* Y,
+                         int64_t ldy, int yt, void* stream);
+// shape: 0 = heuristic, else an index below i8_gemm_shape_count(); ks: waves
+// per workgroup splitting k in the shapes that read straight from global
+// memory (0 = auto).  i8_gemm_shape_ok: whether a shape takes these operands.
+int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, const float* sw, const int8_t* X,
+                   int64_t batch, int64_t ldx, const float* sx, const float* bias, void* Y, int64_t ldy, int yt,
+                   int shape, int ks, void* stream);
+int i8_gemm_shape_count();
+bool i8_gemm_shape_ok(const int8_t* W, int64_t rows, int64_t ldw, const int8_t* X, int64_t batch, int64_t ldx, int shape);
 // Cache eviction of the autotuner: read `bytes` (multiple of 16) at src.
 int launch_read_probe(const void* src, size_t bytes, void* sink, void* stream);
 // The allocation-free entry point's scratch (uw_static.hip): its size, the

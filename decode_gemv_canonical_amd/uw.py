@@ -25,6 +25,7 @@ UW_ERR_HIP = -4
 UW_ERR_UNSUPPORTED = -5
 UW_F32 = 0
 UW_BF16 = 1
+UW_I8 = 2
 UW_VARIANT_AUTO = 0
 UW_VARIANT_FUSED = 1
 UW_VARIANT_DECOMPRESS_GEMM = 2
@@ -104,6 +105,13 @@ def _load() -> ctypes.CDLL:
         "uw_palette_transcode_size": (SZ, [P]),
         "uw_palette_transcode": (I, [P, P, SZ, P]),
         "uw_palette_create_transcoded": (I, [P, P, ctypes.POINTER(P)]),
+        "uw_rmsnorm": (I, [P, I64, I64, I64, I, P, I64, I, P, I64, P, I, ctypes.c_float, P, I64, I, P, P]),
+        "uw_silu_mul": (I, [P, I64, P, I64, I, I64, I64, P, I64, I, P, P]),
+        "uw_i8_quantize": (I, [P, I64, I64, I64, I, P, I64, P, P]),
+        "uw_i8_dequantize": (I, [P, I64, I64, I64, P, P, I64, I, P]),
+        "uw_i8_gemm": (I, [P, I64, I64, I64, P, P, I64, I64, P, P, P, I64, I, P]),
+        "uw_i8_gemm_shaped": (I, [P, I64, I64, I64, P, P, I64, I64, P, P, P, I64, I, I, I, P]),
+        "uw_i8_gemm_shape_count": (I, []),
         "uw_sched_create": (I, [P, SZ, I, I, ctypes.POINTER(P)]),
         "uw_sched_destroy": (None, [P]),
         "uw_sched_decode_cus": (I, [P]),
@@ -555,6 +563,208 @@ def uw_sched_gemm(sched: int, slot: int, handle: int, X, Y, stream=None) -> None
     batch = _gemm_operands(handle, X, Y)
     _check(_lib.uw_sched_gemm(sched, slot, X.data_ptr(), batch, X.stride(0), _dtype_code(X), Y.data_ptr(), Y.stride(0),
                               _dtype_code(Y), _stream(stream)), "uw_sched_gemm")
+
+
+# -- the 8-bit activation path ------------------------------------------------
+# These take no handle: the current device is the one the tensors have to be
+# on, and every shape is checked here, where the buffers' sizes are known.
+
+def _op_device(t, name: str) -> int:
+    import torch
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _op_rows(t, n: int, cols: int, dev: int, name: str) -> int:
+    """Checks an [n, cols] row-major operand; its row stride."""
+    if t.dim() != 2 or t.shape != (n, cols):
+        raise ValueError(f"{name} must have shape ({n}, {cols}), got {tuple(t.shape)}")
+    ld, inner = t.stride()
+    if (inner != 1 and cols > 1) or (ld < cols and n > 1):
+        raise ValueError(f"{name} must have a unit inner stride and rows that do not overlap")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    return ld
+
+
+def _op_scale(t, n: int, dev: int, name: str) -> int:
+    """Checks a contiguous fp32 vector of n values; its address."""
+    import torch
+    if t.dtype != torch.float32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous float32 vector of {n} values on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _op_i8(t, name: str) -> None:
+    import torch
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be int8, got {t.dtype}")
+
+
+def _op_out(Y, scale, n: int, dev: int):
+    """The type code of a row operator's output, and its scales' address."""
+    import torch
+    if Y.dtype != torch.int8:
+        if scale is not None:
+            raise ValueError("scale goes with an int8 output")
+        return _dtype_code(Y), None
+    if scale is None:
+        raise ValueError("an int8 output needs a scale vector")
+    return UW_I8, _op_scale(scale, n, dev, "scale")
+
+
+def uw_rmsnorm(X, gain, Y, scale=None, residual=None, residual_out=None, eps: float = 1e-5, stream=None) -> None:
+    """h = X + residual, Y = h / sqrt(mean(h^2) + eps) * gain per row.  Y is
+    float32, bfloat16, or int8 with `scale` (one float32 per row).
+    residual_out receives h in the residual's dtype (the residual itself
+    updates the stream in place); gain may be None (all ones)."""
+    dev = _op_device(X, "X")
+    if X.dim() != 2:
+        raise ValueError(f"X must be 2-D, got shape {tuple(X.shape)}")
+    n, cols = X.shape
+    ldx = _op_rows(X, n, cols, dev, "X")
+    ldy = _op_rows(Y, n, cols, dev, "Y")
+    yt, sp = _op_out(Y, scale, n, dev)
+    rp = hp = gp = None
+    ldr = ldh = 0
+    rt = gt = UW_F32
+    if residual is not None:
+        ldr, rt, rp = _op_rows(residual, n, cols, dev, "residual"), _dtype_code(residual), residual.data_ptr()
+    if residual_out is not None:
+        if residual is None or residual_out.dtype != residual.dtype:
+            raise ValueError("residual_out needs a residual of its dtype")
+        ldh, hp = _op_rows(residual_out, n, cols, dev, "residual_out"), residual_out.data_ptr()
+    if gain is not None:
+        _check_vector(gain, cols, dev, "gain")
+        gt, gp = _dtype_code(gain), gain.data_ptr()
+    _check(_lib.uw_rmsnorm(X.data_ptr(), n, cols, ldx, _dtype_code(X), rp, ldr, rt, hp, ldh, gp, gt, eps, Y.data_ptr(),
+                           ldy, yt, sp, _stream(stream)), "uw_rmsnorm")
+
+
+def uw_silu_mul(G, U, Y, scale=None, stream=None) -> None:
+    """Y = G / (1 + exp(-G)) * U per element (halves of one product's rows, for
+    instance); Y and scale as for uw_rmsnorm."""
+    dev = _op_device(G, "G")
+    if G.dim() != 2:
+        raise ValueError(f"G must be 2-D, got shape {tuple(G.shape)}")
+    n, cols = G.shape
+    ldg = _op_rows(G, n, cols, dev, "G")
+    ldu = _op_rows(U, n, cols, dev, "U")
+    if U.dtype != G.dtype:
+        raise TypeError("G and U must have the same dtype")
+    ldy = _op_rows(Y, n, cols, dev, "Y")
+    yt, sp = _op_out(Y, scale, n, dev)
+    _check(_lib.uw_silu_mul(G.data_ptr(), ldg, U.data_ptr(), ldu, _dtype_code(G), n, cols, Y.data_ptr(), ldy, yt, sp,
+                            _stream(stream)), "uw_silu_mul")
+
+
+def uw_i8_quantize(X, Q, scale, stream=None) -> None:
+    """Rows of X (float32 or bfloat16) as int8 with one float32 scale each."""
+    dev = _op_device(X, "X")
+    if X.dim() != 2:
+        raise ValueError(f"X must be 2-D, got shape {tuple(X.shape)}")
+    n, cols = X.shape
+    ldx = _op_rows(X, n, cols, dev, "X")
+    _op_i8(Q, "Q")
+    ldq = _op_rows(Q, n, cols, dev, "Q")
+    _check(_lib.uw_i8_quantize(X.data_ptr(), n, cols, ldx, _dtype_code(X), Q.data_ptr(), ldq,
+                               _op_scale(scale, n, dev, "scale"), _stream(stream)), "uw_i8_quantize")
+
+
+def uw_i8_dequantize(Q, scale, Y, stream=None) -> None:
+    """Y = Q * scale per row, float32 or bfloat16."""
+    dev = _op_device(Q, "Q")
+    _op_i8(Q, "Q")
+    if Q.dim() != 2:
+        raise ValueError(f"Q must be 2-D, got shape {tuple(Q.shape)}")
+    n, cols = Q.shape
+    ldq = _op_rows(Q, n, cols, dev, "Q")
+    ldy = _op_rows(Y, n, cols, dev, "Y")
+    _check(_lib.uw_i8_dequantize(Q.data_ptr(), n, cols, ldq, _op_scale(scale, n, dev, "scale"), Y.data_ptr(), ldy,
+                                 _dtype_code(Y), _stream(stream)), "uw_i8_dequantize")
+
+
+def _i8_operands(W, w_scale, X, x_scale, Y, bias):
+    dev = _op_device(W, "W")
+    _op_i8(W, "W")
+    _op_i8(X, "X")
+    if W.dim() != 2 or X.dim() != 2:
+        raise ValueError("W and X must be 2-D")
+    (rows, cols), n = W.shape, X.shape[0]
+    ldw = _op_rows(W, rows, cols, dev, "W")
+    ldx = _op_rows(X, n, cols, dev, "X")
+    ldy = _op_rows(Y, n, rows, dev, "Y")
+    return (W.data_ptr(), rows, cols, ldw, _op_scale(w_scale, rows, dev, "w_scale"), X.data_ptr(), n, ldx,
+            _op_scale(x_scale, n, dev, "x_scale"), None if bias is None else _op_scale(bias, rows, dev, "bias"),
+            Y.data_ptr(), ldy, _dtype_code(Y))
+
+
+def uw_i8_gemm(W, w_scale, X, x_scale, Y, bias=None, stream=None) -> None:
+    """Y[b, n] = x_scale[b] * w_scale[n] * sum_k X[b, k] W[n, k] (+ bias[n]),
+    int8 W [rows, cols] and X [batch, cols], float32 scales and bias, Y
+    float32 or bfloat16.  The sum is exact."""
+    _check(_lib.uw_i8_gemm(*_i8_operands(W, w_scale, X, x_scale, Y, bias), _stream(stream)), "uw_i8_gemm")
+
+
+def uw_i8_gemm_shaped(W, w_scale, X, x_scale, Y, shape: int, ks: int = 0, bias=None, stream=None) -> None:
+    _check(_lib.uw_i8_gemm_shaped(*_i8_operands(W, w_scale, X, x_scale, Y, bias), shape, ks, _stream(stream)),
+           "uw_i8_gemm_shaped")
+
+
+def uw_i8_gemm_shape_count() -> int:
+    return _lib.uw_i8_gemm_shape_count()
+
+
+def i8_rows(rows: int, cols: int, device="cuda"):
+    """An uninitialised int8 [rows, cols] whose rows start at multiples of 16
+    bytes: the layout uw_i8_gemm reads fastest."""
+    import torch
+    return torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8, device=device)[:, :cols]
+
+
+class Int8Matrix:
+    """A weight matrix in 8-bit integers with one scale per row, on the
+    current CUDA device: gemm takes the int8 activations that uw_rmsnorm,
+    uw_silu_mul or uw_i8_quantize write."""
+
+    def __init__(self, q, scale):
+        _op_i8(q, "q")
+        _op_rows(q, *q.shape, _op_device(q, "q"), "q")
+        _op_scale(scale, q.shape[0], q.get_device(), "scale")
+        self.q, self.scale = q, scale
+        self.rows, self.cols = q.shape
+
+    @classmethod
+    def from_weights(cls, W) -> "Int8Matrix":
+        """From a float32 or bfloat16 [rows, cols] on the device, on the current stream."""
+        import torch
+        q = i8_rows(*W.shape, device=W.device)
+        scale = torch.empty(W.shape[0], dtype=torch.float32, device=W.device)
+        uw_i8_quantize(W, q, scale)
+        return cls(q, scale)
+
+    @classmethod
+    def from_compressed(cls, m) -> "Int8Matrix":
+        """From a CompressedMatrix or PaletteMatrix (decompressed once, on the current stream)."""
+        return cls.from_weights(m.decompress())
+
+    def dequantize(self, out=None, out_dtype=None, stream=None):
+        import torch
+        if out is None:
+            out = torch.empty(self.rows, self.cols, dtype=out_dtype or torch.bfloat16, device=self.q.device)
+        uw_i8_dequantize(self.q, self.scale, out, stream)
+        return out
+
+    def gemm(self, X, x_scale, Y=None, bias=None, out_dtype=None, stream=None):
+        import torch
+        if Y is None:
+            Y = torch.empty(X.shape[0], self.rows, dtype=out_dtype or torch.float32, device=X.device)
+        uw_i8_gemm(self.q, self.scale, X, x_scale, Y, bias, stream)
+        return Y
 
 
 class DecodeAhead:

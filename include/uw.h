@@ -76,7 +76,11 @@ typedef enum {
   UW_ERR_UNSUPPORTED = -5  /* valid request that this build cannot run           */
 } uw_status;
 
-typedef enum { UW_F32 = 0, UW_BF16 = 1 } uw_dtype;
+typedef enum {
+  UW_F32 = 0,
+  UW_BF16 = 1,
+  UW_I8 = 2 /* 8-bit integers with an fp32 scale per row: outputs of uw_rmsnorm and uw_silu_mul only */
+} uw_dtype;
 
 /* Execution strategies for uw_gemm_fused ("four pipelines" paragraph: the
  * runtime picks one per matrix and batch size). */
@@ -563,6 +567,114 @@ int uw_sched_prefetch(uw_sched* s, const uw_matrix* m, void* stream, int* slot);
  */
 int uw_sched_gemm(uw_sched* s, int slot, const void* d_X, int64_t batch, int64_t ldx, int xt, void* d_Y, int64_t ldy,
                   int yt, void* stream);
+
+/*
+ * The 8-bit activation path around the products (not on the pages, whose
+ * weights stay lossless): the norm in front of a product, the gated
+ * activation between gate/up and down, matrices in 8-bit integers, and their
+ * product.  With bf16 outputs the first two feed the lossless products
+ * (uw_gemm_fused and the others); with UW_I8 outputs they feed uw_i8_gemm.
+ *
+ * A row p of 8-bit integers: s = max(max|p| / 127, 2^-126),
+ * q = p * (1 / s) rounded to nearest, ties to even, in fp32; p is about
+ * q * s.  A row that holds an infinity or a NaN gets q = 0 and a NaN scale.
+ *
+ * These calls take no handle, allocate nothing, use no workspace and only
+ * enqueue on `stream`; they may be captured into a graph, and calls on
+ * different streams do not disturb each other.  Rows start at any multiple of
+ * the element size (strides in elements).  Nothing outside the rows given is
+ * read or written.  batch (or rows) == 0 is a no-op.
+ */
+
+/*
+ * uw_rmsnorm (device) - h = x + r, y = h / sqrt(mean(h^2) + eps) * gain, row
+ * by row, fp32 arithmetic.
+ *   d_X      batch rows of cols >= 1 elements of xt (UW_F32 or UW_BF16), row
+ *            stride ldx.
+ *   d_R      the residual, rows of rt (UW_F32 or UW_BF16), stride ldr, or
+ *            NULL (h = x).  h is rounded to rt before it is squared.
+ *   d_H      receives h in rt, stride ldh; NULL: not kept.  May be d_R
+ *            itself (the stream updated in place, ldh == ldr) or d_X (where
+ *            rt == xt and ldh == ldx).  Needs d_R.
+ *   d_gain   cols elements of gt (UW_F32 or UW_BF16), or NULL (all ones).
+ *   eps      positive and finite.
+ *   d_Y      receives y in yt, stride ldy >= cols: UW_F32, UW_BF16 (nearest
+ *            even), or UW_I8 with d_scale (batch fp32 values; else ignored,
+ *            may be NULL): there p = h * gain and the scale is
+ *            s / sqrt(mean(h^2) + eps).  May be d_X itself (yt == xt,
+ *            ldy == ldx) where d_H is not d_X too.
+ * A row whose squares sum past the fp32 range comes out as zeros.
+ * Errors: UW_ERR_INVALID, UW_ERR_HIP.
+ */
+int uw_rmsnorm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int xt, const void* d_R, int64_t ldr, int rt,
+               void* d_H, int64_t ldh, const void* d_gain, int gt, float eps, void* d_Y, int64_t ldy, int yt,
+               float* d_scale, void* stream);
+
+/*
+ * uw_silu_mul (device) - p = g / (1 + exp(-g)) * u element by element, fp32
+ * arithmetic: a gated MLP's activation.  d_G and d_U hold batch rows of cols
+ * elements of xt with strides ldg and ldu (halves of one product's rows, for
+ * instance); d_Y, yt, ldy and d_scale as for uw_rmsnorm, and d_Y may be d_G
+ * or d_U itself (same type and stride).
+ * Errors: UW_ERR_INVALID, UW_ERR_HIP.
+ */
+int uw_silu_mul(const void* d_G, int64_t ldg, const void* d_U, int64_t ldu, int xt, int64_t batch, int64_t cols,
+                void* d_Y, int64_t ldy, int yt, float* d_scale, void* stream);
+
+/*
+ * uw_i8_quantize (device) - rows of xt (UW_F32 or UW_BF16) as 8-bit integers
+ * and one scale each: a weight matrix at load (uw_decompress's output, for
+ * instance), or activations that no norm wrote.
+ *   d_Q  rows of cols integers, stride ldq >= cols.   d_scale  rows values.
+ * Strides that are multiples of 16 and a 16-byte aligned d_Q let uw_i8_gemm
+ * use all its shapes.
+ * Errors: UW_ERR_INVALID, UW_ERR_HIP.
+ */
+int uw_i8_quantize(const void* d_X, int64_t rows, int64_t cols, int64_t ldx, int xt, int8_t* d_Q, int64_t ldq,
+                   float* d_scale, void* stream);
+
+/*
+ * uw_i8_dequantize (device) - the values 8-bit rows stand for, q * scale, in
+ * yt (UW_F32, or UW_BF16 rounded to nearest even), stride ldy >= cols.
+ * Errors: UW_ERR_INVALID, UW_ERR_HIP.
+ */
+int uw_i8_dequantize(const int8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq, const float* d_scale, void* d_Y,
+                     int64_t ldy, int yt, void* stream);
+
+/*
+ * uw_i8_gemm (device) - Y[b, n] = xs[b] * ws[n] * sum_k X[b, k] W[n, k]
+ * (+ bias[n]) on the matrix cores.  The sum is exact (32-bit integers), so
+ * results do not depend on the shape run.
+ *   d_W   rows x cols integers, row stride ldw >= cols; d_ws rows fp32 scales.
+ *   d_X   batch x cols integers, row stride ldx >= cols; d_xs batch scales.
+ *   d_bias  rows fp32 values, or NULL.
+ *   d_Y   batch rows of rows elements of yt (UW_F32, or UW_BF16 rounded to
+ *         nearest even), row stride ldy >= rows.
+ *   1 <= cols <= 131071 (the sum stays inside 32 bits for every input).
+ * Operands that are not 16-byte aligned, or whose strides are no multiples of
+ * 16, run on shapes that read them straight from global memory: slower above
+ * 32 rows.
+ * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (cols > 131071, more tiles than
+ *         a launch holds), UW_ERR_HIP.
+ */
+int uw_i8_gemm(const int8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, const float* d_ws, const int8_t* d_X,
+               int64_t batch, int64_t ldx, const float* d_xs, const float* d_bias, void* d_Y, int64_t ldy, int yt,
+               void* stream);
+
+/*
+ * uw_i8_gemm_shaped (device) - uw_i8_gemm with a given shape: shape in
+ * [1, uw_i8_gemm_shape_count()) picks the weight and batch rows a workgroup
+ * holds and whether the operands are staged in LDS, ks (1..8; 0 = auto) the
+ * waves that split k in the shapes that are not.
+ * Errors: as uw_i8_gemm; UW_ERR_INVALID for an unknown shape or ks,
+ *         UW_ERR_UNSUPPORTED for a staged shape on operands that are not
+ *         16-byte aligned with strides that are multiples of 16 (below 2^22).
+ */
+int uw_i8_gemm_shaped(const int8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, const float* d_ws, const int8_t* d_X,
+                      int64_t batch, int64_t ldx, const float* d_xs, const float* d_bias, void* d_Y, int64_t ldy,
+                      int yt, int shape, int ks, void* stream);
+/* Number of shape ids of uw_i8_gemm_shaped (shape 0 is the automatic one). */
+int uw_i8_gemm_shape_count(void);
 
 #ifdef __cplusplus
 }

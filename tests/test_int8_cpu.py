@@ -1,0 +1,148 @@
+"""The 8-bit activation path without a GPU: the oracle's own pins and the
+library's refusals (every bad call is turned away before any launch)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import int8 as o8
+
+uw = pytest.importorskip("decode_gemv_canonical_amd")
+INV, UNSUP, OK = uw.UW_ERR_INVALID, uw.UW_ERR_UNSUPPORTED, uw.UW_OK
+F32, BF16, I8 = uw.UW_F32, uw.UW_BF16, uw.UW_I8
+P = 1 << 20  # stands for a device address: a refused call never touches it
+
+
+def test_oracle_quantize_by_hand():
+    q, s = o8.quantize(np.array([[127.0, -63.5, 0.5, 1.5], [0, 0, 0, 0], [1, np.nan, 2, 3], [np.inf, 1, 2, 3]], np.float32))
+    assert s[0] == 1.0 and q[0].tolist() == [127, -64, 0, 2]  # ties to even: -63.5, 0.5, 1.5
+    assert s[1] == np.float32(2.0 ** -126) and not q[1].any()
+    assert np.isnan(s[2]) and np.isnan(s[3]) and not q[2:].any()
+
+
+def test_oracle_norm_and_silu_by_hand():
+    h = np.array([[3.0, 4.0]])
+    y = o8.rmsnorm(h, np.array([1.0, 2.0]), 1e-5)
+    r = 1 / np.sqrt(12.5 + float(np.float32(1e-5)))
+    assert np.allclose(y, [[3 * r, 8 * r]], rtol=1e-15)
+    assert o8.silu_mul(np.array([[0.0, -800.0]]), np.array([[5.0, 1.0]])).tolist() == [[0.0, 0.0]]
+
+
+def test_oracle_norm_matches_differences_of_scale():
+    # y does not change when h is scaled (eps small against mean(h^2)), and the integers do not depend on the norm
+    rng = np.random.default_rng(0)
+    h = rng.standard_normal((3, 50))
+    assert np.allclose(o8.rmsnorm(h * 64, None, 1e-12), o8.rmsnorm(h, None, 1e-12), rtol=1e-10)
+
+
+def norm(**k):
+    a = dict(X=P, batch=4, cols=64, ldx=64, xt=BF16, R=P, ldr=64, rt=BF16, H=P + 4096, ldh=64, gain=P, gt=BF16, eps=1e-5,
+             Y=P + 8192, ldy=64, yt=BF16, scale=None)
+    a.update(k)
+    return uw.library().uw_rmsnorm(*a.values(), None)
+
+
+@pytest.mark.parametrize("k", [
+    {"X": None}, {"Y": None}, {"batch": -1}, {"cols": 0}, {"cols": -3}, {"cols": 1 << 40}, {"batch": 1 << 40},
+    {"xt": I8}, {"xt": 7}, {"rt": I8}, {"rt": 9}, {"gt": I8}, {"gt": -1}, {"yt": 3}, {"ldx": 63}, {"ldr": 63},
+    {"ldh": 63}, {"ldy": 63}, {"ldx": 1 << 41}, {"eps": 0.0}, {"eps": -1e-5}, {"eps": float("nan")},
+    {"eps": float("inf")}, {"R": None}, {"X": P + 1}, {"Y": P + 1}, {"R": P + 1}, {"H": P + 1}, {"gain": P + 1},
+    {"yt": I8}, {"yt": I8, "scale": P + 2}, {"Y": P + 4096}, {"xt": F32, "X": P + 2},
+])
+def test_rmsnorm_refuses(k):
+    assert norm(**k) == INV
+    assert "uw_rmsnorm" in uw.uw_last_error()
+
+
+def test_empty_batches_are_no_ops():
+    lib = uw.library()
+    assert norm(batch=0) == OK
+    assert lib.uw_silu_mul(None, 64, None, 64, BF16, 0, 64, None, 64, BF16, None, None) == OK
+    assert lib.uw_i8_quantize(None, 0, 64, 64, BF16, None, 64, None, None) == OK
+    assert lib.uw_i8_dequantize(None, 0, 64, 64, None, None, 64, BF16, None) == OK
+    assert lib.uw_i8_gemm(P, 16, 64, 64, P, None, 0, 64, None, None, None, 16, F32, None) == OK
+
+
+def silu(**k):
+    a = dict(G=P, ldg=64, U=P, ldu=64, xt=BF16, batch=4, cols=64, Y=P, ldy=64, yt=BF16, scale=None)
+    a.update(k)
+    return uw.library().uw_silu_mul(*a.values(), None)
+
+
+@pytest.mark.parametrize("k", [
+    {"G": None}, {"U": None}, {"Y": None}, {"xt": I8}, {"yt": 5}, {"yt": I8}, {"ldg": 60}, {"ldu": 60}, {"ldy": 60},
+    {"batch": -2}, {"cols": 0}, {"G": P + 1}, {"U": P + 1},
+])
+def test_silu_mul_refuses(k):
+    assert silu(**k) == INV
+
+
+def quant(**k):
+    a = dict(X=P, rows=4, cols=64, ldx=64, xt=BF16, Q=P, ldq=64, scale=P)
+    a.update(k)
+    return uw.library().uw_i8_quantize(*a.values(), None)
+
+
+def dequant(**k):
+    a = dict(Q=P, rows=4, cols=64, ldq=64, scale=P, Y=P, ldy=64, yt=BF16)
+    a.update(k)
+    return uw.library().uw_i8_dequantize(*a.values(), None)
+
+
+@pytest.mark.parametrize("k", [{"X": None}, {"Q": None}, {"scale": None}, {"scale": P + 1}, {"xt": I8}, {"ldx": 3},
+                               {"ldq": 3}, {"rows": -1}, {"cols": 0}, {"X": P + 1}])
+def test_quantize_refuses(k):
+    assert quant(**k) == INV
+
+
+@pytest.mark.parametrize("k", [{"Y": None}, {"Q": None}, {"scale": None}, {"scale": P + 2}, {"yt": I8}, {"ldy": 3},
+                               {"ldq": 3}, {"rows": -1}, {"cols": 0}, {"Y": P + 1}])
+def test_dequantize_refuses(k):
+    assert dequant(**k) == INV
+
+
+def gemm(shape=None, ks=0, **k):
+    a = dict(W=P, rows=32, cols=64, ldw=64, ws=P, X=P, batch=4, ldx=64, xs=P, bias=None, Y=P, ldy=32, yt=F32)
+    a.update(k)
+    if shape is None:
+        return uw.library().uw_i8_gemm(*a.values(), None)
+    return uw.library().uw_i8_gemm_shaped(*a.values(), shape, ks, None)
+
+
+@pytest.mark.parametrize("k,want", [
+    ({"W": None}, INV), ({"X": None}, INV), ({"Y": None}, INV), ({"ws": None}, INV), ({"xs": None}, INV),
+    ({"ws": P + 1}, INV), ({"xs": P + 3}, INV), ({"bias": P + 2}, INV), ({"yt": I8}, INV), ({"yt": 4}, INV),
+    ({"rows": 0}, INV), ({"batch": -1}, INV), ({"cols": 0}, INV), ({"ldw": 63}, INV), ({"ldx": 63}, INV),
+    ({"ldy": 31}, INV), ({"Y": P + 2}, INV), ({"cols": 131072, "ldw": 131072, "ldx": 131072}, UNSUP),
+    ({"cols": 1 << 40}, INV), ({"rows": 1 << 40}, INV),
+])
+def test_gemm_refuses(k, want):
+    assert gemm(**k) == want
+    assert gemm(shape=1, **k) == want
+
+
+def test_gemm_shaped_refuses():
+    n = uw.uw_i8_gemm_shape_count()
+    assert n > 1
+    for shape in (0, -1, n):
+        assert gemm(shape=shape) == INV
+    for ks in (-1, 9):
+        assert gemm(shape=1, ks=ks) == INV
+    # the last shape is a staged one: 16-byte aligned operands and strides only
+    for k in ({"W": P + 4}, {"X": P + 8}, {"ldw": 72}, {"ldx": 65}, {"ldw": 1 << 22}):
+        assert gemm(shape=n - 1, **k) == UNSUP
+
+
+def test_binding_refuses_host_tensors():
+    x, q, s = torch.zeros(2, 64), torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2)
+    with pytest.raises(ValueError):
+        uw.uw_rmsnorm(x, None, x)
+    with pytest.raises(ValueError):
+        uw.uw_silu_mul(x, x, x)
+    with pytest.raises(ValueError):
+        uw.uw_i8_quantize(x, q, s)
+    with pytest.raises(ValueError):
+        uw.uw_i8_dequantize(q, s, x)
+    with pytest.raises(ValueError):
+        uw.uw_i8_gemm(q, s, q, s, torch.zeros(2, 2))
+    with pytest.raises(ValueError):
+        uw.Int8Matrix(q, s)
