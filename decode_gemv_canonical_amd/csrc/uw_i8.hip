@@ -48,10 +48,15 @@ __device__ __forceinline__ u32x4 load16_any(const int8_t* p) {
 // others read as zero and are not touched.
 __device__ __forceinline__ u32x4 load16_tail(const int8_t* p, int64_t left) {
   if (left >= 16) return load16_any(p);
-  u32x4 v{0u, 0u, 0u, 0u};
+  uint32_t b[15];  // all loads before the first use
+#pragma unroll
+  for (int e = 0; e < 15; ++e) b[e] = 0u;
 #pragma unroll
   for (int e = 0; e < 15; ++e)
-    if (e < left) v[e / 4] |= uint32_t(uint8_t(p[e])) << (8 * (e & 3));
+    if (e < left) b[e] = uint8_t(p[e]);
+  u32x4 v{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 15; ++e) v[e / 4] |= b[e] << (8 * (e & 3));
   return v;
 }
 
@@ -188,26 +193,183 @@ __global__ __launch_bounds__(512) void i8_direct_kernel(I8Args a, int n_groups, 
 }
 
 // 16 bytes per lane from the buffer resource at byte voff + soff into LDS at
-// m0 + 16 * lane (all lanes active).
+// m0 + 16 * lane (all lanes active).  NT: non-temporal, for operands that are
+// read once.
+template <bool NT>
 __device__ __forceinline__ void stage_load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t m0) {
-  asm volatile(
-      "s_nop 4\n"
-      "s_mov_b32 m0, %[m]\n"
-      "s_nop 0\n"
-      "buffer_load_dwordx4 %[v], %[r], %[s] offen lds"
-      :
-      : [m] "s"(m0), [v] "v"(voff), [r] "s"(r), [s] "s"(soff)
-      : "memory");
+  if (NT) {
+    asm volatile(
+        "s_nop 4\n"
+        "s_mov_b32 m0, %[m]\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %[v], %[r], %[s] offen nt lds"
+        :
+        : [m] "s"(m0), [v] "v"(voff), [r] "s"(r), [s] "s"(soff)
+        : "memory");
+  } else {
+    asm volatile(
+        "s_nop 4\n"
+        "s_mov_b32 m0, %[m]\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %[v], %[r], %[s] offen lds"
+        :
+        : [m] "s"(m0), [v] "v"(voff), [r] "s"(r), [s] "s"(soff)
+        : "memory");
+  }
 }
 
-// Both operands staged through LDS by direct loads (no registers), in a ring
-// of ST stages of 128 bytes of k: BW weight rows and BB activation rows per
-// workgroup, whose WGW x WGB waves each hold a BW / WGW by BB / WGB tile.  A
-// 16-byte chunk c of staged row r sits at chunk c ^ (r % 8) of its 128-byte
-// row, so that the 8 rows an operand read touches at a time lie in 8
-// different bank groups.  Needs both operands 16-byte aligned with strides
-// that are multiples of 16; the last cols % 128 bytes go through registers,
-// zero-filled, and nothing outside a row is read.
+// Staging of an operand's tile: rows of 128 bytes of k in LDS, the 16-byte
+// chunk c of row r at chunk c ^ (r % 8), so that the 8 rows an operand read
+// touches at a time lie in 8 different bank groups.  One load moves 8 rows:
+// lane l puts row l / 8's chunk (l % 8) ^ (l / 8) at 16 l.  Needs a 16-byte
+// aligned operand whose stride is a multiple of 16.
+//
+// The block that holds the end of the rows is loaded like the others, but
+// lanes past the last chunk of their row read that chunk again: no address
+// lies outside the 16-byte chunks that hold the operand (and the buffer ends
+// at the last row's last 4-byte word).  What lies past `cols` is masked out
+// of the activation operand when it is read back (whole numbers: any value
+// times zero is zero).
+struct Staged {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int last;  // the tile's last row; the rows past it are that row again
+
+  __device__ __forceinline__ Staged(const int8_t* tile, int64_t rows, int64_t cols, int64_t ld, int tile_rows)
+      : last(int(std::min<int64_t>(tile_rows, rows)) - 1) {
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(tile), int16_t(0),
+                                             int(int64_t(last) * ld + (cols + 3) / 4 * 4), 0x00020000);
+  }
+  // byte offset of staged row `row` (of the lane) at k = 0
+  __device__ __forceinline__ uint32_t row_offset(int row, int64_t ld) const {
+    return uint32_t(min(row, last)) * uint32_t(ld);
+  }
+};
+
+// Masks of the 16 bytes that lane (r, q) reads at step s of the block at k.
+__device__ __forceinline__ u32x4 tail_mask(int64_t cols, int64_t k, int s, int q) {
+  const int left = int(std::min<int64_t>(cols - k, 128)) - 16 * (4 * s + q);
+  u32x4 m;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int n = left - 4 * d;
+    m[d] = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+  }
+  return m;
+}
+
+// s_waitcnt vmcnt for a ring: at most `young` groups of L loads may stay
+// outstanding, young <= MAX.
+template <int L, int MAX>
+__device__ __forceinline__ void wait_ring(int young) {
+  if (young >= MAX) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MAX * L) : "memory");
+  } else if constexpr (MAX > 0) {
+    wait_ring<L, MAX - 1>(young);
+  }
+}
+
+// Small batches: a workgroup holds BW weight rows and BB activation rows, and
+// its KW waves split k: wave w takes the 128-byte blocks w, w + KW, ... for the
+// whole tile.  A wave stages its blocks into its own ring of ST slots in LDS
+// by direct loads and reads them back as operands, so nothing but its own
+// loads is ever waited for: no barrier until the partial tiles are summed at
+// the end.  A slot is refilled as soon as its operands are in registers, so
+// ST blocks are in flight.  NT: the weights are loaded non-temporally.
+template <int BW, int BB, int KW, int ST, bool NT, bool YBF16>
+__global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tiles, int nb_tiles) {
+  constexpr int WI = BW / 16, BJ = BB / 16;
+  constexpr int LW = BW / 8, LB = BB / 8, L = LW + LB;  // 1 KB loads per block
+  constexpr uint32_t kWBytes = BW * 128, kSlot = (BW + BB) * 128;
+  static_assert(ST * L < 64, "vmcnt");
+  // the batch tiles of one weight tile run back to back on one XCD
+  const int id = int(blockIdx.x);
+  const int wt = (id / (kXcds * nb_tiles)) * kXcds + id % kXcds, y = (id / kXcds) % nb_tiles;
+  if (wt >= nw_tiles) return;  // whole workgroups
+  const int64_t row0 = int64_t(wt) * BW, b0 = int64_t(y) * BB;
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int lrow = lane / 8, lchunk = (lane % 8) ^ lrow;
+  const Staged tw(a.W + row0 * a.ldw, a.rows - row0, a.cols, a.ldw, BW);
+  const Staged tx(a.X + b0 * a.ldx, a.batch - b0, a.cols, a.ldx, BB);
+  uint32_t wvo[LW], xvo[LB];
+#pragma unroll
+  for (int u = 0; u < LW; ++u) wvo[u] = tw.row_offset(8 * u + lrow, a.ldw) + 16 * lchunk;
+#pragma unroll
+  for (int u = 0; u < LB; ++u) xvo[u] = tx.row_offset(8 * u + lrow, a.ldx) + 16 * lchunk;
+  const uint32_t ring = uint32_t(wave) * (ST * kSlot);
+  const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
+  // in the last block, how far a lane's chunk lies past the row's last one
+  const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % 128) / 16));
+  auto issue = [&](int i, int st) {
+    const int kb = wave + KW * i;
+    const uint32_t base = ring + uint32_t(st) * kSlot, k = uint32_t(__builtin_amdgcn_readfirstlane(kb)) * 128, back = kb == nkb - 1 ? over : 0;
+#pragma unroll
+    for (int u = 0; u < LW; ++u) stage_load<NT>(tw.rsrc, wvo[u] - back, k, base + u * 1024);
+#pragma unroll
+    for (int u = 0; u < LB; ++u) stage_load<false>(tx.rsrc, xvo[u] - back, k, base + kWBytes + u * 1024);
+  };
+  const int r = lane % 16, q = lane / 16;
+  i32x4 acc[WI][BJ];
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < ST; ++i)
+    if (i < n) issue(i, i);
+  int st = 0;
+  for (int i = 0; i < n; ++i) {
+    wait_ring<L, ST - 1>(n - 1 - i);  // block i has landed
+    const uint32_t base = ring + uint32_t(st) * kSlot;
+    u32x4 w[WI][2], x[BJ][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t at = base + uint32_t(r) * 128 + uint32_t(((4 * s + q) ^ (r & 7)) * 16);
+#pragma unroll
+      for (int e = 0; e < WI; ++e) w[e][s] = __builtin_bit_cast(u32x4, ld128(at + uint32_t(e) * 2048));
+#pragma unroll
+      for (int j = 0; j < BJ; ++j) x[j][s] = __builtin_bit_cast(u32x4, ld128(at + kWBytes + uint32_t(j) * 2048));
+    }
+    if (i + ST < n) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot's operands are in registers
+      issue(i + ST, st);
+    }
+    const int kb = wave + KW * i;
+    if (kb == nkb - 1 && a.cols % 128) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const u32x4 m = tail_mask(a.cols, int64_t(kb) * 128, s, q);
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) x[j][s] &= m;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int e = 0; e < WI; ++e)
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) acc[e][j] = mfma_i8(w[e][s], x[j][s], acc[e][j]);
+    st = st + 1 == ST ? 0 : st + 1;
+  }
+  // partial tile idx = i BJ + j of wave w at (w WI BJ + idx) KB
+  __syncthreads();  // every wave is done with its ring
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int j = 0; j < BJ; ++j)
+      st128(uint32_t(((wave * WI + i) * BJ + j) * 1024 + 16 * lane), __builtin_bit_cast(uint4, acc[i][j]));
+  __syncthreads();
+  for (int idx = wave; idx < WI * BJ; idx += KW) {
+    i32x4 sum{0, 0, 0, 0};
+#pragma unroll
+    for (int v = 0; v < KW; ++v)
+      sum += __builtin_bit_cast(i32x4, ld128(uint32_t((v * WI * BJ + idx) * 1024 + 16 * lane)));
+    store_y4<YBF16>(a, b0 + 16 * (idx % BJ) + r, row0 + 16 * (idx / BJ) + 4 * q, sum);
+  }
+}
+
+// Large batches: both operands of a 128-byte block of k are staged for the
+// whole workgroup, in a ring of ST stages: BW weight rows and BB activation
+// rows, whose WGW x WGB waves each hold a BW / WGW by BB / WGB tile.
 template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16>
 __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
   constexpr int NW = WGW * WGB;
@@ -226,25 +388,22 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   const int64_t row0 = int64_t(in / deep) * BW, b0 = (int64_t(strip) * kDeep + in % deep) * BB;
   const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int lrow = lane / 8, lchunk = (lane % 8) ^ lrow;
-  const int8_t* Wt = a.W + row0 * a.ldw;
-  const int8_t* Xt = a.X + b0 * a.ldx;
-  const int wlast = int(std::min<int64_t>(BW, a.rows - row0)) - 1, blast = int(std::min<int64_t>(BB, a.batch - b0)) - 1;
-  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<int8_t*>(Wt), int16_t(0), int(int64_t(wlast) * a.ldw + a.cols), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<int8_t*>(Xt), int16_t(0), int(int64_t(blast) * a.ldx + a.cols), 0x00020000);
-  // staged row 8 (u NW + wave) + lrow of load u; rows past the last are the last one again
+  const Staged tw(a.W + row0 * a.ldw, a.rows - row0, a.cols, a.ldw, BW);
+  const Staged tx(a.X + b0 * a.ldx, a.batch - b0, a.cols, a.ldx, BB);
   uint32_t wvo[LW], xvo[LB];
 #pragma unroll
-  for (int u = 0; u < LW; ++u) wvo[u] = uint32_t(min(8 * (u * NW + wave) + lrow, wlast)) * uint32_t(a.ldw) + 16 * lchunk;
+  for (int u = 0; u < LW; ++u) wvo[u] = tw.row_offset(8 * (u * NW + wave) + lrow, a.ldw) + 16 * lchunk;
 #pragma unroll
-  for (int u = 0; u < LB; ++u) xvo[u] = uint32_t(min(8 * (u * NW + wave) + lrow, blast)) * uint32_t(a.ldx) + 16 * lchunk;
+  for (int u = 0; u < LB; ++u) xvo[u] = tx.row_offset(8 * (u * NW + wave) + lrow, a.ldx) + 16 * lchunk;
+  const int nkb = int((a.cols + 127) / 128);
+  const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % 128) / 16));
   auto issue = [&](int kb, int st) {
-    const uint32_t base = uint32_t(st) * kStage, k = uint32_t(kb) * 128;
+    const uint32_t base = uint32_t(__builtin_amdgcn_readfirstlane(st)) * kStage, k = uint32_t(__builtin_amdgcn_readfirstlane(kb)) * 128, back = kb == nkb - 1 ? over : 0;
 #pragma unroll
-    for (int u = 0; u < LW; ++u) stage_load(rw, wvo[u], k, base + uint32_t(u * NW + wave) * 1024);
+    for (int u = 0; u < LW; ++u) stage_load<false>(tw.rsrc, wvo[u] - back, k, base + uint32_t(u * NW + wave) * 1024);
 #pragma unroll
-    for (int u = 0; u < LB; ++u) stage_load(rx, xvo[u], k, base + kWBytes + uint32_t(u * NW + wave) * 1024);
+    for (int u = 0; u < LB; ++u)
+      stage_load<false>(tx.rsrc, xvo[u] - back, k, base + kWBytes + uint32_t(u * NW + wave) * 1024);
   };
   const int r = lane % 16, q = lane / 16;
   const int ww = wave / WGB, wb = wave % WGB;
@@ -254,13 +413,18 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   for (int i = 0; i < WI; ++i)
 #pragma unroll
     for (int j = 0; j < BJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  auto multiply = [&](uint32_t base) {
+  auto multiply = [&](uint32_t base, bool tail) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const uint32_t ch = uint32_t(((4 * s + q) ^ (r & 7)) * 16);
       u32x4 x[BJ];
 #pragma unroll
       for (int j = 0; j < BJ; ++j) x[j] = __builtin_bit_cast(u32x4, ld128(base + xrow + uint32_t(j) * 2048 + ch));
+      if (tail) {
+        const u32x4 m = tail_mask(a.cols, int64_t(nkb - 1) * 128, s, q);
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) x[j] &= m;
+      }
 #pragma unroll
       for (int i = 0; i < WI; ++i) {
         const u32x4 w = __builtin_bit_cast(u32x4, ld128(base + arow + uint32_t(i) * 2048 + ch));
@@ -269,35 +433,19 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
       }
     }
   };
-  const int nkb = int(a.cols / 128);
 #pragma unroll
   for (int i = 0; i < ST - 1; ++i)
     if (i < nkb) issue(i, i);
   int st = 0;
-  for (int kb = 0; kb < nkb; ++kb) {
-    // this wave's loads of block kb have landed once only the younger
-    // blocks' (ST - 2 of them) may be pending
-    if (kb + ST - 2 < nkb) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((ST - 2) * (LW + LB)) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    lds_barrier();  // every wave's loads of block kb have landed; block kb - 1 is no longer read
+  auto step = [&](int kb, bool tail) {
+    wait_ring<LW + LB, ST - 2>(nkb - 1 - kb);  // this wave's loads of block kb have landed
+    lds_barrier();                             // every wave's have; block kb - 1 is no longer read
     if (kb + ST - 1 < nkb) issue(kb + ST - 1, st == 0 ? ST - 1 : st - 1);
-    multiply(uint32_t(st) * kStage);
+    multiply(uint32_t(st) * kStage, tail);
     st = st + 1 == ST ? 0 : st + 1;
-  }
-  if (a.cols % 128) {
-    const int64_t k = int64_t(nkb) * 128 + 16 * lchunk;
-    lds_barrier();  // stage 0 may still be read
-#pragma unroll
-    for (int u = 0; u < LW; ++u)
-      st128(uint32_t(u * NW + wave) * 1024 + 16 * lane,
-            __builtin_bit_cast(uint4, load16_tail(Wt + int64_t(wvo[u]) - 16 * lchunk + k, a.cols - k)));
-#pragma unroll
-    for (int u = 0; u < LB; ++u)
-      st128(kWBytes + uint32_t(u * NW + wave) * 1024 + 16 * lane,
-            __builtin_bit_cast(uint4, load16_tail(Xt + int64_t(xvo[u]) - 16 * lchunk + k, a.cols - k)));
-    lds_barrier();
-    multiply(0);
-  }
+  };
+  for (int kb = 0; kb < nkb - 1; ++kb) step(kb, false);
+  step(nkb - 1, a.cols % 128 != 0);
 #pragma unroll
   for (int i = 0; i < WI; ++i)
 #pragma unroll
@@ -331,13 +479,73 @@ int run_stage(const I8Args& a, int yt, hipStream_t s) {
   return hip_check(hipGetLastError(), "i8_stage_kernel launch");
 }
 
-constexpr int kShapes = 11;       // 0 = heuristic
-constexpr int kDirectShapes = 5;  // 1..5; the others are staged
+template <int BW, int BB, int KW, int ST>
+int run_slice(const I8Args& a, int yt, hipStream_t s) {
+  const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
+  const int64_t grid = (nw + kXcds - 1) / kXcds * kXcds * nb;
+  if (grid * KW * kWave >= int64_t(1) << 32) return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
+  // weights that one workgroup reads once pass the caches by
+  auto kern = nb == 1 ? (yt == UW_BF16 ? i8_slice_kernel<BW, BB, KW, ST, true, true> : i8_slice_kernel<BW, BB, KW, ST, true, false>)
+                      : (yt == UW_BF16 ? i8_slice_kernel<BW, BB, KW, ST, false, true> : i8_slice_kernel<BW, BB, KW, ST, false, false>);
+  allow_full_lds(kern);
+  constexpr size_t kLds = std::max(size_t(KW) * ST * (BW + BB) * 128, size_t(KW) * BW * BB * 4);
+  static_assert(kLds <= kLdsLimit, "LDS");
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(KW * kWave), kLds, s, a, int(nw), int(nb));
+  return hip_check(hipGetLastError(), "i8_slice_kernel launch");
+}
+
+// Shapes: weight and batch rows of a workgroup's tile, and how its operands
+// reach the matrix cores: straight from global memory (any alignment), in
+// slices that each wave stages for itself, or staged for all waves.
+enum Kind { kDirect, kSlice, kStage };
+struct I8Shape {
+  int bw, bb;
+  Kind kind;
+};
+constexpr I8Shape kShapeList[] = {
+    {0, 0, kDirect},  // 0: the rule below
+    {16, 16, kDirect},  {16, 32, kDirect},  {32, 32, kDirect},
+    // the rule tries these from the end
+    {16, 16, kSlice},   {64, 16, kSlice},   {64, 16, kSlice},   {16, 32, kSlice},  {32, 32, kSlice}, {64, 32, kSlice},
+    {64, 64, kSlice},   {128, 64, kStage},  {128, 128, kStage}, {256, 128, kStage}, {256, 256, kStage},
+};
+constexpr int kShapes = int(sizeof(kShapeList) / sizeof(kShapeList[0]));
+constexpr int kFirstStaged = 4, kTall4 = 5, kTall8 = 6;  // 64 x 16 with 4 and with 8 waves
 
 bool stage_ok(const I8Args& a) {
   // 16-byte chunks, and 32-bit offsets inside a tile of 256 rows
   return reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldw % 16 == 0 &&
          a.ldx % 16 == 0 && a.ldw < (int64_t(1) << 22) && a.ldx < (int64_t(1) << 22);
+}
+
+// The shape of a product: the largest tile that still gives 160 workgroups
+// (of 256 compute units) and is not mostly padding, else the smallest.  Large
+// tiles read the operands fewer times; fewer workgroups leave compute units
+// idle.  From a sweep of every shape (8 rotated operand sets), us of the
+// shape taken / of the next smaller / of the next larger tile:
+//   1 x 14336 x 4096   64 x 16: 12.4 / 13.3 (32) / 13.4 (64 x 32)
+//   1 x 4096 x 14336   16 x 16: 11.2 / - / 13.5 (32)
+//   32 x 4096 x 14336  16 x 32: 16.4 / 20.2 / 20.9
+//   64 x 8192 x 8192   64 x 32: 20.4 / 22.9 / 25.6
+//   77 x 4096 x 4096   64 x 32:  8.8 /  9.0 / 12.3
+//   256 x 4096 x 4096  64 x 64: 12.9 / 16.8 / 21.8
+//   512 x 14336 x 4096 256 x 128: 48.3 / 68.8 / 83.5
+// Operands that are not 16-byte aligned run the direct shapes.
+void pick_shape(int64_t rows, int64_t batch, bool staged, int* shape) {
+  if (!staged) {
+    *shape = batch <= 16 ? 1 : batch <= 32 ? 2 : 3;
+    return;
+  }
+  for (int i = kShapes - 1; i > kFirstStaged; --i) {
+    const I8Shape& s = kShapeList[i];
+    const int64_t tiles = (rows + s.bw - 1) / s.bw * ((batch + s.bb - 1) / s.bb);
+    if ((s.bb > 16 && s.bb / 2 >= batch) || tiles < 160) continue;
+    // 64 x 16: one workgroup per compute unit takes 8 waves (12.4 us against 12.7 at 1 x 14336 x 4096), more take 4
+    // (22.3 against 24.2 at 16 x 28672 x 4096)
+    *shape = s.bb == 16 ? (tiles <= 256 ? kTall8 : kTall4) : i;
+    return;
+  }
+  *shape = kFirstStaged;
 }
 
 }  // namespace
@@ -350,7 +558,7 @@ bool i8_gemm_shape_ok(const int8_t* W, int64_t rows, int64_t ldw, const int8_t* 
   a.X = X;
   a.ldw = rows > 1 ? ldw : 0;
   a.ldx = batch > 1 ? ldx : 0;
-  return shape <= kDirectShapes || stage_ok(a);
+  return kShapeList[shape].kind == kDirect || stage_ok(a);
 }
 
 int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, const float* sw, const int8_t* X,
@@ -359,24 +567,22 @@ int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, con
   // a single row has no stride
   const I8Args a{W, sw, X, sx, bias, static_cast<char*>(Y), rows, cols, rows > 1 ? ldw : 0, batch, batch > 1 ? ldx : 0, ldy};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (shape <= 0) {
-    if (batch <= 16) shape = 1;
-    else if (batch <= 32) shape = 3;
-    else if (!stage_ok(a)) shape = 5;
-    else if (batch <= 64) shape = 6;
-    else shape = (rows + 255) / 256 * ((batch + 255) / 256) >= 256 ? 10 : (rows + 127) / 128 * ((batch + 127) / 128) >= 128 ? 8 : 6;
-  }
-  if (ks <= 0) ks = shape <= 3 ? 8 : 4;
+  if (shape <= 0) pick_shape(rows, batch, stage_ok(a), &shape);
+  if (ks <= 0) ks = 8;
   switch (shape) {
     case 1: return run_direct<1, 1>(a, yt, ks, s);
-    case 2: return run_direct<2, 1>(a, yt, ks, s);
-    case 3: return run_direct<1, 2>(a, yt, ks, s);
-    case 4: return run_direct<2, 2>(a, yt, ks, s);
-    case 5: return run_direct<2, 4>(a, yt, ks, s);
-    case 6: return run_stage<64, 64, 2, 2, 4>(a, yt, s);
-    case 7: return run_stage<128, 64, 4, 1, 4>(a, yt, s);
-    case 8: return run_stage<128, 128, 2, 2, 3>(a, yt, s);
-    case 9: return run_stage<256, 128, 4, 2, 3>(a, yt, s);
+    case 2: return run_direct<1, 2>(a, yt, ks, s);
+    case 3: return run_direct<2, 2>(a, yt, ks, s);
+    case 4: return run_slice<16, 16, 8, 2>(a, yt, s);
+    case 5: return run_slice<64, 16, 4, 2>(a, yt, s);
+    case 6: return run_slice<64, 16, 8, 2>(a, yt, s);
+    case 7: return run_slice<16, 32, 4, 4>(a, yt, s);
+    case 8: return run_slice<32, 32, 4, 2>(a, yt, s);
+    case 9: return run_slice<64, 32, 4, 2>(a, yt, s);
+    case 10: return run_slice<64, 64, 4, 2>(a, yt, s);
+    case 11: return run_stage<128, 64, 4, 1, 4>(a, yt, s);
+    case 12: return run_stage<128, 128, 2, 2, 3>(a, yt, s);
+    case 13: return run_stage<256, 128, 4, 2, 3>(a, yt, s);
     default: return run_stage<256, 256, 2, 4, 2>(a, yt, s);
   }
 }

@@ -59,19 +59,21 @@ __device__ __forceinline__ Raw8 load8(const char* row, int64_t i, int64_t n) {
     return v;
   }
   const int m = int(n - i);
+  uint32_t w[7];  // all loads before the first use
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if (e >= m) continue;
-    if (T == kF32) {
-      uint32_t w;
-      __builtin_memcpy(&w, p + 4 * e, 4);
-      if (e < 4) v.a[e] = w;
-      else v.b[e - 4] = w;
-    } else {
-      uint16_t w;
-      __builtin_memcpy(&w, p + 2 * e, 2);
-      v.a[e / 2] |= uint32_t(w) << (16 * (e & 1));
+  for (int e = 0; e < 7; ++e) w[e] = 0u;
+#pragma unroll
+  for (int e = 0; e < 7; ++e) {
+    if (e < m) {
+      if (T == kF32) __builtin_memcpy(&w[e], p + 4 * e, 4);
+      else __builtin_memcpy(&w[e], p + 2 * e, 2);
     }
+  }
+#pragma unroll
+  for (int e = 0; e < 7; ++e) {
+    if (T != kF32) v.a[e / 2] |= w[e] << (16 * (e & 1));
+    else if (e < 4) v.a[e] = w[e];
+    else v.b[e - 4] = w[e];
   }
   return v;
 }

@@ -143,9 +143,14 @@ def _check(rc: int, where: str) -> None:
         raise UwError(rc, where, (_lib.uw_last_error() or b"").decode())
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, dev: int | None = None) -> int | None:
+    """The HIP stream of a call; None is the current one (of device `dev`
+    where it is known: its raw handle then comes without a stream object,
+    0.1 us instead of 2.8)."""
     if stream is None:
         import torch
+        if dev is not None and _raw_stream is not None:
+            return _raw_stream(dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -569,21 +574,29 @@ def uw_sched_gemm(sched: int, slot: int, handle: int, X, Y, stream=None) -> None
 # These take no handle: the current device is the one the tensors have to be
 # on, and every shape is checked here, where the buffers' sizes are known.
 
+_raw_stream = None  # torch's accessor of a device's current stream, once a device is known
+
+
 def _op_device(t, name: str) -> int:
+    global _raw_stream
     import torch
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return dev
 
 
-def _op_rows(t, n: int, cols: int, dev: int, name: str) -> int:
-    """Checks an [n, cols] row-major operand; its row stride."""
-    if t.dim() != 2 or t.shape != (n, cols):
-        raise ValueError(f"{name} must have shape ({n}, {cols}), got {tuple(t.shape)}")
+def _op_rows(t, shape, dev: int, name: str) -> int:
+    """Checks a row-major operand of this (rows, cols); its row stride."""
+    if t.shape != shape or len(shape) != 2:
+        want = f"shape {tuple(shape)}" if len(shape) == 2 else "two dimensions"
+        raise ValueError(f"{name} must have {want}, got shape {tuple(t.shape)}")
     ld, inner = t.stride()
+    n, cols = shape
     if (inner != 1 and cols > 1) or (ld < cols and n > 1):
         raise ValueError(f"{name} must have a unit inner stride and rows that do not overlap")
     if t.get_device() != dev:
@@ -594,21 +607,21 @@ def _op_rows(t, n: int, cols: int, dev: int, name: str) -> int:
 def _op_scale(t, n: int, dev: int, name: str) -> int:
     """Checks a contiguous fp32 vector of n values; its address."""
     import torch
-    if t.dtype != torch.float32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.get_device() != dev:
+    if t.shape != (n,) or t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous float32 vector of {n} values on cuda:{dev}")
     return t.data_ptr()
 
 
 def _op_i8(t, name: str) -> None:
     import torch
-    if t.dtype != torch.int8:
+    if t.dtype is not torch.int8:
         raise TypeError(f"{name} must be int8, got {t.dtype}")
 
 
 def _op_out(Y, scale, n: int, dev: int):
     """The type code of a row operator's output, and its scales' address."""
     import torch
-    if Y.dtype != torch.int8:
+    if Y.dtype is not torch.int8:
         if scale is not None:
             raise ValueError("scale goes with an int8 output")
         return _dtype_code(Y), None
@@ -622,97 +635,90 @@ def uw_rmsnorm(X, gain, Y, scale=None, residual=None, residual_out=None, eps: fl
     float32, bfloat16, or int8 with `scale` (one float32 per row).
     residual_out receives h in the residual's dtype (the residual itself
     updates the stream in place); gain may be None (all ones)."""
-    dev = _op_device(X, "X")
-    if X.dim() != 2:
-        raise ValueError(f"X must be 2-D, got shape {tuple(X.shape)}")
-    n, cols = X.shape
-    ldx = _op_rows(X, n, cols, dev, "X")
-    ldy = _op_rows(Y, n, cols, dev, "Y")
+    dev, shape = _op_device(X, "X"), X.shape
+    ldx = _op_rows(X, shape, dev, "X")
+    n, cols = shape
+    ldy = _op_rows(Y, shape, dev, "Y")
     yt, sp = _op_out(Y, scale, n, dev)
     rp = hp = gp = None
     ldr = ldh = 0
     rt = gt = UW_F32
     if residual is not None:
-        ldr, rt, rp = _op_rows(residual, n, cols, dev, "residual"), _dtype_code(residual), residual.data_ptr()
+        ldr, rt, rp = _op_rows(residual, shape, dev, "residual"), _dtype_code(residual), residual.data_ptr()
     if residual_out is not None:
         if residual is None or residual_out.dtype != residual.dtype:
             raise ValueError("residual_out needs a residual of its dtype")
-        ldh, hp = _op_rows(residual_out, n, cols, dev, "residual_out"), residual_out.data_ptr()
+        ldh, hp = _op_rows(residual_out, shape, dev, "residual_out"), residual_out.data_ptr()
     if gain is not None:
-        _check_vector(gain, cols, dev, "gain")
+        if gain.shape != (cols,) or not gain.is_contiguous() or gain.get_device() != dev:
+            raise ValueError(f"gain must be a contiguous vector of {cols} elements on cuda:{dev}")
         gt, gp = _dtype_code(gain), gain.data_ptr()
     _check(_lib.uw_rmsnorm(X.data_ptr(), n, cols, ldx, _dtype_code(X), rp, ldr, rt, hp, ldh, gp, gt, eps, Y.data_ptr(),
-                           ldy, yt, sp, _stream(stream)), "uw_rmsnorm")
+                           ldy, yt, sp, _stream(stream, dev)), "uw_rmsnorm")
 
 
 def uw_silu_mul(G, U, Y, scale=None, stream=None) -> None:
     """Y = G / (1 + exp(-G)) * U per element (halves of one product's rows, for
     instance); Y and scale as for uw_rmsnorm."""
-    dev = _op_device(G, "G")
-    if G.dim() != 2:
-        raise ValueError(f"G must be 2-D, got shape {tuple(G.shape)}")
-    n, cols = G.shape
-    ldg = _op_rows(G, n, cols, dev, "G")
-    ldu = _op_rows(U, n, cols, dev, "U")
+    dev, shape = _op_device(G, "G"), G.shape
+    ldg = _op_rows(G, shape, dev, "G")
+    ldu = _op_rows(U, shape, dev, "U")
     if U.dtype != G.dtype:
         raise TypeError("G and U must have the same dtype")
-    ldy = _op_rows(Y, n, cols, dev, "Y")
+    n, cols = shape
+    ldy = _op_rows(Y, shape, dev, "Y")
     yt, sp = _op_out(Y, scale, n, dev)
     _check(_lib.uw_silu_mul(G.data_ptr(), ldg, U.data_ptr(), ldu, _dtype_code(G), n, cols, Y.data_ptr(), ldy, yt, sp,
-                            _stream(stream)), "uw_silu_mul")
+                            _stream(stream, dev)), "uw_silu_mul")
 
 
 def uw_i8_quantize(X, Q, scale, stream=None) -> None:
     """Rows of X (float32 or bfloat16) as int8 with one float32 scale each."""
-    dev = _op_device(X, "X")
-    if X.dim() != 2:
-        raise ValueError(f"X must be 2-D, got shape {tuple(X.shape)}")
-    n, cols = X.shape
-    ldx = _op_rows(X, n, cols, dev, "X")
+    dev, shape = _op_device(X, "X"), X.shape
+    ldx = _op_rows(X, shape, dev, "X")
     _op_i8(Q, "Q")
-    ldq = _op_rows(Q, n, cols, dev, "Q")
+    ldq = _op_rows(Q, shape, dev, "Q")
+    n, cols = shape
     _check(_lib.uw_i8_quantize(X.data_ptr(), n, cols, ldx, _dtype_code(X), Q.data_ptr(), ldq,
-                               _op_scale(scale, n, dev, "scale"), _stream(stream)), "uw_i8_quantize")
+                               _op_scale(scale, n, dev, "scale"), _stream(stream, dev)), "uw_i8_quantize")
 
 
 def uw_i8_dequantize(Q, scale, Y, stream=None) -> None:
     """Y = Q * scale per row, float32 or bfloat16."""
-    dev = _op_device(Q, "Q")
+    dev, shape = _op_device(Q, "Q"), Q.shape
     _op_i8(Q, "Q")
-    if Q.dim() != 2:
-        raise ValueError(f"Q must be 2-D, got shape {tuple(Q.shape)}")
-    n, cols = Q.shape
-    ldq = _op_rows(Q, n, cols, dev, "Q")
-    ldy = _op_rows(Y, n, cols, dev, "Y")
+    ldq = _op_rows(Q, shape, dev, "Q")
+    ldy = _op_rows(Y, shape, dev, "Y")
+    n, cols = shape
     _check(_lib.uw_i8_dequantize(Q.data_ptr(), n, cols, ldq, _op_scale(scale, n, dev, "scale"), Y.data_ptr(), ldy,
-                                 _dtype_code(Y), _stream(stream)), "uw_i8_dequantize")
+                                 _dtype_code(Y), _stream(stream, dev)), "uw_i8_dequantize")
 
 
-def _i8_operands(W, w_scale, X, x_scale, Y, bias):
-    dev = _op_device(W, "W")
+def _i8_operands(W, w_scale, X, x_scale, Y, bias, stream):
+    dev, shape = _op_device(W, "W"), W.shape
     _op_i8(W, "W")
     _op_i8(X, "X")
-    if W.dim() != 2 or X.dim() != 2:
-        raise ValueError("W and X must be 2-D")
-    (rows, cols), n = W.shape, X.shape[0]
-    ldw = _op_rows(W, rows, cols, dev, "W")
-    ldx = _op_rows(X, n, cols, dev, "X")
-    ldy = _op_rows(Y, n, rows, dev, "Y")
+    ldw = _op_rows(W, shape, dev, "W")
+    rows, cols = shape
+    n = x_scale.shape[0] if x_scale.dim() == 1 else -1
+    ldx = _op_rows(X, (n, cols), dev, "X")
+    ldy = _op_rows(Y, (n, rows), dev, "Y")
     return (W.data_ptr(), rows, cols, ldw, _op_scale(w_scale, rows, dev, "w_scale"), X.data_ptr(), n, ldx,
             _op_scale(x_scale, n, dev, "x_scale"), None if bias is None else _op_scale(bias, rows, dev, "bias"),
-            Y.data_ptr(), ldy, _dtype_code(Y))
+            Y.data_ptr(), ldy, _dtype_code(Y)), _stream(stream, dev)
 
 
 def uw_i8_gemm(W, w_scale, X, x_scale, Y, bias=None, stream=None) -> None:
     """Y[b, n] = x_scale[b] * w_scale[n] * sum_k X[b, k] W[n, k] (+ bias[n]),
     int8 W [rows, cols] and X [batch, cols], float32 scales and bias, Y
     float32 or bfloat16.  The sum is exact."""
-    _check(_lib.uw_i8_gemm(*_i8_operands(W, w_scale, X, x_scale, Y, bias), _stream(stream)), "uw_i8_gemm")
+    a, s = _i8_operands(W, w_scale, X, x_scale, Y, bias, stream)
+    _check(_lib.uw_i8_gemm(*a, s), "uw_i8_gemm")
 
 
 def uw_i8_gemm_shaped(W, w_scale, X, x_scale, Y, shape: int, ks: int = 0, bias=None, stream=None) -> None:
-    _check(_lib.uw_i8_gemm_shaped(*_i8_operands(W, w_scale, X, x_scale, Y, bias), shape, ks, _stream(stream)),
-           "uw_i8_gemm_shaped")
+    a, s = _i8_operands(W, w_scale, X, x_scale, Y, bias, stream)
+    _check(_lib.uw_i8_gemm_shaped(*a, shape, ks, s), "uw_i8_gemm_shaped")
 
 
 def uw_i8_gemm_shape_count() -> int:
@@ -733,7 +739,7 @@ class Int8Matrix:
 
     def __init__(self, q, scale):
         _op_i8(q, "q")
-        _op_rows(q, *q.shape, _op_device(q, "q"), "q")
+        _op_rows(q, q.shape, _op_device(q, "q"), "q")
         _op_scale(scale, q.shape[0], q.get_device(), "scale")
         self.q, self.scale = q, scale
         self.rows, self.cols = q.shape

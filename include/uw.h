@@ -652,8 +652,7 @@ int uw_i8_dequantize(const int8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq,
  *         nearest even), row stride ldy >= rows.
  *   1 <= cols <= 131071 (the sum stays inside 32 bits for every input).
  * Operands that are not 16-byte aligned, or whose strides are no multiples of
- * 16, run on shapes that read them straight from global memory: slower above
- * 32 rows.
+ * 16, run on shapes that read them straight from global memory: slower.
  * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (cols > 131071, more tiles than
  *         a launch holds), UW_ERR_HIP.
  */
@@ -664,8 +663,9 @@ int uw_i8_gemm(const int8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, const
 /*
  * uw_i8_gemm_shaped (device) - uw_i8_gemm with a given shape: shape in
  * [1, uw_i8_gemm_shape_count()) picks the weight and batch rows a workgroup
- * holds and whether the operands are staged in LDS, ks (1..8; 0 = auto) the
- * waves that split k in the shapes that are not.
+ * holds and how the operands reach the matrix cores: 1..3 straight from global
+ * memory (ks = the waves that split k, 1..8; 0 = 8), the others through LDS
+ * (ks does not apply).
  * Errors: as uw_i8_gemm; UW_ERR_INVALID for an unknown shape or ks,
  *         UW_ERR_UNSUPPORTED for a staged shape on operands that are not
  *         16-byte aligned with strides that are multiples of 16 (below 2^22).

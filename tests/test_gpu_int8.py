@@ -377,7 +377,7 @@ def test_gemm_shapes(b, rows, cols, shape):
 @pytest.mark.parametrize("ks", range(1, 9))
 @pytest.mark.parametrize("cols", [100, 256, 1500, 4096])
 def test_gemm_direct_waves(ks, cols):
-    for shape in (1, 2, 3, 4, 5):
+    for shape in (1, 2, 3):
         run_gemm(20, 48, cols, "f32", shape=shape, ks=ks)
 
 
