@@ -29,6 +29,14 @@ __device__ inline uint16_t f32_to_bf16(float f) {
   return uint16_t(u >> 16);
 }
 
+// fp32 pair -> bf16 pair, round to nearest even (v_cvt_pk_bf16_f32; a NaN stays a NaN).
+__device__ inline uint32_t pack_bf16(float lo, float hi) {
+  bf16x2_t v;
+  v[0] = static_cast<__bf16>(lo);
+  v[1] = static_cast<__bf16>(hi);
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 __device__ inline float dot2_bf16(uint32_t a, uint32_t b, float c) {
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, a), __builtin_bit_cast(bf16x2_t, b), c, false);
 }
@@ -89,6 +97,11 @@ __device__ inline uint4 ld128(uint32_t addr) {
 }
 __device__ inline void st128(uint32_t addr, uint4 v) {
   *reinterpret_cast<lds_quad*>(size_t(addr)) = u32x4{v.x, v.y, v.z, v.w};
+}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) u32x2 lds_pair;
+__device__ inline void st64(uint32_t addr, uint32_t lo, uint32_t hi) {
+  *reinterpret_cast<lds_pair*>(size_t(addr)) = u32x2{lo, hi};
 }
 __device__ inline void st16(uint32_t addr, uint32_t v) { *reinterpret_cast<lds_half*>(size_t(addr)) = uint16_t(v); }
 

@@ -60,30 +60,19 @@ __device__ __forceinline__ u32x4 load16_tail(const int8_t* p, int64_t left) {
   return v;
 }
 
-// Four consecutive values of row b of Y, weight rows n .. n + 3.
+// Four consecutive values of row b of Y, weight rows n .. n + 3 (n < rows).
 template <bool YBF16>
-__device__ __forceinline__ void store_y4(const I8Args& a, int64_t b, int64_t n, const i32x4& acc) {
-  if (b >= a.batch || n >= a.rows) return;
-  const float sx = a.sx[b];
+__device__ __forceinline__ void store_row4(const I8Args& a, int64_t b, int64_t n, const float (&v)[4]) {
   const int m = int(std::min<int64_t>(4, a.rows - n));
-  float v[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (e >= m) continue;
-    v[e] = float(acc[e]) * (sx * a.sw[n + e]);
-    if (a.bias) v[e] += a.bias[n + e];
-  }
   if (YBF16) {
     uint16_t* y = reinterpret_cast<uint16_t*>(a.Y) + b * a.ldy + n;
-    uint16_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = e < m ? f32_to_bf16(v[e]) : 0;
+    const uint32_t w[2] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     if (m == 4) {
       __builtin_memcpy(y, w, 8);
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        if (e < m) y[e] = w[e];
+        if (e < m) y[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
     }
   } else {
     float* y = reinterpret_cast<float*>(a.Y) + b * a.ldy + n;
@@ -94,6 +83,135 @@ __device__ __forceinline__ void store_y4(const I8Args& a, int64_t b, int64_t n, 
       for (int e = 0; e < 3; ++e)
         if (e < m) y[e] = v[e];
     }
+  }
+}
+
+// Values n .. n + 3 of a vector of `rows`; past the end, its last one.
+__device__ __forceinline__ void load_row4(const float* p, int64_t n, int64_t rows, float (&v)[4]) {
+  if (n + 4 <= rows) {
+    __builtin_memcpy(v, p + n, 16);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = p[std::min<int64_t>(n + e, rows - 1)];
+}
+
+// 16 bytes of row b of Y from column n on: 16 / SIZE values.
+template <int SIZE>
+__device__ __forceinline__ void store_row16(const I8Args& a, int64_t b, int64_t n, const uint4& v) {
+  if (b >= a.batch || n >= a.rows) return;
+  char* y = a.Y + (b * a.ldy + n) * SIZE;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int m = int(std::min<int64_t>(16 / SIZE, a.rows - n));
+  if (m == 16 / SIZE) {
+    __builtin_memcpy(y, w, 16);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 16 / SIZE - 1; ++e) {
+    if (e >= m) continue;
+    if (SIZE == 4) {
+      __builtin_memcpy(y + 4 * e, &w[e], 4);
+    } else {
+      const uint16_t h = uint16_t(w[e / 2] >> (16 * (e & 1)));
+      __builtin_memcpy(y + 2 * e, &h, 2);
+    }
+  }
+}
+
+// The same from the integer sums of one 16 x 16 tile.
+template <bool YBF16>
+__device__ __forceinline__ void store_y4(const I8Args& a, int64_t b, int64_t n, const i32x4& acc) {
+  if (b >= a.batch || n >= a.rows) return;
+  const float sx = a.sx[b];
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t at = std::min<int64_t>(n + e, a.rows - 1);
+    v[e] = float(acc[e]) * (sx * a.sw[at]);
+    if (a.bias) v[e] += a.bias[at];
+  }
+  store_row4<YBF16>(a, b, n, v);
+}
+
+// Epilogue of a wave's WI x BJ tiles at (row0, b0): the scales are read before
+// the first store.
+template <int WI, int BJ, bool YBF16>
+__device__ __forceinline__ void store_tiles(const I8Args& a, int64_t row0, int64_t b0, int r, int q,
+                                            const i32x4 (&acc)[WI][BJ]) {
+  float sx[BJ];
+#pragma unroll
+  for (int j = 0; j < BJ; ++j) sx[j] = a.sx[std::min<int64_t>(b0 + 16 * j + r, a.batch - 1)];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) {
+    const int64_t n = row0 + 16 * i + 4 * q;
+    float sw[4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t at = std::min<int64_t>(n + e, a.rows - 1);
+      sw[e] = a.sw[at];
+      bias[e] = a.bias ? a.bias[at] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) {
+      const int64_t b = b0 + 16 * j + r;
+      if (b >= a.batch || n >= a.rows) continue;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = float(acc[i][j][e]) * (sx[j] * sw[e]);
+        if (a.bias) v[e] += bias[e];
+      }
+      store_row4<YBF16>(a, b, n, v);
+    }
+  }
+}
+
+// Epilogue of a wave's WI x BJ tiles at (n0, bw0), through LDS: 16 activation
+// rows at a time as the wave's 16 WI columns, so that rows go out in runs of
+// 32 WI bytes (bf16) or twice that (without it, 4096 x 4096 x 64 took 19.1 us,
+// with it 13.4); 16 bytes of padding a row spread the writes over the banks.
+// The scales are read before anything is stored.  LDS: bytes a wave has.
+template <int WI, int BJ, bool YBF16, int LDS>
+__device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, int64_t bw0, int wave, int lane,
+                                                  const i32x4 (&acc)[WI][BJ]) {
+  constexpr int kCols = 16 * WI, kSize = YBF16 ? 2 : 4, kPitch = kCols * kSize + 16;
+  static_assert(16 * kPitch <= LDS, "LDS");
+  const int r = lane % 16, q = lane / 16;
+  float sx[BJ], sw[WI][4], bias[WI][4];
+#pragma unroll
+  for (int j = 0; j < BJ; ++j) sx[j] = a.sx[std::min<int64_t>(bw0 + 16 * j + r, a.batch - 1)];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) {
+    load_row4(a.sw, n0 + 16 * i + 4 * q, a.rows, sw[i]);
+    if (a.bias) load_row4(a.bias, n0 + 16 * i + 4 * q, a.rows, bias[i]);
+  }
+  __syncthreads();  // no wave reads the ring any more
+  const uint32_t out = uint32_t(wave) * (16 * kPitch);
+#pragma unroll
+  for (int j = 0; j < BJ; ++j) {
+#pragma unroll
+    for (int i = 0; i < WI; ++i) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = float(acc[i][j][e]) * (sx[j] * sw[i][e]);
+        if (a.bias) v[e] += bias[i][e];
+      }
+      const uint32_t dst = out + uint32_t(r) * kPitch + uint32_t(16 * i + 4 * q) * kSize;
+      if (YBF16) st64(dst, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      else st128(dst, uint4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])});
+    }
+    wave_lds_fence();
+    constexpr int kPer = 16 / kSize, kLanes = kCols / kPer;  // values a lane stores; lanes of a row
+    constexpr int kChunks = 16 * kLanes;                     // of the 16 rows
+#pragma unroll
+    for (int c0 = 0; c0 < kChunks; c0 += kWave) {
+      const int at = c0 + lane, br = at / kLanes, c = at % kLanes * kPer;
+      if (kChunks % kWave == 0 || at < kChunks)
+        store_row16<kSize>(a, bw0 + 16 * j + br, n0 + c, ld128(out + uint32_t(br) * kPitch + uint32_t(c) * kSize));
+    }
+    wave_lds_fence();
   }
 }
 
@@ -171,10 +289,7 @@ __global__ __launch_bounds__(512) void i8_direct_kernel(I8Args a, int n_groups, 
     mul(wc, xc);
   }
   if (KS == 1) {
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int t = 0; t < TB; ++t) store_y4<YBF16>(a, b0 + 16 * t + r, row0 + 16 * i + 4 * q, acc[i][t]);
+    store_tiles<RB, TB, YBF16>(a, row0, b0, r, q, acc);
     return;
   }
   // partial tile (i, t) of wave w at ((w * RB + i) * TB + t) KB
@@ -204,7 +319,7 @@ __device__ __forceinline__ void stage_load(__amdgpu_buffer_rsrc_t r, uint32_t vo
         "s_nop 0\n"
         "buffer_load_dwordx4 %[v], %[r], %[s] offen nt lds"
         :
-        : [m] "s"(m0), [v] "v"(voff), [r] "s"(r), [s] "s"(soff)
+        : [m] "s"(__builtin_amdgcn_readfirstlane(m0)), [v] "v"(voff), [r] "s"(r), [s] "s"(__builtin_amdgcn_readfirstlane(soff))
         : "memory");
   } else {
     asm volatile(
@@ -213,7 +328,7 @@ __device__ __forceinline__ void stage_load(__amdgpu_buffer_rsrc_t r, uint32_t vo
         "s_nop 0\n"
         "buffer_load_dwordx4 %[v], %[r], %[s] offen lds"
         :
-        : [m] "s"(m0), [v] "v"(voff), [r] "s"(r), [s] "s"(soff)
+        : [m] "s"(__builtin_amdgcn_readfirstlane(m0)), [v] "v"(voff), [r] "s"(r), [s] "s"(__builtin_amdgcn_readfirstlane(soff))
         : "memory");
   }
 }
@@ -235,9 +350,12 @@ struct Staged {
   int last;  // the tile's last row; the rows past it are that row again
 
   __device__ __forceinline__ Staged(const int8_t* tile, int64_t rows, int64_t cols, int64_t ld, int tile_rows)
-      : last(int(std::min<int64_t>(tile_rows, rows)) - 1) {
-    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(tile), int16_t(0),
-                                             int(int64_t(last) * ld + (cols + 3) / 4 * 4), 0x00020000);
+      : last(__builtin_amdgcn_readfirstlane(int(std::min<int64_t>(tile_rows, rows)) - 1)) {
+    // the same in every lane; readfirstlane keeps it in scalar registers
+    const uint64_t p = reinterpret_cast<uint64_t>(tile);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(p)), hi = __builtin_amdgcn_readfirstlane(uint32_t(p >> 32));
+    const int bytes = __builtin_amdgcn_readfirstlane(int(int64_t(last) * ld + (cols + 3) / 4 * 4));
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uint64_t(hi) << 32 | lo), int16_t(0), bytes, 0x00020000);
   }
   // byte offset of staged row `row` (of the lane) at k = 0
   __device__ __forceinline__ uint32_t row_offset(int row, int64_t ld) const {
@@ -245,9 +363,8 @@ struct Staged {
   }
 };
 
-// Masks of the 16 bytes that lane (r, q) reads at step s of the block at k.
-__device__ __forceinline__ u32x4 tail_mask(int64_t cols, int64_t k, int s, int q) {
-  const int left = int(std::min<int64_t>(cols - k, 128)) - 16 * (4 * s + q);
+// Mask of 16 bytes of which the first `left` lie inside their row.
+__device__ __forceinline__ u32x4 tail_mask(int left) {
   u32x4 m;
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
@@ -301,7 +418,7 @@ __global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tile
   const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % 128) / 16));
   auto issue = [&](int i, int st) {
     const int kb = wave + KW * i;
-    const uint32_t base = ring + uint32_t(st) * kSlot, k = uint32_t(__builtin_amdgcn_readfirstlane(kb)) * 128, back = kb == nkb - 1 ? over : 0;
+    const uint32_t base = ring + uint32_t(st) * kSlot, k = uint32_t(kb) * 128, back = kb == nkb - 1 ? over : 0;
 #pragma unroll
     for (int u = 0; u < LW; ++u) stage_load<NT>(tw.rsrc, wvo[u] - back, k, base + u * 1024);
 #pragma unroll
@@ -337,7 +454,7 @@ __global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tile
     if (kb == nkb - 1 && a.cols % 128) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const u32x4 m = tail_mask(a.cols, int64_t(kb) * 128, s, q);
+        const u32x4 m = tail_mask(int(a.cols - int64_t(kb) * 128) - 16 * (4 * s + q));
 #pragma unroll
         for (int j = 0; j < BJ; ++j) x[j][s] &= m;
       }
@@ -367,16 +484,18 @@ __global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tile
   }
 }
 
-// Large batches: both operands of a 128-byte block of k are staged for the
+// Large batches: both operands of a BK-byte block of k are staged for the
 // whole workgroup, in a ring of ST stages: BW weight rows and BB activation
 // rows, whose WGW x WGB waves each hold a BW / WGW by BB / WGB tile.
-template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16>
+template <int BW, int BB, int WGW, int WGB, int BK, int ST, bool YBF16>
 __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
   constexpr int NW = WGW * WGB;
   constexpr int WI = BW / WGW / 16, BJ = BB / WGB / 16;
-  constexpr int LW = BW / 8 / NW, LB = BB / 8 / NW;  // 1 KB loads per wave and stage
-  constexpr uint32_t kWBytes = BW * 128, kStage = (BW + BB) * 128;
-  static_assert(BW % (8 * NW) == 0 && BB % (8 * NW) == 0, "whole loads");
+  constexpr int LR = 1024 / BK;                      // rows of a 1 KB load
+  constexpr int LW = BW / LR / NW, LB = BB / LR / NW;  // loads per wave and stage
+  constexpr uint32_t kWBytes = BW * BK, kStage = (BW + BB) * BK;
+  static_assert(BW % (LR * NW) == 0 && BB % (LR * NW) == 0, "whole loads");
+  static_assert(BK == 64 || BK == 128, "bank spread");
   // workgroups are dealt to the XCDs round-robin: each XCD takes a run of
   // tiles, 4 activation tiles deep, so that its L2 serves the rereads
   const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
@@ -387,18 +506,19 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   const int in = id - strip * kDeep * nw_tiles;
   const int64_t row0 = int64_t(in / deep) * BW, b0 = (int64_t(strip) * kDeep + in % deep) * BB;
   const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
-  const int lrow = lane / 8, lchunk = (lane % 8) ^ lrow;
+  // chunk c of row r lies at c ^ (r % 8) of rows of 8 chunks, c ^ (r / 2 % 4) of 4
+  const int lrow = lane / (BK / 16), lchunk = (lane % (BK / 16)) ^ (BK == 128 ? lrow & 7 : (lrow >> 1) & 3);
   const Staged tw(a.W + row0 * a.ldw, a.rows - row0, a.cols, a.ldw, BW);
   const Staged tx(a.X + b0 * a.ldx, a.batch - b0, a.cols, a.ldx, BB);
   uint32_t wvo[LW], xvo[LB];
 #pragma unroll
-  for (int u = 0; u < LW; ++u) wvo[u] = tw.row_offset(8 * (u * NW + wave) + lrow, a.ldw) + 16 * lchunk;
+  for (int u = 0; u < LW; ++u) wvo[u] = tw.row_offset(LR * (u * NW + wave) + lrow, a.ldw) + 16 * lchunk;
 #pragma unroll
-  for (int u = 0; u < LB; ++u) xvo[u] = tx.row_offset(8 * (u * NW + wave) + lrow, a.ldx) + 16 * lchunk;
-  const int nkb = int((a.cols + 127) / 128);
-  const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % 128) / 16));
+  for (int u = 0; u < LB; ++u) xvo[u] = tx.row_offset(LR * (u * NW + wave) + lrow, a.ldx) + 16 * lchunk;
+  const int nkb = int((a.cols + BK - 1) / BK);
+  const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % BK) / 16));
   auto issue = [&](int kb, int st) {
-    const uint32_t base = uint32_t(__builtin_amdgcn_readfirstlane(st)) * kStage, k = uint32_t(__builtin_amdgcn_readfirstlane(kb)) * 128, back = kb == nkb - 1 ? over : 0;
+    const uint32_t base = uint32_t(st) * kStage, k = uint32_t(kb) * BK, back = kb == nkb - 1 ? over : 0;
 #pragma unroll
     for (int u = 0; u < LW; ++u) stage_load<false>(tw.rsrc, wvo[u] - back, k, base + uint32_t(u * NW + wave) * 1024);
 #pragma unroll
@@ -407,7 +527,7 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   };
   const int r = lane % 16, q = lane / 16;
   const int ww = wave / WGB, wb = wave % WGB;
-  const uint32_t arow = uint32_t(ww * WI * 16 + r) * 128, xrow = kWBytes + uint32_t(wb * BJ * 16 + r) * 128;
+  const uint32_t arow = uint32_t(ww * WI * 16 + r) * BK, xrow = kWBytes + uint32_t(wb * BJ * 16 + r) * BK;
   i32x4 acc[WI][BJ];
 #pragma unroll
   for (int i = 0; i < WI; ++i)
@@ -415,19 +535,19 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
     for (int j = 0; j < BJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
   auto multiply = [&](uint32_t base, bool tail) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const uint32_t ch = uint32_t(((4 * s + q) ^ (r & 7)) * 16);
+    for (int s = 0; s < BK / 64; ++s) {
+      const uint32_t ch = uint32_t(((4 * s + q) ^ (BK == 128 ? r & 7 : (r >> 1) & 3)) * 16);
       u32x4 x[BJ];
 #pragma unroll
-      for (int j = 0; j < BJ; ++j) x[j] = __builtin_bit_cast(u32x4, ld128(base + xrow + uint32_t(j) * 2048 + ch));
+      for (int j = 0; j < BJ; ++j) x[j] = __builtin_bit_cast(u32x4, ld128(base + xrow + uint32_t(j) * (16 * BK) + ch));
       if (tail) {
-        const u32x4 m = tail_mask(a.cols, int64_t(nkb - 1) * 128, s, q);
+        const u32x4 m = tail_mask(int(a.cols - int64_t(nkb - 1) * BK) - 16 * (4 * s + q));
 #pragma unroll
         for (int j = 0; j < BJ; ++j) x[j] &= m;
       }
 #pragma unroll
       for (int i = 0; i < WI; ++i) {
-        const u32x4 w = __builtin_bit_cast(u32x4, ld128(base + arow + uint32_t(i) * 2048 + ch));
+        const u32x4 w = __builtin_bit_cast(u32x4, ld128(base + arow + uint32_t(i) * (16 * BK) + ch));
 #pragma unroll
         for (int j = 0; j < BJ; ++j) acc[i][j] = mfma_i8(w, x[j], acc[i][j]);
       }
@@ -445,12 +565,123 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
     st = st + 1 == ST ? 0 : st + 1;
   };
   for (int kb = 0; kb < nkb - 1; ++kb) step(kb, false);
-  step(nkb - 1, a.cols % 128 != 0);
+  step(nkb - 1, a.cols % BK != 0);
+  store_through_lds<WI, BJ, YBF16, int(ST * kStage) / NW>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16, wave, lane, acc);
+}
+
+// The largest batches.  As above with the operands of the next step read
+// between this step's products: WGW x WGB waves (two per SIMD: one alone
+// issues the 16 x 16 products at 0.85 of the rate), steps of 64 bytes of k, one
+// barrier per step; the slot a step's operands came from is refilled while
+// its products run, so ST steps are in flight.
+// Bound by power: with operands of zeros 4096 x 4096 x 16384 runs in 153 us
+// (3.6 POP/s, 4.0 inside the loop), with random ones in 202 us (2.7 POP/s),
+// the clock falling from 2.3 to about 1.8 GHz; products alone, operands held
+// in registers, reach 3.4 POP/s on random values.  32 x 32 products (twice the
+// accumulator traffic per operation) took 265 us there, four waves with the
+// 16 x 16 form 241 us, the kernel above at 256 x 256 219 us.
+template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16>
+__global__ __launch_bounds__(64 * WGW * WGB) void i8_wide_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
+  constexpr int NW = WGW * WGB;
+  constexpr int WI = BW / WGW / 16, BJ = BB / WGB / 16;  // 16 x 16 tiles of a wave
+  constexpr int NLW = BW / 16, NLB = BB / 16;            // 1 KB loads of a step
+  constexpr int LW = (NLW + NW - 1) / NW, LB = (NLB + NW - 1) / NW, L = LW + LB;  // per wave
+  constexpr int G = WI + BJ, M = WI * BJ;                // operand reads and products per step
+  constexpr uint32_t kWBytes = BW * 64, kStep = (BW + BB) * 64;
+  static_assert(ST * kStep <= kLdsLimit && ST >= 3 && M >= 2 * G && M >= 4 * L, "ring");
+  const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
+  if (id >= nw_tiles * nb_tiles) return;  // whole workgroups
+  constexpr int kDeep = 4;
+  const int strip = id / (kDeep * nw_tiles);
+  const int deep = min(kDeep, nb_tiles - strip * kDeep);
+  const int in = id - strip * kDeep * nw_tiles;
+  const int64_t row0 = int64_t(in / deep) * BW, b0 = (int64_t(strip) * kDeep + in % deep) * BB;
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int lrow = lane / 4, lchunk = (lane % 4) ^ ((lrow >> 1) & 3);
+  const Staged tw(a.W + row0 * a.ldw, a.rows - row0, a.cols, a.ldw, BW);
+  const Staged tx(a.X + b0 * a.ldx, a.batch - b0, a.cols, a.ldx, BB);
+  // load u of this wave; a tile whose loads the waves do not share evenly has
+  // its last one made twice (the same bytes to the same place)
+  uint32_t vo[L], dst[L];
+#pragma unroll
+  for (int u = 0; u < LW; ++u) {
+    const int l = min(u * NW + wave, NLW - 1);
+    vo[u] = tw.row_offset(16 * l + lrow, a.ldw) + 16 * lchunk;
+    dst[u] = uint32_t(l) * 1024;
+  }
+#pragma unroll
+  for (int u = 0; u < LB; ++u) {
+    const int l = min(u * NW + wave, NLB - 1);
+    vo[LW + u] = tx.row_offset(16 * l + lrow, a.ldx) + 16 * lchunk;
+    dst[LW + u] = kWBytes + uint32_t(l) * 1024;
+  }
+  const int n = int((a.cols + 63) / 64);
+  const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % 64) / 16));
+  auto issue = [&](int u, int t, int slot, bool last) {
+    stage_load<false>(u < LW ? tw.rsrc : tx.rsrc, vo[u] - (last ? over : 0), uint32_t(t) * 64, uint32_t(slot) * kStep + dst[u]);
+  };
+  const int r = lane % 16, q = lane / 16;
+  const int ww = wave / WGB, wb = wave % WGB;
+  const uint32_t chunk = uint32_t((q ^ ((r >> 1) & 3)) * 16);
+  const uint32_t arow = uint32_t(ww * WI * 16 + r) * 64 + chunk, xrow = kWBytes + uint32_t(wb * BJ * 16 + r) * 64 + chunk;
+  i32x4 acc[WI][BJ];
 #pragma unroll
   for (int i = 0; i < WI; ++i)
 #pragma unroll
-    for (int j = 0; j < BJ; ++j)
-      store_y4<YBF16>(a, b0 + (wb * BJ + j) * 16 + r, row0 + (ww * WI + i) * 16 + 4 * q, acc[i][j]);
+    for (int j = 0; j < BJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  u32x4 f0[G], f1[G];  // a step's operands: BJ of the activations, WI of the weights
+  auto read = [&](int g, int slot, u32x4 (&f)[G]) {
+    const uint32_t base = uint32_t(slot) * kStep;
+    f[g] = __builtin_bit_cast(u32x4, ld128(g < BJ ? base + xrow + uint32_t(g) * 1024 : base + arow + uint32_t(g - BJ) * 1024));
+  };
+#pragma unroll
+  for (int t = 0; t < ST; ++t)
+    if (t < n) {
+#pragma unroll
+      for (int u = 0; u < L; ++u) issue(u, t, t, t == n - 1);
+    }
+  wait_ring<L, ST - 1>(n - 1);
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int g = 0; g < G; ++g) read(g, 0, f0);
+  int slot = 0;
+  auto step = [&](int t, const u32x4 (&fc)[G], u32x4 (&fn)[G], bool steady) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): fc is in registers
+    const bool more = steady || t + 1 < n, refill = steady || t + ST < n;
+    if (more) {
+      wait_ring<L, ST - 2>(steady ? ST - 2 : n - 2 - t);  // this wave's loads of step t + 1 have landed
+      asm volatile("s_barrier" ::: "memory");             // every wave's have, and every wave holds step t
+    }
+    const int next = slot + 1 == ST ? 0 : slot + 1;
+#pragma unroll
+    for (int g = 0; g < M; ++g) {
+      if (more && g % 2 == 0 && g / 2 < G) read(g / 2, next, fn);
+      if (refill && g % 4 == 1 && g / 4 < L) issue(g / 4, t + ST, slot, !steady && t + ST == n - 1);
+      const int i = g / BJ, j = g % BJ;
+      acc[i][j] = mfma_i8(fc[BJ + i], fc[j], acc[i][j]);
+      if (g % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    slot = next;
+  };
+  int t = 0;
+  for (; t + ST + 2 < n; t += 2) {
+    step(t, f0, f1, true);
+    step(t + 1, f1, f0, true);
+  }
+  auto mask = [&](int t, u32x4 (&f)[G]) {
+    if (t != n - 1 || a.cols % 64 == 0) return;
+    const u32x4 m = tail_mask(int(a.cols - int64_t(t) * 64) - 16 * q);
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) f[j] &= m;
+  };
+  for (; t < n; t += 2) {
+    mask(t, f0);
+    step(t, f0, f1, false);
+    if (t + 1 >= n) break;
+    mask(t + 1, f1);
+    step(t + 1, f1, f0, false);
+  }
+  store_through_lds<WI, BJ, YBF16, int(ST * kStep) / NW>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16, wave, lane, acc);
 }
 
 template <int RB, int TB>
@@ -465,16 +696,16 @@ int run_direct(const I8Args& a, int yt, int ks, hipStream_t s) {
   return hip_check(hipGetLastError(), "i8_direct_kernel launch");
 }
 
-template <int BW, int BB, int WGW, int WGB, int ST>
+template <int BW, int BB, int WGW, int WGB, int BK, int ST>
 int run_stage(const I8Args& a, int yt, hipStream_t s) {
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
   const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   constexpr int kThreads = 64 * WGW * WGB;
   if (per_xcd * kXcds * kThreads >= int64_t(1) << 32)
     return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
-  auto kern = yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, true> : i8_stage_kernel<BW, BB, WGW, WGB, ST, false>;
+  auto kern = yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, BK, ST, true> : i8_stage_kernel<BW, BB, WGW, WGB, BK, ST, false>;
   allow_full_lds(kern);
-  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * 128, s, a, int(nw),
+  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * BK, s, a, int(nw),
                      int(nb), int(per_xcd));
   return hip_check(hipGetLastError(), "i8_stage_kernel launch");
 }
@@ -494,6 +725,19 @@ int run_slice(const I8Args& a, int yt, hipStream_t s) {
   return hip_check(hipGetLastError(), "i8_slice_kernel launch");
 }
 
+template <int BW, int BB, int WGW, int WGB, int ST>
+int run_wide(const I8Args& a, int yt, hipStream_t s) {
+  const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
+  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
+  constexpr int kThreads = 64 * WGW * WGB;
+  if (per_xcd * kXcds * kThreads >= int64_t(1) << 32) return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
+  auto kern = yt == UW_BF16 ? i8_wide_kernel<BW, BB, WGW, WGB, ST, true> : i8_wide_kernel<BW, BB, WGW, WGB, ST, false>;
+  allow_full_lds(kern);
+  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * 64, s, a, int(nw),
+                     int(nb), int(per_xcd));
+  return hip_check(hipGetLastError(), "i8_wide_kernel launch");
+}
+
 // Shapes: weight and batch rows of a workgroup's tile, and how its operands
 // reach the matrix cores: straight from global memory (any alignment), in
 // slices that each wave stages for itself, or staged for all waves.
@@ -507,10 +751,12 @@ constexpr I8Shape kShapeList[] = {
     {16, 16, kDirect},  {16, 32, kDirect},  {32, 32, kDirect},
     // the rule tries these from the end
     {16, 16, kSlice},   {64, 16, kSlice},   {64, 16, kSlice},   {16, 32, kSlice},  {32, 32, kSlice}, {64, 32, kSlice},
-    {64, 64, kSlice},   {128, 64, kStage},  {128, 128, kStage}, {256, 128, kStage}, {256, 256, kStage},
+    {64, 64, kSlice},   {128, 64, kStage},  {128, 128, kStage}, {256, 128, kStage}, {224, 256, kStage}, {256, 256, kStage},
 };
 constexpr int kShapes = int(sizeof(kShapeList) / sizeof(kShapeList[0]));
 constexpr int kFirstStaged = 4, kTall4 = 5, kTall8 = 6;  // 64 x 16 with 4 and with 8 waves
+constexpr int kWide224 = 14, kWide256 = 15;
+constexpr int kCus = 256;
 
 bool stage_ok(const I8Args& a) {
   // 16-byte chunks, and 32-bit offsets inside a tile of 256 rows
@@ -529,7 +775,12 @@ bool stage_ok(const I8Args& a) {
 //   64 x 8192 x 8192   64 x 32: 20.4 / 22.9 / 25.6
 //   77 x 4096 x 4096   64 x 32:  8.8 /  9.0 / 12.3
 //   256 x 4096 x 4096  64 x 64: 12.9 / 16.8 / 21.8
-//   512 x 14336 x 4096 256 x 128: 48.3 / 68.8 / 83.5
+//   256 x 14336 x 4096 128 x 128: 28.0 / 36.8 / 37.5
+//   512 x 14336 x 4096 256 x 128: 39.5 / 52.0 / 55.1
+//   1024 x 14336 x 4096 256 x 256: 58.4 / 73.3 / -
+// At 256 activation rows the tile has 224 weight rows instead of 256 where
+// that wastes less of the last round of workgroups (4096 x 14336 x 4096: 4
+// rounds either way, 223 us against 235).
 // Operands that are not 16-byte aligned run the direct shapes.
 void pick_shape(int64_t rows, int64_t batch, bool staged, int* shape) {
   if (!staged) {
@@ -537,12 +788,17 @@ void pick_shape(int64_t rows, int64_t batch, bool staged, int* shape) {
     return;
   }
   for (int i = kShapes - 1; i > kFirstStaged; --i) {
+    if (i == kWide224) continue;
     const I8Shape& s = kShapeList[i];
     const int64_t tiles = (rows + s.bw - 1) / s.bw * ((batch + s.bb - 1) / s.bb);
     if ((s.bb > 16 && s.bb / 2 >= batch) || tiles < 160) continue;
     // 64 x 16: one workgroup per compute unit takes 8 waves (12.4 us against 12.7 at 1 x 14336 x 4096), more take 4
     // (22.3 against 24.2 at 16 x 28672 x 4096)
-    *shape = s.bb == 16 ? (tiles <= 256 ? kTall8 : kTall4) : i;
+    *shape = s.bb == 16 ? (tiles <= kCus ? kTall8 : kTall4) : i;
+    if (i == kWide256) {
+      const int64_t t224 = (rows + 223) / 224 * ((batch + 255) / 256);
+      if ((t224 + kCus - 1) / kCus * 224 < (tiles + kCus - 1) / kCus * 256) *shape = kWide224;
+    }
     return;
   }
   *shape = kFirstStaged;
@@ -580,10 +836,11 @@ int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, con
     case 8: return run_slice<32, 32, 4, 2>(a, yt, s);
     case 9: return run_slice<64, 32, 4, 2>(a, yt, s);
     case 10: return run_slice<64, 64, 4, 2>(a, yt, s);
-    case 11: return run_stage<128, 64, 4, 1, 4>(a, yt, s);
-    case 12: return run_stage<128, 128, 2, 2, 3>(a, yt, s);
-    case 13: return run_stage<256, 128, 4, 2, 3>(a, yt, s);
-    default: return run_stage<256, 256, 2, 4, 2>(a, yt, s);
+    case 11: return run_stage<128, 64, 4, 1, 128, 4>(a, yt, s);
+    case 12: return run_stage<128, 128, 2, 2, 128, 3>(a, yt, s);
+    case 13: return run_stage<256, 128, 4, 2, 128, 3>(a, yt, s);
+    case 14: return run_wide<224, 256, 2, 4, 4>(a, yt, s);
+    default: return run_wide<256, 256, 2, 4, 4>(a, yt, s);
   }
 }
 

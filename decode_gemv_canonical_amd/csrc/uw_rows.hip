@@ -87,14 +87,6 @@ __device__ __forceinline__ void unpack8(const Raw8& r, float (&f)[8]) {
   }
 }
 
-// fp32 pair -> bf16 pair, round to nearest even (v_cvt_pk_bf16_f32; a NaN stays a NaN).
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  bf16x2_t v;
-  v[0] = static_cast<__bf16>(lo);
-  v[1] = static_cast<__bf16>(hi);
-  return __builtin_bit_cast(uint32_t, v);
-}
-
 // Values [i, i + 8) of a row of n, written as bf16 or fp32.
 __device__ __forceinline__ void store8(char* row, int type, int64_t i, int64_t n, const float (&f)[8]) {
   if (i >= n) return;
