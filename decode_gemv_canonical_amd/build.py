@@ -1,5 +1,6 @@
 """Build libuw.so in-tree: hipcc for the gfx950 kernels, g++ for the host C++ (no
-library beyond the HIP runtime is linked).
+library beyond the HIP runtime is linked); and _uw_torch.so, the C++ side of
+the Python binding (torch's headers and libraries, g++).
 
     python decode_gemv_canonical_amd/build.py
 
@@ -8,9 +9,11 @@ rebuilt)
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libuw.so")
+BINDING = os.path.join(CSRC, "binding", "uw_torch.cpp")
+TORCH_LIB = os.path.join(LIBDIR, "_uw_torch.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
 
@@ -42,6 +47,15 @@ def _run(cmd: list[str], verbose: bool) -> None:
         print(err, file=sys.stderr)
 
 
+def _binding_command(out: str) -> list[str]:
+    # torch is found without importing it; its import takes longer than this compile
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc = os.path.join(torch_dir, "include")
+    return ["g++", *CXX_FLAGS, "-DUSE_ROCM", "-shared", "-Wno-sign-compare", f"-isystem{inc}",
+            f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-I{sysconfig.get_paths()['include']}",
+            BINDING, "-o", out, f"-L{os.path.join(torch_dir, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -57,12 +71,14 @@ def build(verbose: bool = False) -> str:
         else:
             continue
         objs.append(obj)
+    jobs.append(_binding_command(TORCH_LIB + ".tmp"))
     with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
         list(ex.map(lambda c: _run(c, verbose), jobs))
     tmp = LIB + ".tmp"
     _run([os.path.join(ROCM, "bin", "hipcc"), "-shared", f"--offload-arch={ARCH}", "-o", tmp, *objs,
           "-lpthread"], verbose)
     os.replace(tmp, LIB)
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
     return LIB
 
 

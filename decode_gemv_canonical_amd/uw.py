@@ -8,6 +8,8 @@ module raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 
@@ -15,6 +17,7 @@ import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libuw.so")
+TORCH_PATH = os.path.join(_HERE, "lib", "_uw_torch.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "uw.h")
 
 UW_OK = 0
@@ -143,14 +146,9 @@ def _check(rc: int, where: str) -> None:
         raise UwError(rc, where, (_lib.uw_last_error() or b"").decode())
 
 
-def _stream(stream, dev: int | None = None) -> int | None:
-    """The HIP stream of a call; None is the current one (of device `dev`
-    where it is known: its raw handle then comes without a stream object,
-    0.1 us instead of 2.8)."""
+def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        if dev is not None and _raw_stream is not None:
-            return _raw_stream(dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -571,63 +569,28 @@ def uw_sched_gemm(sched: int, slot: int, handle: int, X, Y, stream=None) -> None
 
 
 # -- the 8-bit activation path ------------------------------------------------
-# These take no handle: the current device is the one the tensors have to be
-# on, and every shape is checked here, where the buffers' sizes are known.
+# These take no handle.  A decode step calls them on kernels of a few
+# microseconds, so their checks (types, shapes, strides, the current device)
+# and the call itself are made in C++ (csrc/binding/uw_torch.cpp): 2.9 us less
+# per call than the same through ctypes.
 
-_raw_stream = None  # torch's accessor of a device's current stream, once a device is known
-
-
-def _op_device(t, name: str) -> int:
-    global _raw_stream
-    import torch
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    if _raw_stream is None:
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return dev
+_torch_side = None
 
 
-def _op_rows(t, shape, dev: int, name: str) -> int:
-    """Checks a row-major operand of this (rows, cols); its row stride."""
-    if t.shape != shape or len(shape) != 2:
-        want = f"shape {tuple(shape)}" if len(shape) == 2 else "two dimensions"
-        raise ValueError(f"{name} must have {want}, got shape {tuple(t.shape)}")
-    ld, inner = t.stride()
-    n, cols = shape
-    if (inner != 1 and cols > 1) or (ld < cols and n > 1):
-        raise ValueError(f"{name} must have a unit inner stride and rows that do not overlap")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    return ld
-
-
-def _op_scale(t, n: int, dev: int, name: str) -> int:
-    """Checks a contiguous fp32 vector of n values; its address."""
-    import torch
-    if t.shape != (n,) or t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name} must be a contiguous float32 vector of {n} values on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _op_i8(t, name: str) -> None:
-    import torch
-    if t.dtype is not torch.int8:
-        raise TypeError(f"{name} must be int8, got {t.dtype}")
-
-
-def _op_out(Y, scale, n: int, dev: int):
-    """The type code of a row operator's output, and its scales' address."""
-    import torch
-    if Y.dtype is not torch.int8:
-        if scale is not None:
-            raise ValueError("scale goes with an int8 output")
-        return _dtype_code(Y), None
-    if scale is None:
-        raise ValueError("an int8 output needs a scale vector")
-    return UW_I8, _op_scale(scale, n, dev, "scale")
+def _ops():
+    """The C++ side of the binding, loaded on first use (it needs torch)."""
+    global _torch_side
+    if _torch_side is None:
+        import torch  # noqa: F401  (its libraries have to be there first)
+        if not os.path.exists(TORCH_PATH):
+            raise ImportError(f"{TORCH_PATH} is not built; run python decode_gemv_canonical_amd/build.py")
+        loader = importlib.machinery.ExtensionFileLoader("_uw_torch", TORCH_PATH)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_uw_torch", loader))
+        loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
+            "uw_rmsnorm", "uw_silu_mul", "uw_i8_quantize", "uw_i8_dequantize", "uw_i8_gemm", "uw_i8_gemm_shaped")))
+        _torch_side = mod
+    return _torch_side
 
 
 def uw_rmsnorm(X, gain, Y, scale=None, residual=None, residual_out=None, eps: float = 1e-5, stream=None) -> None:
@@ -635,90 +598,46 @@ def uw_rmsnorm(X, gain, Y, scale=None, residual=None, residual_out=None, eps: fl
     float32, bfloat16, or int8 with `scale` (one float32 per row).
     residual_out receives h in the residual's dtype (the residual itself
     updates the stream in place); gain may be None (all ones)."""
-    dev, shape = _op_device(X, "X"), X.shape
-    ldx = _op_rows(X, shape, dev, "X")
-    n, cols = shape
-    ldy = _op_rows(Y, shape, dev, "Y")
-    yt, sp = _op_out(Y, scale, n, dev)
-    rp = hp = gp = None
-    ldr = ldh = 0
-    rt = gt = UW_F32
-    if residual is not None:
-        ldr, rt, rp = _op_rows(residual, shape, dev, "residual"), _dtype_code(residual), residual.data_ptr()
-    if residual_out is not None:
-        if residual is None or residual_out.dtype != residual.dtype:
-            raise ValueError("residual_out needs a residual of its dtype")
-        ldh, hp = _op_rows(residual_out, shape, dev, "residual_out"), residual_out.data_ptr()
-    if gain is not None:
-        if gain.shape != (cols,) or not gain.is_contiguous() or gain.get_device() != dev:
-            raise ValueError(f"gain must be a contiguous vector of {cols} elements on cuda:{dev}")
-        gt, gp = _dtype_code(gain), gain.data_ptr()
-    _check(_lib.uw_rmsnorm(X.data_ptr(), n, cols, ldx, _dtype_code(X), rp, ldr, rt, hp, ldh, gp, gt, eps, Y.data_ptr(),
-                           ldy, yt, sp, _stream(stream, dev)), "uw_rmsnorm")
+    rc = (_torch_side or _ops()).rmsnorm(X, gain, Y, scale, residual, residual_out, eps, stream)
+    if rc:
+        _check(rc, "uw_rmsnorm")
 
 
 def uw_silu_mul(G, U, Y, scale=None, stream=None) -> None:
     """Y = G / (1 + exp(-G)) * U per element (halves of one product's rows, for
     instance); Y and scale as for uw_rmsnorm."""
-    dev, shape = _op_device(G, "G"), G.shape
-    ldg = _op_rows(G, shape, dev, "G")
-    ldu = _op_rows(U, shape, dev, "U")
-    if U.dtype != G.dtype:
-        raise TypeError("G and U must have the same dtype")
-    n, cols = shape
-    ldy = _op_rows(Y, shape, dev, "Y")
-    yt, sp = _op_out(Y, scale, n, dev)
-    _check(_lib.uw_silu_mul(G.data_ptr(), ldg, U.data_ptr(), ldu, _dtype_code(G), n, cols, Y.data_ptr(), ldy, yt, sp,
-                            _stream(stream, dev)), "uw_silu_mul")
+    rc = (_torch_side or _ops()).silu_mul(G, U, Y, scale, stream)
+    if rc:
+        _check(rc, "uw_silu_mul")
 
 
 def uw_i8_quantize(X, Q, scale, stream=None) -> None:
     """Rows of X (float32 or bfloat16) as int8 with one float32 scale each."""
-    dev, shape = _op_device(X, "X"), X.shape
-    ldx = _op_rows(X, shape, dev, "X")
-    _op_i8(Q, "Q")
-    ldq = _op_rows(Q, shape, dev, "Q")
-    n, cols = shape
-    _check(_lib.uw_i8_quantize(X.data_ptr(), n, cols, ldx, _dtype_code(X), Q.data_ptr(), ldq,
-                               _op_scale(scale, n, dev, "scale"), _stream(stream, dev)), "uw_i8_quantize")
+    rc = (_torch_side or _ops()).quantize(X, Q, scale, stream)
+    if rc:
+        _check(rc, "uw_i8_quantize")
 
 
 def uw_i8_dequantize(Q, scale, Y, stream=None) -> None:
     """Y = Q * scale per row, float32 or bfloat16."""
-    dev, shape = _op_device(Q, "Q"), Q.shape
-    _op_i8(Q, "Q")
-    ldq = _op_rows(Q, shape, dev, "Q")
-    ldy = _op_rows(Y, shape, dev, "Y")
-    n, cols = shape
-    _check(_lib.uw_i8_dequantize(Q.data_ptr(), n, cols, ldq, _op_scale(scale, n, dev, "scale"), Y.data_ptr(), ldy,
-                                 _dtype_code(Y), _stream(stream, dev)), "uw_i8_dequantize")
-
-
-def _i8_operands(W, w_scale, X, x_scale, Y, bias, stream):
-    dev, shape = _op_device(W, "W"), W.shape
-    _op_i8(W, "W")
-    _op_i8(X, "X")
-    ldw = _op_rows(W, shape, dev, "W")
-    rows, cols = shape
-    n = x_scale.shape[0] if x_scale.dim() == 1 else -1
-    ldx = _op_rows(X, (n, cols), dev, "X")
-    ldy = _op_rows(Y, (n, rows), dev, "Y")
-    return (W.data_ptr(), rows, cols, ldw, _op_scale(w_scale, rows, dev, "w_scale"), X.data_ptr(), n, ldx,
-            _op_scale(x_scale, n, dev, "x_scale"), None if bias is None else _op_scale(bias, rows, dev, "bias"),
-            Y.data_ptr(), ldy, _dtype_code(Y)), _stream(stream, dev)
+    rc = (_torch_side or _ops()).dequantize(Q, scale, Y, stream)
+    if rc:
+        _check(rc, "uw_i8_dequantize")
 
 
 def uw_i8_gemm(W, w_scale, X, x_scale, Y, bias=None, stream=None) -> None:
     """Y[b, n] = x_scale[b] * w_scale[n] * sum_k X[b, k] W[n, k] (+ bias[n]),
     int8 W [rows, cols] and X [batch, cols], float32 scales and bias, Y
     float32 or bfloat16.  The sum is exact."""
-    a, s = _i8_operands(W, w_scale, X, x_scale, Y, bias, stream)
-    _check(_lib.uw_i8_gemm(*a, s), "uw_i8_gemm")
+    rc = (_torch_side or _ops()).gemm(W, w_scale, X, x_scale, Y, bias, stream)
+    if rc:
+        _check(rc, "uw_i8_gemm")
 
 
 def uw_i8_gemm_shaped(W, w_scale, X, x_scale, Y, shape: int, ks: int = 0, bias=None, stream=None) -> None:
-    a, s = _i8_operands(W, w_scale, X, x_scale, Y, bias, stream)
-    _check(_lib.uw_i8_gemm_shaped(*a, shape, ks, s), "uw_i8_gemm_shaped")
+    rc = (_torch_side or _ops()).gemm_shaped(W, w_scale, X, x_scale, Y, bias, shape, ks, stream)
+    if rc:
+        _check(rc, "uw_i8_gemm_shaped")
 
 
 def uw_i8_gemm_shape_count() -> int:
@@ -738,9 +657,11 @@ class Int8Matrix:
     uw_silu_mul or uw_i8_quantize write."""
 
     def __init__(self, q, scale):
-        _op_i8(q, "q")
-        _op_rows(q, q.shape, _op_device(q, "q"), "q")
-        _op_scale(scale, q.shape[0], q.get_device(), "scale")
+        import torch
+        if q.dtype != torch.int8 or q.dim() != 2 or not q.is_cuda or (q.stride(1) != 1 and q.shape[1] > 1):
+            raise ValueError("q must be a 2-D int8 CUDA tensor with a unit inner stride")
+        if scale.dtype != torch.float32 or scale.shape != q.shape[:1] or scale.device != q.device:
+            raise ValueError(f"scale must be a float32 vector of {q.shape[0]} values on {q.device}")
         self.q, self.scale = q, scale
         self.rows, self.cols = q.shape
 

@@ -607,7 +607,18 @@ def test_refusals_name_the_operand():
     ):
         with pytest.raises(TypeError):
             call()
+    for call in (
+        lambda: uw.uw_rmsnorm(x, None, y, stream="s"),
+        lambda: uw.uw_rmsnorm(x, None, y, eps="e"),
+        lambda: uw.uw_rmsnorm([1.0], None, y),
+    ):
+        with pytest.raises(TypeError):
+            call()
     with pytest.raises(uw.UwError):
         uw.uw_rmsnorm(x, None, y, eps=0.0)
+    with pytest.raises(uw.UwError):
+        uw.uw_i8_gemm_shaped(q, s, q, s, torch.zeros(4, 4, device=DEV), 1 << 40)
+    raw = torch.cuda.current_stream().cuda_stream
+    uw.uw_rmsnorm(x, None, y, stream=raw)
     uw.uw_rmsnorm(x[:0], None, y[:0])  # no rows: nothing to do
     uw.uw_i8_gemm(q, s, q[:0], s[:0], torch.zeros(0, 4, device=DEV))
