@@ -8,9 +8,9 @@ Tolerances, u = 2^-24 (half a step of fp32) and 2^-8 half a step of bf16:
            mean, root, reciprocal, gain and the last product add 6 u.  Scales
            add the division by 127 and one product.  Below: 32 u for values
            and scales.
-  silu     exp within 1 ulp (2 u), 1 + e (1 u), reciprocal within 1 ulp
-           (2 u), two products (2 u): 7 u, below 8 u, and 2^-118 |u_max| where the
-           reciprocal of a number past 2^126 is flushed.
+  silu     exp within 1.5 ulp (3 u), 1 + e (1 u), reciprocal within 1 ulp
+           (2 u), two products (2 u): 8 u, and 2^-118 |u_max| where the reciprocal
+           of a number past 2^126 is flushed.
   integers to the bit for the norm and quantize (the definition rounds every
            step in fp32); for silu p carries 8 u and the step another 10 u:
            an integer may move by one where p / s is within 127 * 20 u of a tie.
