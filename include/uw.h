@@ -582,8 +582,10 @@ int uw_sched_gemm(uw_sched* s, int slot, const void* d_X, int64_t batch, int64_t
  * These calls take no handle, allocate nothing, use no workspace and only
  * enqueue on `stream`; they may be captured into a graph, and calls on
  * different streams do not disturb each other.  Rows start at any multiple of
- * the element size (strides in elements).  Nothing outside the rows given is
- * read or written.  batch (or rows) == 0 is a no-op.
+ * the element size (strides in elements; a single row has none).  Nothing
+ * outside the rows given is written, and nothing outside the 16-byte words
+ * that hold them is read.  Outputs may be inputs only where it says so; other
+ * overlaps are not allowed.  batch (or rows) == 0 is a no-op.
  */
 
 /*
@@ -644,7 +646,8 @@ int uw_i8_dequantize(const int8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq,
 /*
  * uw_i8_gemm (device) - Y[b, n] = xs[b] * ws[n] * sum_k X[b, k] W[n, k]
  * (+ bias[n]) on the matrix cores.  The sum is exact (32-bit integers), so
- * results do not depend on the shape run.
+ * results do not depend on the shape run; it is rounded to fp32, multiplied by
+ * the product of the two scales (formed first, in fp32), and the bias added.
  *   d_W   rows x cols integers, row stride ldw >= cols; d_ws rows fp32 scales.
  *   d_X   batch x cols integers, row stride ldx >= cols; d_xs batch scales.
  *   d_bias  rows fp32 values, or NULL.
