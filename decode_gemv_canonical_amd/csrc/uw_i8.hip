@@ -14,6 +14,7 @@
 // the result holds weight rows 4 q .. 4 q + 3 for activation row r, four
 // consecutive values of a row of Y.
 #include <algorithm>
+#include <cmath>
 
 #include "uw_device.h"
 
@@ -484,18 +485,16 @@ __global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tile
   }
 }
 
-// Large batches: both operands of a BK-byte block of k are staged for the
+// Large batches: both operands of a 128-byte block of k are staged for the
 // whole workgroup, in a ring of ST stages: BW weight rows and BB activation
 // rows, whose WGW x WGB waves each hold a BW / WGW by BB / WGB tile.
-template <int BW, int BB, int WGW, int WGB, int BK, int ST, bool YBF16>
+template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16>
 __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
-  constexpr int NW = WGW * WGB;
+  constexpr int NW = WGW * WGB, BK = 128;
   constexpr int WI = BW / WGW / 16, BJ = BB / WGB / 16;
-  constexpr int LR = 1024 / BK;                      // rows of a 1 KB load
-  constexpr int LW = BW / LR / NW, LB = BB / LR / NW;  // loads per wave and stage
+  constexpr int LW = BW / 8 / NW, LB = BB / 8 / NW;  // 1 KB loads (8 rows) per wave and stage
   constexpr uint32_t kWBytes = BW * BK, kStage = (BW + BB) * BK;
-  static_assert(BW % (LR * NW) == 0 && BB % (LR * NW) == 0, "whole loads");
-  static_assert(BK == 64 || BK == 128, "bank spread");
+  static_assert(BW % (8 * NW) == 0 && BB % (8 * NW) == 0, "whole loads");
   // workgroups are dealt to the XCDs round-robin: each XCD takes a run of
   // tiles, 4 activation tiles deep, so that its L2 serves the rereads
   const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
@@ -506,15 +505,14 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   const int in = id - strip * kDeep * nw_tiles;
   const int64_t row0 = int64_t(in / deep) * BW, b0 = (int64_t(strip) * kDeep + in % deep) * BB;
   const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
-  // chunk c of row r lies at c ^ (r % 8) of rows of 8 chunks, c ^ (r / 2 % 4) of 4
-  const int lrow = lane / (BK / 16), lchunk = (lane % (BK / 16)) ^ (BK == 128 ? lrow & 7 : (lrow >> 1) & 3);
+  const int lrow = lane / 8, lchunk = (lane % 8) ^ lrow;
   const Staged tw(a.W + row0 * a.ldw, a.rows - row0, a.cols, a.ldw, BW);
   const Staged tx(a.X + b0 * a.ldx, a.batch - b0, a.cols, a.ldx, BB);
   uint32_t wvo[LW], xvo[LB];
 #pragma unroll
-  for (int u = 0; u < LW; ++u) wvo[u] = tw.row_offset(LR * (u * NW + wave) + lrow, a.ldw) + 16 * lchunk;
+  for (int u = 0; u < LW; ++u) wvo[u] = tw.row_offset(8 * (u * NW + wave) + lrow, a.ldw) + 16 * lchunk;
 #pragma unroll
-  for (int u = 0; u < LB; ++u) xvo[u] = tx.row_offset(LR * (u * NW + wave) + lrow, a.ldx) + 16 * lchunk;
+  for (int u = 0; u < LB; ++u) xvo[u] = tx.row_offset(8 * (u * NW + wave) + lrow, a.ldx) + 16 * lchunk;
   const int nkb = int((a.cols + BK - 1) / BK);
   const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % BK) / 16));
   auto issue = [&](int kb, int st) {
@@ -536,7 +534,7 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   auto multiply = [&](uint32_t base, bool tail) {
 #pragma unroll
     for (int s = 0; s < BK / 64; ++s) {
-      const uint32_t ch = uint32_t(((4 * s + q) ^ (BK == 128 ? r & 7 : (r >> 1) & 3)) * 16);
+      const uint32_t ch = uint32_t(((4 * s + q) ^ (r & 7)) * 16);
       u32x4 x[BJ];
 #pragma unroll
       for (int j = 0; j < BJ; ++j) x[j] = __builtin_bit_cast(u32x4, ld128(base + xrow + uint32_t(j) * (16 * BK) + ch));
@@ -696,16 +694,16 @@ int run_direct(const I8Args& a, int yt, int ks, hipStream_t s) {
   return hip_check(hipGetLastError(), "i8_direct_kernel launch");
 }
 
-template <int BW, int BB, int WGW, int WGB, int BK, int ST>
+template <int BW, int BB, int WGW, int WGB, int ST>
 int run_stage(const I8Args& a, int yt, hipStream_t s) {
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
   const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   constexpr int kThreads = 64 * WGW * WGB;
   if (per_xcd * kXcds * kThreads >= int64_t(1) << 32)
     return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
-  auto kern = yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, BK, ST, true> : i8_stage_kernel<BW, BB, WGW, WGB, BK, ST, false>;
+  auto kern = yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, true> : i8_stage_kernel<BW, BB, WGW, WGB, ST, false>;
   allow_full_lds(kern);
-  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * BK, s, a, int(nw),
+  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * 128, s, a, int(nw),
                      int(nb), int(per_xcd));
   return hip_check(hipGetLastError(), "i8_stage_kernel launch");
 }
@@ -740,22 +738,41 @@ int run_wide(const I8Args& a, int yt, hipStream_t s) {
 
 // Shapes: weight and batch rows of a workgroup's tile, and how its operands
 // reach the matrix cores: straight from global memory (any alignment), in
-// slices that each wave stages for itself, or staged for all waves.
+// slices that each wave stages for itself, or staged for all waves.  per_cu
+// workgroups fit a compute unit (by their LDS); start, alone and shared are us,
+// for expected_us below.
 enum Kind { kDirect, kSlice, kStage };
 struct I8Shape {
   int bw, bb;
   Kind kind;
+  int per_cu;
+  float start, alone, shared;
 };
 constexpr I8Shape kShapeList[] = {
-    {0, 0, kDirect},  // 0: the rule below
-    {16, 16, kDirect},  {16, 32, kDirect},  {32, 32, kDirect},
-    // the rule tries these from the end
-    {16, 16, kSlice},   {64, 16, kSlice},   {64, 16, kSlice},   {16, 32, kSlice},  {32, 32, kSlice}, {64, 32, kSlice},
-    {64, 64, kSlice},   {128, 64, kStage},  {128, 128, kStage}, {256, 128, kStage}, {224, 256, kStage}, {256, 256, kStage},
+    {0, 0, kDirect, 1, 0, 0, 0},  // 0: the choice below
+    {16, 16, kDirect, 1, 0, 0, 0},
+    {16, 32, kDirect, 1, 0, 0, 0},
+    {32, 32, kDirect, 1, 0, 0, 0},
+    {16, 16, kSlice, 2, 1.52f, 0.061f, 0.054f},
+    {64, 16, kSlice, 2, 1.77f, 0.165f, 0.141f},  // 4 waves
+    {64, 16, kSlice, 1, 1.77f, 0.165f, 0.141f},  // 8 waves: see pick_shape
+    {16, 32, kSlice, 1, 1.61f, 0.080f, 0.077f},
+    {32, 32, kSlice, 2, 1.81f, 0.120f, 0.115f},
+    {64, 32, kSlice, 1, 2.57f, 0.199f, 0.f},
+    {64, 64, kSlice, 1, 4.06f, 0.267f, 0.189f},
+    {32, 32, kStage, 5, 1.47f, 0.210f, 0.138f},
+    {32, 64, kStage, 3, 1.55f, 0.235f, 0.196f},
+    {64, 64, kStage, 4, 1.58f, 0.484f, 0.300f},  // 2 slots
+    {64, 64, kStage, 2, 1.76f, 0.327f, 0.304f},  // 4 slots
+    {64, 128, kStage, 2, 2.48f, 0.442f, 0.437f},
+    {128, 128, kStage, 2, 3.85f, 0.780f, 0.590f},  // 2 slots
+    {128, 128, kStage, 1, 3.85f, 0.700f, 0.570f},  // 3 slots
+    {256, 128, kStage, 1, 4.27f, 1.039f, 0.989f},
+    {224, 256, kStage, 1, 7.87f, 1.333f, 1.883f},  // see pick_shape
+    {256, 256, kStage, 1, 7.87f, 1.333f, 1.883f},
 };
 constexpr int kShapes = int(sizeof(kShapeList) / sizeof(kShapeList[0]));
-constexpr int kFirstStaged = 4, kTall4 = 5, kTall8 = 6;  // 64 x 16 with 4 and with 8 waves
-constexpr int kWide224 = 14, kWide256 = 15;
+constexpr int kFirstStaged = 4, kTall4 = 5, kTall8 = 6, kWide224 = 19, kWide256 = 20;
 constexpr int kCus = 256;
 
 bool stage_ok(const I8Args& a) {
@@ -764,44 +781,51 @@ bool stage_ok(const I8Args& a) {
          a.ldx % 16 == 0 && a.ldw < (int64_t(1) << 22) && a.ldx < (int64_t(1) << 22);
 }
 
-// The shape of a product: the largest tile that still gives 160 workgroups
-// (of 256 compute units) and is not mostly padding, else the smallest.  Large
-// tiles read the operands fewer times; fewer workgroups leave compute units
-// idle.  From a sweep of every shape (8 rotated operand sets), us of the
-// shape taken / of the next smaller / of the next larger tile:
-//   1 x 14336 x 4096   64 x 16: 12.4 / 13.3 (32) / 13.4 (64 x 32)
-//   1 x 4096 x 14336   16 x 16: 11.2 / - / 13.5 (32)
-//   32 x 4096 x 14336  16 x 32: 16.4 / 20.2 / 20.9
-//   64 x 8192 x 8192   64 x 32: 20.4 / 22.9 / 25.6
-//   77 x 4096 x 4096   64 x 32:  8.8 /  9.0 / 12.3
-//   256 x 4096 x 4096  64 x 64: 12.9 / 16.8 / 21.8
-//   256 x 14336 x 4096 128 x 128: 28.0 / 36.8 / 37.5
-//   512 x 14336 x 4096 256 x 128: 39.5 / 52.0 / 55.1
-//   1024 x 14336 x 4096 256 x 256: 58.4 / 73.3 / -
-// At 256 activation rows the tile has 224 weight rows instead of 256 where
-// that wastes less of the last round of workgroups (4096 x 14336 x 4096: 4
-// rounds either way, 223 us against 235).
-// Operands that are not 16-byte aligned run the direct shapes.
-void pick_shape(int64_t rows, int64_t batch, bool staged, int* shape) {
+// What a product takes on a shape, in us: 1.6 for the launch, then rounds of
+// workgroups.  Each round costs `start` (first loads, epilogue) and `alone` per
+// 128-byte block of k where a workgroup waits on its own loads; a compute unit
+// needs `shared` per block and workgroup it holds; and the operands' bytes come
+// at 5.4 TB/s.  The three limits of the loop add as fourth powers (the largest
+// rules, a near second counts).
+// The constants are fits to every shape's times on 520 sizes drawn over 1..4096
+// x 64..28672 x 64..14336 (and the MLP's), each on 3 to 8 rotated operand sets;
+// the shapes so chosen take 1.03 of the best shape's time in the mean, against
+// 1.20 for the largest tile that gives 160 workgroups.
+float expected_us(const I8Shape& s, int64_t rows, int64_t cols, int64_t batch) {
+  const float blocks = float((cols + 127) / 128);
+  const float n = float((rows + s.bw - 1) / s.bw) * float((batch + s.bb - 1) / s.bb) / kCus;
+  const float rounds = std::ceil(n / float(s.per_cu));
+  const float held = n < 1.f ? n : 0.5f * (n + std::ceil(n));
+  const auto p4 = [](float v) { return v * v * v * v; };
+  const float loop = p4(blocks * s.alone * rounds) + p4(blocks * s.shared * held) +
+                     p4(float(rows + batch) * blocks * (128.f / 5.4e6f));
+  return 1.6f + s.start * rounds + std::sqrt(std::sqrt(loop));
+}
+
+// Operands that are not 16-byte aligned run the direct shapes; the others the
+// shape expected to be fastest.  Two choices the expectation is too coarse for:
+//   64 x 16: one workgroup per compute unit takes 8 waves (1 x 14336 x 4096 12.4
+//     us against 12.7), more take 4 (16 x 28672 x 4096 22.3 against 24.2);
+//   256 x 256: 224 weight rows instead where that wastes less of the last round
+//     of workgroups (4096 x 14336 x 4096: 4 rounds either way, 223 against 235).
+void pick_shape(int64_t rows, int64_t cols, int64_t batch, bool staged, int* shape) {
   if (!staged) {
     *shape = batch <= 16 ? 1 : batch <= 32 ? 2 : 3;
     return;
   }
-  for (int i = kShapes - 1; i > kFirstStaged; --i) {
-    if (i == kWide224) continue;
-    const I8Shape& s = kShapeList[i];
-    const int64_t tiles = (rows + s.bw - 1) / s.bw * ((batch + s.bb - 1) / s.bb);
-    if ((s.bb > 16 && s.bb / 2 >= batch) || tiles < 160) continue;
-    // 64 x 16: one workgroup per compute unit takes 8 waves (12.4 us against 12.7 at 1 x 14336 x 4096), more take 4
-    // (22.3 against 24.2 at 16 x 28672 x 4096)
-    *shape = s.bb == 16 ? (tiles <= kCus ? kTall8 : kTall4) : i;
-    if (i == kWide256) {
-      const int64_t t224 = (rows + 223) / 224 * ((batch + 255) / 256);
-      if ((t224 + kCus - 1) / kCus * 224 < (tiles + kCus - 1) / kCus * 256) *shape = kWide224;
+  float best = 0.f;
+  for (int i = kFirstStaged; i < kShapes; ++i) {
+    if (i == kTall8 || i == kWide224) continue;
+    const float us = expected_us(kShapeList[i], rows, cols, batch);
+    if (i == kFirstStaged || us < best) {
+      best = us;
+      *shape = i;
     }
-    return;
   }
-  *shape = kFirstStaged;
+  const auto tiles = [&](int bw, int bb) { return (rows + bw - 1) / bw * ((batch + bb - 1) / bb); };
+  const auto rounds = [&](int bw) { return (tiles(bw, 256) + kCus - 1) / kCus * bw; };
+  if (*shape == kTall4 && tiles(64, 16) <= kCus) *shape = kTall8;
+  if (*shape == kWide256 && rounds(224) < rounds(256)) *shape = kWide224;
 }
 
 }  // namespace
@@ -823,7 +847,7 @@ int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, con
   // a single row has no stride
   const I8Args a{W, sw, X, sx, bias, static_cast<char*>(Y), rows, cols, rows > 1 ? ldw : 0, batch, batch > 1 ? ldx : 0, ldy};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (shape <= 0) pick_shape(rows, batch, stage_ok(a), &shape);
+  if (shape <= 0) pick_shape(rows, cols, batch, stage_ok(a), &shape);
   if (ks <= 0) ks = 8;
   switch (shape) {
     case 1: return run_direct<1, 1>(a, yt, ks, s);
@@ -836,10 +860,15 @@ int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, con
     case 8: return run_slice<32, 32, 4, 2>(a, yt, s);
     case 9: return run_slice<64, 32, 4, 2>(a, yt, s);
     case 10: return run_slice<64, 64, 4, 2>(a, yt, s);
-    case 11: return run_stage<128, 64, 4, 1, 128, 4>(a, yt, s);
-    case 12: return run_stage<128, 128, 2, 2, 128, 3>(a, yt, s);
-    case 13: return run_stage<256, 128, 4, 2, 128, 3>(a, yt, s);
-    case 14: return run_wide<224, 256, 2, 4, 4>(a, yt, s);
+    case 11: return run_stage<32, 32, 2, 2, 4>(a, yt, s);
+    case 12: return run_stage<32, 64, 2, 2, 4>(a, yt, s);
+    case 13: return run_stage<64, 64, 2, 2, 2>(a, yt, s);
+    case 14: return run_stage<64, 64, 2, 2, 4>(a, yt, s);
+    case 15: return run_stage<64, 128, 2, 2, 3>(a, yt, s);
+    case 16: return run_stage<128, 128, 2, 2, 2>(a, yt, s);
+    case 17: return run_stage<128, 128, 2, 2, 3>(a, yt, s);
+    case 18: return run_stage<256, 128, 4, 2, 3>(a, yt, s);
+    case 19: return run_wide<224, 256, 2, 4, 4>(a, yt, s);
     default: return run_wide<256, 256, 2, 4, 4>(a, yt, s);
   }
 }

@@ -370,7 +370,7 @@ int run_rows(const RowArgs& a, hipStream_t s) {
   if (chunks <= 64) return go(row_kernel<OP, XT, RT, I8, 64, 1>, 256, 4);
   if (chunks <= 128) return go(row_kernel<OP, XT, RT, I8, 64, 2>, 256, 4);
   if (chunks <= 256) return go(row_kernel<OP, XT, RT, I8, 256, 1>, 256, 1);
-  if (chunks <= 512 && a.rows > 4096) return go(row_kernel<OP, XT, RT, I8, 256, 2>, 256, 1);
+  if (chunks <= 512 && a.rows > 1024) return go(row_kernel<OP, XT, RT, I8, 256, 2>, 256, 1);
   if (chunks <= 512) return go(row_kernel<OP, XT, RT, I8, 512, 1>, 512, 1);
   if (chunks <= 1024) return go(row_kernel<OP, XT, RT, I8, 1024, 1>, 1024, 1);
   if (chunks <= 2048) return go(row_kernel<OP, XT, RT, I8, 1024, 2>, 1024, 1);
