@@ -97,15 +97,17 @@ __device__ __forceinline__ void load_row4(const float* p, int64_t n, int64_t row
   for (int e = 0; e < 4; ++e) v[e] = p[std::min<int64_t>(n + e, rows - 1)];
 }
 
-// 16 bytes of row b of Y from column n on: 16 / SIZE values.
-template <int SIZE>
+// 16 bytes of row b of Y from column n on: 16 / SIZE values.  NT: whole lines
+// are written, past the caches.
+template <int SIZE, bool NT>
 __device__ __forceinline__ void store_row16(const I8Args& a, int64_t b, int64_t n, const uint4& v) {
   if (b >= a.batch || n >= a.rows) return;
   char* y = a.Y + (b * a.ldy + n) * SIZE;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   const int m = int(std::min<int64_t>(16 / SIZE, a.rows - n));
   if (m == 16 / SIZE) {
-    __builtin_memcpy(y, w, 16);
+    if (NT) __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(y));
+    else __builtin_memcpy(y, w, 16);
     return;
   }
 #pragma unroll
@@ -173,7 +175,10 @@ __device__ __forceinline__ void store_tiles(const I8Args& a, int64_t row0, int64
 // 32 WI bytes (bf16) or twice that (without it, 4096 x 4096 x 64 took 19.1 us,
 // with it 13.4); 16 bytes of padding a row spread the writes over the banks.
 // The scales are read before anything is stored.  LDS: bytes a wave has.
-template <int WI, int BJ, bool YBF16, int LDS>
+// NT: Y's rows start at whole lines, which are then stored non-temporally and
+// leave the caches to the operands (4096 x 14336 x 4096: 237 -> 215 us, 2048 x
+// 4096 x 14336: 124 -> 117; a silu that reads the result next loses nothing).
+template <int WI, int BJ, bool YBF16, bool NT, int LDS>
 __device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, int64_t bw0, int wave, int lane,
                                                   const i32x4 (&acc)[WI][BJ]) {
   constexpr int kCols = 16 * WI, kSize = YBF16 ? 2 : 4, kPitch = kCols * kSize + 16;
@@ -210,7 +215,7 @@ __device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, i
     for (int c0 = 0; c0 < kChunks; c0 += kWave) {
       const int at = c0 + lane, br = at / kLanes, c = at % kLanes * kPer;
       if (kChunks % kWave == 0 || at < kChunks)
-        store_row16<kSize>(a, bw0 + 16 * j + br, n0 + c, ld128(out + uint32_t(br) * kPitch + uint32_t(c) * kSize));
+        store_row16<kSize, NT>(a, bw0 + 16 * j + br, n0 + c, ld128(out + uint32_t(br) * kPitch + uint32_t(c) * kSize));
     }
     wave_lds_fence();
   }
@@ -488,7 +493,7 @@ __global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tile
 // Large batches: both operands of a 128-byte block of k are staged for the
 // whole workgroup, in a ring of ST stages: BW weight rows and BB activation
 // rows, whose WGW x WGB waves each hold a BW / WGW by BB / WGB tile.
-template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16>
+template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16, bool NT>
 __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
   constexpr int NW = WGW * WGB, BK = 128;
   constexpr int WI = BW / WGW / 16, BJ = BB / WGB / 16;
@@ -564,7 +569,7 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   };
   for (int kb = 0; kb < nkb - 1; ++kb) step(kb, false);
   step(nkb - 1, a.cols % BK != 0);
-  store_through_lds<WI, BJ, YBF16, int(ST * kStage) / NW>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16, wave, lane, acc);
+  store_through_lds<WI, BJ, YBF16, NT, int(ST * kStage) / NW>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16, wave, lane, acc);
 }
 
 // The largest batches.  As above with the operands of the next step read
@@ -578,14 +583,14 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
 // in registers, reach 3.4 POP/s on random values.  32 x 32 products (twice the
 // accumulator traffic per operation) took 265 us there, four waves with the
 // 16 x 16 form 241 us, the kernel above at 256 x 256 219 us.
-template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16>
+template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16, bool NT>
 __global__ __launch_bounds__(64 * WGW * WGB) void i8_wide_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
   constexpr int NW = WGW * WGB;
   constexpr int WI = BW / WGW / 16, BJ = BB / WGB / 16;  // 16 x 16 tiles of a wave
-  constexpr int NLW = BW / 16, NLB = BB / 16;            // 1 KB loads of a step
-  constexpr int LW = (NLW + NW - 1) / NW, LB = (NLB + NW - 1) / NW, L = LW + LB;  // per wave
+  constexpr int LW = BW / 16 / NW, LB = BB / 16 / NW, L = LW + LB;  // 1 KB loads (16 rows) per wave and step
   constexpr int G = WI + BJ, M = WI * BJ;                // operand reads and products per step
   constexpr uint32_t kWBytes = BW * 64, kStep = (BW + BB) * 64;
+  static_assert(BW % (16 * NW) == 0 && BB % (16 * NW) == 0, "whole loads");
   static_assert(ST * kStep <= kLdsLimit && ST >= 3 && M >= 2 * G && M >= 4 * L, "ring");
   const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
   if (id >= nw_tiles * nb_tiles) return;  // whole workgroups
@@ -598,25 +603,16 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_wide_kernel(I8Args a, int n
   const int lrow = lane / 4, lchunk = (lane % 4) ^ ((lrow >> 1) & 3);
   const Staged tw(a.W + row0 * a.ldw, a.rows - row0, a.cols, a.ldw, BW);
   const Staged tx(a.X + b0 * a.ldx, a.batch - b0, a.cols, a.ldx, BB);
-  // load u of this wave; a tile whose loads the waves do not share evenly has
-  // its last one made twice (the same bytes to the same place)
-  uint32_t vo[L], dst[L];
+  uint32_t vo[L];
 #pragma unroll
-  for (int u = 0; u < LW; ++u) {
-    const int l = min(u * NW + wave, NLW - 1);
-    vo[u] = tw.row_offset(16 * l + lrow, a.ldw) + 16 * lchunk;
-    dst[u] = uint32_t(l) * 1024;
-  }
+  for (int u = 0; u < LW; ++u) vo[u] = tw.row_offset(16 * (u * NW + wave) + lrow, a.ldw) + 16 * lchunk;
 #pragma unroll
-  for (int u = 0; u < LB; ++u) {
-    const int l = min(u * NW + wave, NLB - 1);
-    vo[LW + u] = tx.row_offset(16 * l + lrow, a.ldx) + 16 * lchunk;
-    dst[LW + u] = kWBytes + uint32_t(l) * 1024;
-  }
+  for (int u = 0; u < LB; ++u) vo[LW + u] = tx.row_offset(16 * (u * NW + wave) + lrow, a.ldx) + 16 * lchunk;
   const int n = int((a.cols + 63) / 64);
   const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % 64) / 16));
   auto issue = [&](int u, int t, int slot, bool last) {
-    stage_load<false>(u < LW ? tw.rsrc : tx.rsrc, vo[u] - (last ? over : 0), uint32_t(t) * 64, uint32_t(slot) * kStep + dst[u]);
+    const uint32_t dst = uint32_t(slot) * kStep + (u < LW ? uint32_t(u * NW + wave) * 1024 : kWBytes + uint32_t((u - LW) * NW + wave) * 1024);
+    stage_load<false>(u < LW ? tw.rsrc : tx.rsrc, vo[u] - (last ? over : 0), uint32_t(t) * 64, dst);
   };
   const int r = lane % 16, q = lane / 16;
   const int ww = wave / WGB, wb = wave % WGB;
@@ -679,7 +675,7 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_wide_kernel(I8Args a, int n
     mask(t + 1, f1);
     step(t + 1, f1, f0, false);
   }
-  store_through_lds<WI, BJ, YBF16, int(ST * kStep) / NW>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16, wave, lane, acc);
+  store_through_lds<WI, BJ, YBF16, NT, int(ST * kStep) / NW>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16, wave, lane, acc);
 }
 
 template <int RB, int TB>
@@ -694,6 +690,11 @@ int run_direct(const I8Args& a, int yt, int ks, hipStream_t s) {
   return hip_check(hipGetLastError(), "i8_direct_kernel launch");
 }
 
+// Whether every row of Y starts at a 128-byte line.
+bool whole_lines(const I8Args& a, int yt) {
+  return reinterpret_cast<uintptr_t>(a.Y) % 128 == 0 && a.ldy * int64_t(elem_size(yt)) % 128 == 0;
+}
+
 template <int BW, int BB, int WGW, int WGB, int ST>
 int run_stage(const I8Args& a, int yt, hipStream_t s) {
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
@@ -701,7 +702,9 @@ int run_stage(const I8Args& a, int yt, hipStream_t s) {
   constexpr int kThreads = 64 * WGW * WGB;
   if (per_xcd * kXcds * kThreads >= int64_t(1) << 32)
     return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
-  auto kern = yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, true> : i8_stage_kernel<BW, BB, WGW, WGB, ST, false>;
+  auto kern = whole_lines(a, yt)
+                  ? (yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, true, true> : i8_stage_kernel<BW, BB, WGW, WGB, ST, false, true>)
+                  : (yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, true, false> : i8_stage_kernel<BW, BB, WGW, WGB, ST, false, false>);
   allow_full_lds(kern);
   hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * 128, s, a, int(nw),
                      int(nb), int(per_xcd));
@@ -729,7 +732,9 @@ int run_wide(const I8Args& a, int yt, hipStream_t s) {
   const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   constexpr int kThreads = 64 * WGW * WGB;
   if (per_xcd * kXcds * kThreads >= int64_t(1) << 32) return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
-  auto kern = yt == UW_BF16 ? i8_wide_kernel<BW, BB, WGW, WGB, ST, true> : i8_wide_kernel<BW, BB, WGW, WGB, ST, false>;
+  auto kern = whole_lines(a, yt)
+                  ? (yt == UW_BF16 ? i8_wide_kernel<BW, BB, WGW, WGB, ST, true, true> : i8_wide_kernel<BW, BB, WGW, WGB, ST, false, true>)
+                  : (yt == UW_BF16 ? i8_wide_kernel<BW, BB, WGW, WGB, ST, true, false> : i8_wide_kernel<BW, BB, WGW, WGB, ST, false, false>);
   allow_full_lds(kern);
   hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * 64, s, a, int(nw),
                      int(nb), int(per_xcd));
@@ -768,11 +773,10 @@ constexpr I8Shape kShapeList[] = {
     {128, 128, kStage, 2, 3.85f, 0.780f, 0.590f},  // 2 slots
     {128, 128, kStage, 1, 3.85f, 0.700f, 0.570f},  // 3 slots
     {256, 128, kStage, 1, 4.27f, 1.039f, 0.989f},
-    {224, 256, kStage, 1, 7.87f, 1.333f, 1.883f},  // see pick_shape
     {256, 256, kStage, 1, 7.87f, 1.333f, 1.883f},
 };
 constexpr int kShapes = int(sizeof(kShapeList) / sizeof(kShapeList[0]));
-constexpr int kFirstStaged = 4, kTall4 = 5, kTall8 = 6, kWide224 = 19, kWide256 = 20;
+constexpr int kFirstStaged = 4, kTall4 = 5, kTall8 = 6;
 constexpr int kCus = 256;
 
 bool stage_ok(const I8Args& a) {
@@ -803,11 +807,9 @@ float expected_us(const I8Shape& s, int64_t rows, int64_t cols, int64_t batch) {
 }
 
 // Operands that are not 16-byte aligned run the direct shapes; the others the
-// shape expected to be fastest.  Two choices the expectation is too coarse for:
-//   64 x 16: one workgroup per compute unit takes 8 waves (1 x 14336 x 4096 12.4
-//     us against 12.7), more take 4 (16 x 28672 x 4096 22.3 against 24.2);
-//   256 x 256: 224 weight rows instead where that wastes less of the last round
-//     of workgroups (4096 x 14336 x 4096: 4 rounds either way, 223 against 235).
+// shape expected to be fastest.  64 x 16 comes twice, too close for the
+// expectation: one workgroup per compute unit takes 8 waves (1 x 14336 x 4096
+// 12.4 us against 12.7), more take 4 (16 x 28672 x 4096 22.3 against 24.2).
 void pick_shape(int64_t rows, int64_t cols, int64_t batch, bool staged, int* shape) {
   if (!staged) {
     *shape = batch <= 16 ? 1 : batch <= 32 ? 2 : 3;
@@ -815,17 +817,14 @@ void pick_shape(int64_t rows, int64_t cols, int64_t batch, bool staged, int* sha
   }
   float best = 0.f;
   for (int i = kFirstStaged; i < kShapes; ++i) {
-    if (i == kTall8 || i == kWide224) continue;
+    if (i == kTall8) continue;
     const float us = expected_us(kShapeList[i], rows, cols, batch);
     if (i == kFirstStaged || us < best) {
       best = us;
       *shape = i;
     }
   }
-  const auto tiles = [&](int bw, int bb) { return (rows + bw - 1) / bw * ((batch + bb - 1) / bb); };
-  const auto rounds = [&](int bw) { return (tiles(bw, 256) + kCus - 1) / kCus * bw; };
-  if (*shape == kTall4 && tiles(64, 16) <= kCus) *shape = kTall8;
-  if (*shape == kWide256 && rounds(224) < rounds(256)) *shape = kWide224;
+  if (*shape == kTall4 && (rows + 63) / 64 * ((batch + 15) / 16) <= kCus) *shape = kTall8;
 }
 
 }  // namespace
@@ -868,7 +867,6 @@ int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, con
     case 16: return run_stage<128, 128, 2, 2, 2>(a, yt, s);
     case 17: return run_stage<128, 128, 2, 2, 3>(a, yt, s);
     case 18: return run_stage<256, 128, 4, 2, 3>(a, yt, s);
-    case 19: return run_wide<224, 256, 2, 4, 4>(a, yt, s);
     default: return run_wide<256, 256, 2, 4, 4>(a, yt, s);
   }
 }

@@ -381,6 +381,13 @@ def test_gemm_direct_waves(ks, cols):
         run_gemm(20, 48, cols, "f32", shape=shape, ks=ks)
 
 
+@pytest.mark.parametrize("shape", range(4, uw.uw_i8_gemm_shape_count()))
+def test_gemm_whole_lines(shape):
+    """Rows of Y at multiples of 128 bytes (the others above mostly are not), with the row's end inside a line."""
+    for b, rows, out in ((300, 512, "bf16"), (300, 320, "f32"), (130, 500, "bf16"), (70, 250, "f32")):
+        run_gemm(b, rows, 384, out, bias=True, shape=shape, ypad=-rows % (64 if out == "bf16" else 32))
+
+
 @pytest.mark.parametrize("b", [1, 2, 8, 15, 16, 17, 32, 33, 48, 64, 65, 96, 128, 200, 256])
 @pytest.mark.parametrize("rows,cols", [(1024, 1024), (1000, 4100), (517, 333)])
 def test_gemm_auto(b, rows, cols):
