@@ -87,13 +87,22 @@ __device__ __forceinline__ void unpack8(const Raw8& r, float (&f)[8]) {
   }
 }
 
+// 16 bytes at any element alignment; past: non-temporally.
+__device__ __forceinline__ void store16_any(void* p, const u32x4& v, bool past) {
+  typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
+  const any4 w{v.x, v.y, v.z, v.w};
+  if (past) __builtin_nontemporal_store(w, static_cast<any4*>(p));
+  else *static_cast<any4*>(p) = w;
+}
+
 // Values [i, i + 8) of a row of n, written as bf16 or fp32.
-__device__ __forceinline__ void store8(char* row, int type, int64_t i, int64_t n, const float (&f)[8]) {
+__device__ __forceinline__ void store8(char* row, int type, int64_t i, int64_t n, const float (&f)[8], bool past = false) {
   if (i >= n) return;
   if (type == UW_F32) {
     float* p = reinterpret_cast<float*>(row) + i;
     if (i + 8 <= n) {
-      __builtin_memcpy(p, f, 32);
+      store16_any(p, u32x4{f32_bits(f[0]), f32_bits(f[1]), f32_bits(f[2]), f32_bits(f[3])}, past);
+      store16_any(p + 4, u32x4{f32_bits(f[4]), f32_bits(f[5]), f32_bits(f[6]), f32_bits(f[7])}, past);
       return;
     }
 #pragma unroll
@@ -106,7 +115,7 @@ __device__ __forceinline__ void store8(char* row, int type, int64_t i, int64_t n
   for (int e = 0; e < 4; ++e) w[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
   uint16_t* p = reinterpret_cast<uint16_t*>(row) + i;
   if (i + 8 <= n) {
-    __builtin_memcpy(p, w, 16);
+    store16_any(p, u32x4{w[0], w[1], w[2], w[3]}, past);
     return;
   }
 #pragma unroll
@@ -181,7 +190,15 @@ struct RowArgs {
   int64_t rows, cols, ldx, ldr, ldh, ldy;  // strides in elements
   float eps, inv_cols;
   int gt, yt;
+  bool h_past;  // h is stored past the caches
 };
+
+// A stream of this many bytes is not read again before other data has taken
+// its place in the caches: stored past them, it leaves them to what the norm
+// reads and to y, which the next product reads (1111 x 8192, fp32 stream: 24.0
+// -> 19.6 us, 25.1 -> 24.1 with cold inputs; 2048 x 4096, bf16: 18.2 -> 17.9
+// with the dequantize behind it).  y itself stored so is slower to read next.
+constexpr int64_t kStreamPast = int64_t(16) << 20;
 
 // exp(-g) = 2^t, t = -g log2(e): 2^t from the transcendental unit (1 ulp),
 // times 2^d for what the rounding of t lost, d = (-g log2(e)) - t with log2(e)
@@ -212,7 +229,7 @@ __device__ __forceinline__ void chunk_p(const RowArgs& a, const Raw8& xr, const 
 #pragma unroll
         for (int e = 0; e < 8; ++e) p[e] = static_cast<float>(static_cast<__bf16>(p[e]));
       }
-      if (hrow) store8(hrow, RT, i, a.cols, p);
+      if (hrow) store8(hrow, RT, i, a.cols, p, a.h_past);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = fmaf(p[e], p[e], sum);
@@ -417,7 +434,7 @@ int launch_rmsnorm(const void* X, int64_t batch, int64_t cols, int64_t ldx, int 
                    float* scale, void* stream) {
   RowArgs a{static_cast<const char*>(X), static_cast<const char*>(R), static_cast<const char*>(gain),
             static_cast<char*>(H), static_cast<char*>(Y), scale, batch, cols, ldx, ldr, ldh, ldy, eps,
-            float(1.0 / double(cols)), gt, yt};
+            float(1.0 / double(cols)), gt, yt, batch * cols * int64_t(elem_size(rt)) >= kStreamPast};
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!R) return xt == UW_F32 ? run_out<kNorm, kF32, kNone>(a, s) : run_out<kNorm, kBf16, kNone>(a, s);
   if (rt == UW_F32) return xt == UW_F32 ? run_out<kNorm, kF32, kF32>(a, s) : run_out<kNorm, kBf16, kF32>(a, s);
@@ -427,7 +444,7 @@ int launch_rmsnorm(const void* X, int64_t batch, int64_t cols, int64_t ldx, int 
 int launch_silu_mul(const void* G, int64_t ldg, const void* U, int64_t ldu, int xt, int64_t batch, int64_t cols,
                     void* Y, int64_t ldy, int yt, float* scale, void* stream) {
   RowArgs a{static_cast<const char*>(G), static_cast<const char*>(U), nullptr, nullptr, static_cast<char*>(Y), scale,
-            batch, cols, ldg, ldu, 0, ldy, 0.f, 0.f, 0, yt};
+            batch, cols, ldg, ldu, 0, ldy, 0.f, 0.f, 0, yt, false};
   hipStream_t s = static_cast<hipStream_t>(stream);
   return xt == UW_F32 ? run_out<kSilu, kF32, kF32>(a, s) : run_out<kSilu, kBf16, kBf16>(a, s);
 }
@@ -435,7 +452,7 @@ int launch_silu_mul(const void* G, int64_t ldg, const void* U, int64_t ldu, int 
 int launch_i8_quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, int xt, int8_t* Q, int64_t ldq,
                        float* scale, void* stream) {
   RowArgs a{static_cast<const char*>(X), nullptr, nullptr, nullptr, reinterpret_cast<char*>(Q), scale, rows, cols, ldx,
-            0, 0, ldq, 0.f, 0.f, 0, UW_I8};
+            0, 0, ldq, 0.f, 0.f, 0, UW_I8, false};
   hipStream_t s = static_cast<hipStream_t>(stream);
   return xt == UW_F32 ? run_rows<kQuantize, kF32, kNone, true>(a, s) : run_rows<kQuantize, kBf16, kNone, true>(a, s);
 }

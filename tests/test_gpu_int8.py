@@ -151,6 +151,10 @@ def test_norm_strides_and_offsets(cols, pad, shift):
 def test_norm_many_rows():
     run_norm(1111, 4096, "bf16", "bf16", "bf16", "i8")
     run_norm(2049, 96, "bf16", "f32", "bf16", "bf16")
+    # streams of over 16 MiB
+    run_norm(2100, 4096, "bf16", "bf16", "bf16", "i8")
+    run_norm(1030, 4101, "bf16", "f32", "bf16", "bf16", pad=3, shift=1)
+    run_norm(140, 33000, "f32", "f32", "f32", "f32")
 
 
 def special_rows(cols, dtype):
