@@ -420,10 +420,19 @@ __global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tile
   for (int u = 0; u < LB; ++u) xvo[u] = tx.row_offset(8 * u + lrow, a.ldx) + 16 * lchunk;
   const uint32_t ring = uint32_t(wave) * (ST * kSlot);
   const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
+  // Rows whose stride is a multiple of 4 KB have the same k on the same memory
+  // channels: the workgroups of an XCD then start at k's spread over the row
+  // (1 x 8192 x 8192: 13.4 -> 12.2 us, 16 x 28672 x 4096: 22.3 -> 20.5, 32 x
+  // 8192 x 8192: 17.3 -> 15.2; at a stride of 14336 it costs 2 %).
+  const int rot = a.ldw % 4096 == 0 ? __builtin_amdgcn_readfirstlane(int(int64_t(wt / kXcds % 32) * nkb / 32)) : 0;
+  auto block = [&](int i) {
+    const int p = wave + KW * i + rot;
+    return p >= nkb ? p - nkb : p;
+  };
   // in the last block, how far a lane's chunk lies past the row's last one
   const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % 128) / 16));
   auto issue = [&](int i, int st) {
-    const int kb = wave + KW * i;
+    const int kb = block(i);
     const uint32_t base = ring + uint32_t(st) * kSlot, k = uint32_t(kb) * 128, back = kb == nkb - 1 ? over : 0;
 #pragma unroll
     for (int u = 0; u < LW; ++u) stage_load<NT>(tw.rsrc, wvo[u] - back, k, base + u * 1024);
@@ -456,7 +465,7 @@ __global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tile
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot's operands are in registers
       issue(i + ST, st);
     }
-    const int kb = wave + KW * i;
+    const int kb = block(i);
     if (kb == nkb - 1 && a.cols % 128) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
