@@ -227,12 +227,11 @@ __device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, i
 // summed in LDS.  The next group's loads are issued before this group's
 // products.  Rows may start at any byte; nothing outside a row is read.
 template <int RB, int TB, bool YBF16>
-__global__ __launch_bounds__(512) void i8_direct_kernel(I8Args a, int n_groups, int ny) {
+__global__ __launch_bounds__(512) void i8_direct_kernel(I8Args a, int n_groups, int ny, int KS) {
   const int L = int(blockIdx.x);
   const int grp = (L / (kXcds * ny)) * kXcds + L % kXcds;
   const int y = (L / kXcds) % ny;
   if (grp >= n_groups) return;  // whole workgroups
-  const int KS = int(blockDim.x) / kWave;
   const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int r = lane % 16, q = lane / 16;
   const int64_t row0 = int64_t(grp) * 16 * RB, b0 = int64_t(y) * 16 * TB;
@@ -695,7 +694,7 @@ int run_direct(const I8Args& a, int yt, int ks, hipStream_t s) {
   const size_t lds = ks > 1 ? size_t(ks) * RB * TB * 1024 : 0;
   auto kern = yt == UW_BF16 ? i8_direct_kernel<RB, TB, true> : i8_direct_kernel<RB, TB, false>;
   allow_full_lds(kern);
-  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(ks * kWave), lds, s, a, int(n_groups), int(ny));
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(ks * kWave), lds, s, a, int(n_groups), int(ny), ks);
   return hip_check(hipGetLastError(), "i8_direct_kernel launch");
 }
 

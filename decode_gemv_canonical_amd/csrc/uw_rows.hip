@@ -180,6 +180,7 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
   }
 }
 
+// 112 bytes: with 120 every launch took 0.4 us longer.
 struct RowArgs {
   const char* x;
   const char* r;  // the residual (norm) or u (silu)
@@ -189,7 +190,7 @@ struct RowArgs {
   float* scale;  // 8-bit outputs
   int64_t rows, cols, ldx, ldr, ldh, ldy;  // strides in elements
   float eps, inv_cols;
-  int gt, yt;
+  int8_t gt, yt;
   bool h_past;  // h is stored past the caches
 };
 
@@ -434,7 +435,7 @@ int launch_rmsnorm(const void* X, int64_t batch, int64_t cols, int64_t ldx, int 
                    float* scale, void* stream) {
   RowArgs a{static_cast<const char*>(X), static_cast<const char*>(R), static_cast<const char*>(gain),
             static_cast<char*>(H), static_cast<char*>(Y), scale, batch, cols, ldx, ldr, ldh, ldy, eps,
-            float(1.0 / double(cols)), gt, yt, batch * cols * int64_t(elem_size(rt)) >= kStreamPast};
+            float(1.0 / double(cols)), int8_t(gt), int8_t(yt), batch * cols * int64_t(elem_size(rt)) >= kStreamPast};
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!R) return xt == UW_F32 ? run_out<kNorm, kF32, kNone>(a, s) : run_out<kNorm, kBf16, kNone>(a, s);
   if (rt == UW_F32) return xt == UW_F32 ? run_out<kNorm, kF32, kF32>(a, s) : run_out<kNorm, kBf16, kF32>(a, s);
@@ -444,7 +445,7 @@ int launch_rmsnorm(const void* X, int64_t batch, int64_t cols, int64_t ldx, int 
 int launch_silu_mul(const void* G, int64_t ldg, const void* U, int64_t ldu, int xt, int64_t batch, int64_t cols,
                     void* Y, int64_t ldy, int yt, float* scale, void* stream) {
   RowArgs a{static_cast<const char*>(G), static_cast<const char*>(U), nullptr, nullptr, static_cast<char*>(Y), scale,
-            batch, cols, ldg, ldu, 0, ldy, 0.f, 0.f, 0, yt, false};
+            batch, cols, ldg, ldu, 0, ldy, 0.f, 0.f, 0, int8_t(yt), false};
   hipStream_t s = static_cast<hipStream_t>(stream);
   return xt == UW_F32 ? run_out<kSilu, kF32, kF32>(a, s) : run_out<kSilu, kBf16, kBf16>(a, s);
 }
