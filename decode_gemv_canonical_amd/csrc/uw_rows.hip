@@ -311,6 +311,20 @@ __global__ __launch_bounds__(NT == kWave ? 256 : NT) void row_kernel(RowArgs a) 
   }
 }
 
+// silu(g) * u without scales has nothing to reduce: a row is spread over
+// workgroups, one chunk per thread (one row of 14336: 3.5 us held in one
+// workgroup, whose compute unit the exponentials keep busy for 1 us, 2.1 here).
+template <int XT>
+__global__ __launch_bounds__(256) void silu_kernel(RowArgs a, unsigned per_row) {
+  constexpr int kXs = XT == kF32 ? 4 : 2;
+  const int64_t row = blockIdx.x / per_row, i = 8 * (int64_t(blockIdx.x % per_row) * 256 + threadIdx.x);
+  if (i >= a.cols) return;
+  const Raw8 xr = load8<XT>(a.x + row * a.ldx * kXs, i, a.cols), ur = load8<XT>(a.r + row * a.ldr * kXs, i, a.cols);
+  float p[8], unused = 0.f;
+  chunk_p<kSilu, XT, XT>(a, xr, ur, Raw8{}, p, nullptr, i, unused);
+  store8(a.y + row * a.ldy * (a.yt == UW_F32 ? 4 : 2), a.yt, i, a.cols, p);
+}
+
 // Rows past the register form's 32768 values: two passes over the row, the
 // second reading h back where it was kept (r may have been overwritten by
 // it) and computing it again where not.
@@ -396,6 +410,23 @@ int run_rows(const RowArgs& a, hipStream_t s) {
   return go(long_row_kernel<OP, XT, RT, I8>, 1024, 1);
 }
 
+template <int XT>
+int run_silu(const RowArgs& a, hipStream_t s) {
+  constexpr int kXs = XT == kF32 ? 4 : 2;
+  const int64_t per_row = (a.cols + 2047) / 2048;
+  const int64_t band = std::max<int64_t>(1, (int64_t(1) << 23) / per_row);  // under 2^32 threads a launch
+  for (int64_t row0 = 0; row0 < a.rows; row0 += band) {
+    RowArgs b = a;
+    b.rows = std::min(band, a.rows - row0);
+    b.x += row0 * a.ldx * kXs;
+    b.r += row0 * a.ldr * kXs;
+    b.y += row0 * a.ldy * int64_t(elem_size(a.yt));
+    hipLaunchKernelGGL(silu_kernel<XT>, dim3(unsigned(b.rows * per_row)), dim3(256), 0, s, b, unsigned(per_row));
+    if (int rc = hip_check(hipGetLastError(), "silu_kernel launch")) return rc;
+  }
+  return UW_OK;
+}
+
 template <int OP, int XT, int RT>
 int run_out(const RowArgs& a, hipStream_t s) {
   return a.yt == UW_I8 ? run_rows<OP, XT, RT, true>(a, s) : run_rows<OP, XT, RT, false>(a, s);
@@ -447,7 +478,8 @@ int launch_silu_mul(const void* G, int64_t ldg, const void* U, int64_t ldu, int 
   RowArgs a{static_cast<const char*>(G), static_cast<const char*>(U), nullptr, nullptr, static_cast<char*>(Y), scale,
             batch, cols, ldg, ldu, 0, ldy, 0.f, 0.f, 0, int8_t(yt), false};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return xt == UW_F32 ? run_out<kSilu, kF32, kF32>(a, s) : run_out<kSilu, kBf16, kBf16>(a, s);
+  if (yt != UW_I8) return xt == UW_F32 ? run_silu<kF32>(a, s) : run_silu<kBf16>(a, s);
+  return xt == UW_F32 ? run_rows<kSilu, kF32, kF32, true>(a, s) : run_rows<kSilu, kBf16, kBf16, true>(a, s);
 }
 
 int launch_i8_quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, int xt, int8_t* Q, int64_t ldq,
