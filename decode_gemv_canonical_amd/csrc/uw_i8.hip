@@ -170,19 +170,22 @@ __device__ __forceinline__ void store_tiles(const I8Args& a, int64_t row0, int64
   }
 }
 
+template <int WI, bool YBF16>
+constexpr int epilogue_bytes = 16 * (16 * WI * (YBF16 ? 2 : 4) + 16);
+
 // Epilogue of a wave's WI x BJ tiles at (n0, bw0), through LDS: 16 activation
 // rows at a time as the wave's 16 WI columns, so that rows go out in runs of
 // 32 WI bytes (bf16) or twice that (without it, 4096 x 4096 x 64 took 19.1 us,
 // with it 13.4); 16 bytes of padding a row spread the writes over the banks.
-// The scales are read before anything is stored.  LDS: bytes a wave has.
+// The scales are read before anything is stored.  out: the wave's place in
+// LDS, epilogue_bytes<WI, YBF16> that nothing else uses any more.
 // NT: Y's rows start at whole lines, which are then stored non-temporally and
 // leave the caches to the operands (4096 x 14336 x 4096: 237 -> 215 us, 2048 x
 // 4096 x 14336: 124 -> 117; a silu that reads the result next loses nothing).
-template <int WI, int BJ, bool YBF16, bool NT, int LDS>
-__device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, int64_t bw0, int wave, int lane,
+template <int WI, int BJ, bool YBF16, bool NT>
+__device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, int64_t bw0, uint32_t out, int lane,
                                                   const i32x4 (&acc)[WI][BJ]) {
   constexpr int kCols = 16 * WI, kSize = YBF16 ? 2 : 4, kPitch = kCols * kSize + 16;
-  static_assert(16 * kPitch <= LDS, "LDS");
   const int r = lane % 16, q = lane / 16;
   float sx[BJ], sw[WI][4], bias[WI][4];
 #pragma unroll
@@ -192,8 +195,6 @@ __device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, i
     load_row4(a.sw, n0 + 16 * i + 4 * q, a.rows, sw[i]);
     if (a.bias) load_row4(a.bias, n0 + 16 * i + 4 * q, a.rows, bias[i]);
   }
-  __syncthreads();  // no wave reads the ring any more
-  const uint32_t out = uint32_t(wave) * (16 * kPitch);
 #pragma unroll
   for (int j = 0; j < BJ; ++j) {
 #pragma unroll
@@ -500,14 +501,19 @@ __global__ __launch_bounds__(64 * KW) void i8_slice_kernel(I8Args a, int nw_tile
 
 // Large batches: both operands of a 128-byte block of k are staged for the
 // whole workgroup, in a ring of ST stages: BW weight rows and BB activation
-// rows, whose WGW x WGB waves each hold a BW / WGW by BB / WGB tile.
-template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16, bool NT>
-__global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
-  constexpr int NW = WGW * WGB, BK = 128;
+// rows, whose WGW x WGB waves each hold a BW / WGW by BB / WGB tile.  KG groups
+// of such waves, each with its own ring, take every KG-th block and add their
+// sums in LDS at the end: where the tiles are few and k is long, a compute
+// unit then works on as many blocks at a time as with KG workgroups.
+template <int BW, int BB, int WGW, int WGB, int ST, int KG, bool YBF16, bool NT>
+__global__ __launch_bounds__(64 * WGW * WGB * KG) void i8_stage_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
+  constexpr int NW = WGW * WGB;
   constexpr int WI = BW / WGW / 16, BJ = BB / WGB / 16;
   constexpr int LW = BW / 8 / NW, LB = BB / 8 / NW;  // 1 KB loads (8 rows) per wave and stage
-  constexpr uint32_t kWBytes = BW * BK, kStage = (BW + BB) * BK;
+  constexpr uint32_t kWBytes = BW * 128, kStage = (BW + BB) * 128;
+  constexpr int kPartial = NW * WI * BJ * 1024;  // a group's sums
   static_assert(BW % (8 * NW) == 0 && BB % (8 * NW) == 0, "whole loads");
+  static_assert((KG - 1) * kPartial + NW * epilogue_bytes<WI, YBF16> <= KG * ST * int(kStage), "LDS");
   // workgroups are dealt to the XCDs round-robin: each XCD takes a run of
   // tiles, 4 activation tiles deep, so that its L2 serves the rereads
   const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
@@ -517,7 +523,8 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   const int deep = min(kDeep, nb_tiles - strip * kDeep);
   const int in = id - strip * kDeep * nw_tiles;
   const int64_t row0 = int64_t(in / deep) * BW, b0 = (int64_t(strip) * kDeep + in % deep) * BB;
-  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int lane = int(threadIdx.x) % kWave, w_all = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int group = w_all / NW, wave = w_all % NW;
   const int lrow = lane / 8, lchunk = (lane % 8) ^ lrow;
   const Staged tw(a.W + row0 * a.ldw, a.rows - row0, a.cols, a.ldw, BW);
   const Staged tx(a.X + b0 * a.ldx, a.batch - b0, a.cols, a.ldx, BB);
@@ -526,10 +533,13 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   for (int u = 0; u < LW; ++u) wvo[u] = tw.row_offset(8 * (u * NW + wave) + lrow, a.ldw) + 16 * lchunk;
 #pragma unroll
   for (int u = 0; u < LB; ++u) xvo[u] = tx.row_offset(8 * (u * NW + wave) + lrow, a.ldx) + 16 * lchunk;
-  const int nkb = int((a.cols + BK - 1) / BK);
-  const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % BK) / 16));
-  auto issue = [&](int kb, int st) {
-    const uint32_t base = uint32_t(st) * kStage, k = uint32_t(kb) * BK, back = kb == nkb - 1 ? over : 0;
+  const int nkb = int((a.cols + 127) / 128);
+  const int n = (nkb - group + KG - 1) / KG;  // this group's blocks; the first group has the most
+  const int over = max(0, 16 * (lchunk - (int(a.cols - 1) % 128) / 16));
+  const uint32_t ring = uint32_t(group) * (ST * kStage);
+  auto issue = [&](int i, int st) {
+    const int kb = i * KG + group;
+    const uint32_t base = ring + uint32_t(st) * kStage, k = uint32_t(kb) * 128, back = kb == nkb - 1 ? over : 0;
 #pragma unroll
     for (int u = 0; u < LW; ++u) stage_load<false>(tw.rsrc, wvo[u] - back, k, base + uint32_t(u * NW + wave) * 1024);
 #pragma unroll
@@ -538,7 +548,7 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   };
   const int r = lane % 16, q = lane / 16;
   const int ww = wave / WGB, wb = wave % WGB;
-  const uint32_t arow = uint32_t(ww * WI * 16 + r) * BK, xrow = kWBytes + uint32_t(wb * BJ * 16 + r) * BK;
+  const uint32_t arow = uint32_t(ww * WI * 16 + r) * 128, xrow = kWBytes + uint32_t(wb * BJ * 16 + r) * 128;
   i32x4 acc[WI][BJ];
 #pragma unroll
   for (int i = 0; i < WI; ++i)
@@ -546,19 +556,19 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
     for (int j = 0; j < BJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
   auto multiply = [&](uint32_t base, bool tail) {
 #pragma unroll
-    for (int s = 0; s < BK / 64; ++s) {
+    for (int s = 0; s < 2; ++s) {
       const uint32_t ch = uint32_t(((4 * s + q) ^ (r & 7)) * 16);
       u32x4 x[BJ];
 #pragma unroll
-      for (int j = 0; j < BJ; ++j) x[j] = __builtin_bit_cast(u32x4, ld128(base + xrow + uint32_t(j) * (16 * BK) + ch));
+      for (int j = 0; j < BJ; ++j) x[j] = __builtin_bit_cast(u32x4, ld128(base + xrow + uint32_t(j) * 2048 + ch));
       if (tail) {
-        const u32x4 m = tail_mask(int(a.cols - int64_t(nkb - 1) * BK) - 16 * (4 * s + q));
+        const u32x4 m = tail_mask(int(a.cols - int64_t(nkb - 1) * 128) - 16 * (4 * s + q));
 #pragma unroll
         for (int j = 0; j < BJ; ++j) x[j] &= m;
       }
 #pragma unroll
       for (int i = 0; i < WI; ++i) {
-        const u32x4 w = __builtin_bit_cast(u32x4, ld128(base + arow + uint32_t(i) * (16 * BK) + ch));
+        const u32x4 w = __builtin_bit_cast(u32x4, ld128(base + arow + uint32_t(i) * 2048 + ch));
 #pragma unroll
         for (int j = 0; j < BJ; ++j) acc[i][j] = mfma_i8(w, x[j], acc[i][j]);
       }
@@ -566,18 +576,41 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_stage_kernel(I8Args a, int 
   };
 #pragma unroll
   for (int i = 0; i < ST - 1; ++i)
-    if (i < nkb) issue(i, i);
+    if (i < n) issue(i, i);
   int st = 0;
-  auto step = [&](int kb, bool tail) {
-    wait_ring<LW + LB, ST - 2>(nkb - 1 - kb);  // this wave's loads of block kb have landed
-    lds_barrier();                             // every wave's have; block kb - 1 is no longer read
-    if (kb + ST - 1 < nkb) issue(kb + ST - 1, st == 0 ? ST - 1 : st - 1);
-    multiply(uint32_t(st) * kStage, tail);
+  // every wave takes part in the barriers of the first group's n blocks
+  const int steps = (nkb + KG - 1) / KG;
+  auto step = [&](int i, bool last) {
+    if (i < n) wait_ring<LW + LB, ST - 2>(n - 1 - i);  // this wave's loads of block i have landed
+    lds_barrier();                                     // every wave's have; block i - 1 is no longer read
+    if (i + ST - 1 < n) issue(i + ST - 1, st == 0 ? ST - 1 : st - 1);
+    if (!last || i < n) multiply(ring + uint32_t(st) * kStage, last && a.cols % 128 != 0 && i * KG + group == nkb - 1);
     st = st + 1 == ST ? 0 : st + 1;
   };
-  for (int kb = 0; kb < nkb - 1; ++kb) step(kb, false);
-  step(nkb - 1, a.cols % BK != 0);
-  store_through_lds<WI, BJ, YBF16, NT, int(ST * kStage) / NW>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16, wave, lane, acc);
+  for (int i = 0; i < steps - 1; ++i) step(i, false);  // every group has these
+  step(steps - 1, true);
+  __syncthreads();  // no wave reads the rings any more
+  if (KG > 1) {
+    const uint32_t mine = uint32_t(wave) * (WI * BJ * 1024) + 16 * lane;
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < WI; ++i)
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+          st128(uint32_t((group - 1) * kPartial) + mine + uint32_t(i * BJ + j) * 1024, __builtin_bit_cast(uint4, acc[i][j]));
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < WI; ++i)
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+          acc[i][j] += __builtin_bit_cast(i32x4, ld128(uint32_t(g * kPartial) + mine + uint32_t(i * BJ + j) * 1024));
+  }
+  store_through_lds<WI, BJ, YBF16, NT>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16,
+                                       uint32_t((KG - 1) * kPartial + wave * epilogue_bytes<WI, YBF16>), lane, acc);
 }
 
 // The largest batches.  As above with the operands of the next step read
@@ -683,7 +716,10 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_wide_kernel(I8Args a, int n
     mask(t + 1, f1);
     step(t + 1, f1, f0, false);
   }
-  store_through_lds<WI, BJ, YBF16, NT, int(ST * kStep) / NW>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16, wave, lane, acc);
+  static_assert(NW * epilogue_bytes<WI, YBF16> <= ST * int(kStep), "LDS");
+  __syncthreads();  // no wave reads the ring any more
+  store_through_lds<WI, BJ, YBF16, NT>(a, row0 + ww * 16 * WI, b0 + wb * BJ * 16,
+                                       uint32_t(wave) * epilogue_bytes<WI, YBF16>, lane, acc);
 }
 
 template <int RB, int TB>
@@ -703,18 +739,18 @@ bool whole_lines(const I8Args& a, int yt) {
   return reinterpret_cast<uintptr_t>(a.Y) % 128 == 0 && a.ldy * int64_t(elem_size(yt)) % 128 == 0;
 }
 
-template <int BW, int BB, int WGW, int WGB, int ST>
+template <int BW, int BB, int WGW, int WGB, int ST, int KG = 1>
 int run_stage(const I8Args& a, int yt, hipStream_t s) {
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
   const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
-  constexpr int kThreads = 64 * WGW * WGB;
+  constexpr int kThreads = 64 * WGW * WGB * KG;
   if (per_xcd * kXcds * kThreads >= int64_t(1) << 32)
     return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
   auto kern = whole_lines(a, yt)
-                  ? (yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, true, true> : i8_stage_kernel<BW, BB, WGW, WGB, ST, false, true>)
-                  : (yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, true, false> : i8_stage_kernel<BW, BB, WGW, WGB, ST, false, false>);
+                  ? (yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, KG, true, true> : i8_stage_kernel<BW, BB, WGW, WGB, ST, KG, false, true>)
+                  : (yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, KG, true, false> : i8_stage_kernel<BW, BB, WGW, WGB, ST, KG, false, false>);
   allow_full_lds(kern);
-  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(ST) * (BW + BB) * 128, s, a, int(nw),
+  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(KG) * ST * (BW + BB) * 128, s, a, int(nw),
                      int(nb), int(per_xcd));
   return hip_check(hipGetLastError(), "i8_stage_kernel launch");
 }
@@ -766,22 +802,22 @@ constexpr I8Shape kShapeList[] = {
     {16, 16, kDirect, 1, 0, 0, 0},
     {16, 32, kDirect, 1, 0, 0, 0},
     {32, 32, kDirect, 1, 0, 0, 0},
-    {16, 16, kSlice, 2, 1.52f, 0.061f, 0.054f},
-    {64, 16, kSlice, 2, 1.77f, 0.165f, 0.141f},  // 4 waves
-    {64, 16, kSlice, 1, 1.77f, 0.165f, 0.141f},  // 8 waves: see pick_shape
-    {16, 32, kSlice, 1, 1.61f, 0.080f, 0.077f},
-    {32, 32, kSlice, 2, 1.81f, 0.120f, 0.115f},
-    {64, 32, kSlice, 1, 2.57f, 0.199f, 0.f},
-    {64, 64, kSlice, 1, 4.06f, 0.267f, 0.189f},
-    {32, 32, kStage, 5, 1.47f, 0.210f, 0.138f},
-    {32, 64, kStage, 3, 1.55f, 0.235f, 0.196f},
-    {64, 64, kStage, 4, 1.58f, 0.484f, 0.300f},  // 2 slots
-    {64, 64, kStage, 2, 1.76f, 0.327f, 0.304f},  // 4 slots
-    {64, 128, kStage, 2, 2.48f, 0.442f, 0.437f},
-    {128, 128, kStage, 2, 3.85f, 0.780f, 0.590f},  // 2 slots
-    {128, 128, kStage, 1, 3.85f, 0.700f, 0.570f},  // 3 slots
-    {256, 128, kStage, 1, 4.27f, 1.039f, 0.989f},
-    {256, 256, kStage, 1, 7.87f, 1.333f, 1.883f},
+    {16, 16, kSlice, 2, 1.55f, 0.052f, 0.056f},
+    {64, 16, kSlice, 2, 1.75f, 0.157f, 0.145f},  // 4 waves
+    {64, 16, kSlice, 1, 1.75f, 0.157f, 0.145f},  // 8 waves: see pick_shape
+    {16, 32, kSlice, 1, 1.58f, 0.083f, 0.068f},
+    {32, 32, kSlice, 2, 1.79f, 0.119f, 0.118f},
+    {64, 32, kSlice, 1, 2.54f, 0.198f, 0.107f},
+    {32, 32, kStage, 5, 1.53f, 0.219f, 0.138f},
+    {32, 64, kStage, 3, 1.70f, 0.252f, 0.191f},
+    {64, 64, kStage, 4, 1.65f, 0.490f, 0.295f},
+    {64, 64, kStage, 1, 2.32f, 0.228f, 0.236f},    // 3 groups of waves
+    {64, 128, kStage, 1, 2.86f, 0.347f, 0.379f},   // 2 groups
+    {128, 128, kStage, 2, 3.86f, 0.756f, 0.597f},  // 2 slots
+    {128, 128, kStage, 1, 3.80f, 0.623f, 0.517f},  // 3 slots
+    {128, 128, kStage, 1, 4.05f, 0.560f, 0.560f},  // 2 groups
+    {256, 128, kStage, 1, 4.48f, 1.040f, 0.941f},
+    {256, 256, kStage, 1, 8.17f, 1.313f, 1.729f},
 };
 constexpr int kShapes = int(sizeof(kShapeList) / sizeof(kShapeList[0]));
 constexpr int kFirstStaged = 4, kTall4 = 5, kTall8 = 6;
@@ -799,7 +835,7 @@ bool stage_ok(const I8Args& a) {
 // needs `shared` per block and workgroup it holds; and the operands' bytes come
 // at 5.4 TB/s.  The three limits of the loop add as fourth powers (the largest
 // rules, a near second counts).
-// The constants are fits to every shape's times on 520 sizes drawn over 1..4096
+// The constants are fits to every shape's times on 687 sizes drawn over 1..4096
 // x 64..28672 x 64..14336 (and the MLP's), each on 3 to 8 rotated operand sets;
 // the shapes so chosen take 1.03 of the best shape's time in the mean, against
 // 1.20 for the largest tile that gives 160 workgroups.
@@ -866,14 +902,14 @@ int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, con
     case 7: return run_slice<16, 32, 4, 4>(a, yt, s);
     case 8: return run_slice<32, 32, 4, 2>(a, yt, s);
     case 9: return run_slice<64, 32, 4, 2>(a, yt, s);
-    case 10: return run_slice<64, 64, 4, 2>(a, yt, s);
-    case 11: return run_stage<32, 32, 2, 2, 4>(a, yt, s);
-    case 12: return run_stage<32, 64, 2, 2, 4>(a, yt, s);
-    case 13: return run_stage<64, 64, 2, 2, 2>(a, yt, s);
-    case 14: return run_stage<64, 64, 2, 2, 4>(a, yt, s);
-    case 15: return run_stage<64, 128, 2, 2, 3>(a, yt, s);
-    case 16: return run_stage<128, 128, 2, 2, 2>(a, yt, s);
-    case 17: return run_stage<128, 128, 2, 2, 3>(a, yt, s);
+    case 10: return run_stage<32, 32, 2, 2, 4>(a, yt, s);
+    case 11: return run_stage<32, 64, 2, 2, 4>(a, yt, s);
+    case 12: return run_stage<64, 64, 2, 2, 2>(a, yt, s);
+    case 13: return run_stage<64, 64, 2, 2, 3, 3>(a, yt, s);
+    case 14: return run_stage<64, 128, 2, 2, 3, 2>(a, yt, s);
+    case 15: return run_stage<128, 128, 2, 2, 2>(a, yt, s);
+    case 16: return run_stage<128, 128, 2, 2, 3>(a, yt, s);
+    case 17: return run_stage<128, 128, 2, 2, 2, 2>(a, yt, s);
     case 18: return run_stage<256, 128, 4, 2, 3>(a, yt, s);
     default: return run_wide<256, 256, 2, 4, 4>(a, yt, s);
   }
