@@ -381,8 +381,7 @@ def test_gemm_shapes(b, rows, cols, shape):
 @pytest.mark.parametrize("ks", range(1, 9))
 @pytest.mark.parametrize("cols", [100, 256, 1500, 4096])
 def test_gemm_direct_waves(ks, cols):
-    for shape in (1, 2, 3):
-        run_gemm(20, 48, cols, "f32", shape=shape, ks=ks)
+    run_gemm(20, 48, cols, "f32", shape=1, ks=ks)
 
 
 @pytest.mark.parametrize("shape", range(4, uw.uw_i8_gemm_shape_count()))
@@ -404,6 +403,13 @@ def test_gemm_unaligned_operands(b, pad, shift):
     for cols in (333, 256, 1025):
         run_gemm(b, 130, cols, "f32", pad=pad, shift=shift, bias=True)
         run_gemm(b, 37, cols, "bf16", pad=pad, shift=shift, ypad=3)
+        for shape in range(1, 4):
+            run_gemm(b, 130, cols, "f32", pad=pad, shift=shift, shape=shape)
+
+
+def test_gemm_unaligned_large():
+    run_gemm(2100, 2100, 130, "bf16", pad=0, shift=3, bias=True)
+    run_gemm(300, 1000, 4100, "f32", pad=0)
 
 
 def test_gemm_mlp_sizes():
