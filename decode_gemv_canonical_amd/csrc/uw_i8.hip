@@ -554,7 +554,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i8_stage_kernel(I8Args a,
 // into the other of two LDS buffers, one block ahead of the products.  Rows
 // may start at any byte; nothing outside a row is read.
 // Bound by the loads: off a 16-byte boundary they take a lane per cycle, 0.5 us
-// per 16 KB and compute unit (4096 x 14336 x 4099: 484 us, against 5865 for 32
+// per 16 KB and compute unit (4096 x 14336 x 4099: 435 us, against 5865 for 32
 // x 32 tiles in i8_direct_kernel; aligned rows: 209).  Eight waves beat four
 // (64 x 14336 x 4099: 19.9 us against 23.2); two to four blocks ahead changed
 // nothing, nor did words loaded on a 4-byte boundary and shifted.
@@ -747,10 +747,17 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_wide_kernel(I8Args a, int n
                                        uint32_t(wave) * epilogue_bytes<WI, YBF16>, lane, acc);
 }
 
+// A launch holds fewer than 2^32 threads: nw x nb tiles, rounded up to a
+// multiple of kXcds.  In double: sizes below 2^40 make products past 64 bits.
+int check_launch(int64_t nw, int64_t nb, int threads) {
+  if ((double(nw) * double(nb) + kXcds) * threads < 4294967296.0) return UW_OK;
+  return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
+}
+
 int run_direct(const I8Args& a, int yt, int ks, hipStream_t s) {
   const int64_t n_groups = (a.rows + 15) / 16, ny = (a.batch + 15) / 16;
+  if (int rc = check_launch((n_groups + kXcds - 1) / kXcds * kXcds, ny, ks * kWave)) return rc;
   const int64_t grid = (n_groups + kXcds - 1) / kXcds * kXcds * ny;
-  if (grid * ks * kWave >= int64_t(1) << 32) return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
   auto kern = yt == UW_BF16 ? i8_direct_kernel<true> : i8_direct_kernel<false>;
   hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(ks * kWave), size_t(ks) * 1024, s, a, int(n_groups), int(ny), ks);
   return hip_check(hipGetLastError(), "i8_direct_kernel launch");
@@ -764,10 +771,9 @@ bool whole_lines(const I8Args& a, int yt) {
 template <int BW, int BB, int WGW, int WGB, int ST, int KG = 1>
 int run_stage(const I8Args& a, int yt, hipStream_t s) {
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
-  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   constexpr int kThreads = 64 * WGW * WGB * KG;
-  if (per_xcd * kXcds * kThreads >= int64_t(1) << 32)
-    return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
+  if (int rc = check_launch(nw, nb, kThreads)) return rc;
+  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   auto kern = whole_lines(a, yt)
                   ? (yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, KG, true, true> : i8_stage_kernel<BW, BB, WGW, WGB, ST, KG, false, true>)
                   : (yt == UW_BF16 ? i8_stage_kernel<BW, BB, WGW, WGB, ST, KG, true, false> : i8_stage_kernel<BW, BB, WGW, WGB, ST, KG, false, false>);
@@ -780,8 +786,8 @@ int run_stage(const I8Args& a, int yt, hipStream_t s) {
 template <int BW, int BB, int KW, int ST>
 int run_slice(const I8Args& a, int yt, hipStream_t s) {
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
+  if (int rc = check_launch((nw + kXcds - 1) / kXcds * kXcds, nb, KW * kWave)) return rc;
   const int64_t grid = (nw + kXcds - 1) / kXcds * kXcds * nb;
-  if (grid * KW * kWave >= int64_t(1) << 32) return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
   // weights that one workgroup reads once pass the caches by
   auto kern = nb == 1 ? (yt == UW_BF16 ? i8_slice_kernel<BW, BB, KW, ST, true, true> : i8_slice_kernel<BW, BB, KW, ST, true, false>)
                       : (yt == UW_BF16 ? i8_slice_kernel<BW, BB, KW, ST, false, true> : i8_slice_kernel<BW, BB, KW, ST, false, false>);
@@ -795,10 +801,9 @@ int run_slice(const I8Args& a, int yt, hipStream_t s) {
 template <int BW, int BB, int WGW, int WGB>
 int run_loose(const I8Args& a, int yt, hipStream_t s) {
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
-  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   constexpr int kThreads = 64 * WGW * WGB;
-  if (per_xcd * kXcds * kThreads >= int64_t(1) << 32)
-    return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
+  if (int rc = check_launch(nw, nb, kThreads)) return rc;
+  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   auto kern = yt == UW_BF16 ? i8_loose_kernel<BW, BB, WGW, WGB, true> : i8_loose_kernel<BW, BB, WGW, WGB, false>;
   allow_full_lds(kern);
   hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), size_t(2) * (BW + BB) * 128, s, a, int(nw),
@@ -809,9 +814,9 @@ int run_loose(const I8Args& a, int yt, hipStream_t s) {
 template <int BW, int BB, int WGW, int WGB, int ST>
 int run_wide(const I8Args& a, int yt, hipStream_t s) {
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
-  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   constexpr int kThreads = 64 * WGW * WGB;
-  if (per_xcd * kXcds * kThreads >= int64_t(1) << 32) return fail(UW_ERR_UNSUPPORTED, "uw_i8_gemm: too many tiles for one launch");
+  if (int rc = check_launch(nw, nb, kThreads)) return rc;
+  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
   auto kern = whole_lines(a, yt)
                   ? (yt == UW_BF16 ? i8_wide_kernel<BW, BB, WGW, WGB, ST, true, true> : i8_wide_kernel<BW, BB, WGW, WGB, ST, false, true>)
                   : (yt == UW_BF16 ? i8_wide_kernel<BW, BB, WGW, WGB, ST, true, false> : i8_wide_kernel<BW, BB, WGW, WGB, ST, false, false>);
@@ -870,7 +875,7 @@ bool stage_ok(const I8Args& a) {
 // needs `shared` per block and workgroup it holds; and the operands' bytes come
 // at 5.4 TB/s.  The three limits of the loop add as fourth powers (the largest
 // rules, a near second counts).
-// The constants are fits to every shape's times on 687 sizes drawn over 1..4096
+// The constants are fits to the shapes' times on 687 sizes drawn over 1..4096
 // x 64..28672 x 64..14336 (and the MLP's), each on 3 to 8 rotated operand sets;
 // the shapes so chosen take 1.03 of the best shape's time in the mean, against
 // 1.20 for the largest tile that gives 160 workgroups.

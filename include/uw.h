@@ -655,7 +655,7 @@ int uw_i8_dequantize(const int8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq,
  *         nearest even), row stride ldy >= rows.
  *   1 <= cols <= 131071 (the sum stays inside 32 bits for every input).
  * Operands that are not 16-byte aligned, or whose strides are no multiples of
- * 16, run on shapes that read them straight from global memory: slower.
+ * 16, run on other shapes: half as fast at large batches, less at small ones.
  * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (cols > 131071, more tiles than
  *         a launch holds), UW_ERR_HIP.
  */
@@ -666,9 +666,10 @@ int uw_i8_gemm(const int8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, const
 /*
  * uw_i8_gemm_shaped (device) - uw_i8_gemm with a given shape: shape in
  * [1, uw_i8_gemm_shape_count()) picks the weight and batch rows a workgroup
- * holds and how the operands reach the matrix cores: 1..3 straight from global
- * memory (ks = the waves that split k, 1..8; 0 = 8), the others through LDS
- * (ks does not apply).
+ * holds and how the operands reach the matrix cores: 1 straight from global
+ * memory (ks = the waves that split k, 1..8; 0 = one per 256 bytes of k, at
+ * most 8), 2 and 3 through registers into LDS, the others by loads straight
+ * into LDS (ks applies to none of these).
  * Errors: as uw_i8_gemm; UW_ERR_INVALID for an unknown shape or ks,
  *         UW_ERR_UNSUPPORTED for a staged shape on operands that are not
  *         16-byte aligned with strides that are multiples of 16 (below 2^22).

@@ -132,6 +132,14 @@ def test_gemm_shaped_refuses():
         assert gemm(shape=n - 1, **k) == UNSUP
 
 
+def test_gemm_refuses_more_tiles_than_a_launch_holds():
+    big = dict(rows=1 << 39, batch=1 << 39, ldy=1 << 39)
+    assert gemm(**big) == UNSUP
+    assert gemm(W=P + 1, **big) == UNSUP
+    for shape in range(1, uw.uw_i8_gemm_shape_count()):
+        assert gemm(shape=shape, **big) == UNSUP
+
+
 def test_binding_refuses_host_tensors():
     x, q, s = torch.zeros(2, 64), torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2)
     with pytest.raises(ValueError):
