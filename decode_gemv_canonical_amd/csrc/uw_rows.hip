@@ -170,7 +170,7 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
     s_sum[wave] = sum;
     s_top[wave] = top;
   }
-  __syncthreads();
+  lds_barrier();  // h's stores stay in flight (1111 x 8192, fp32 stream: 24.7 -> 24.3 us)
   sum = s_sum[0];
   top = s_top[0];
 #pragma unroll
