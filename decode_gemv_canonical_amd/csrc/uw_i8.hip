@@ -61,6 +61,15 @@ __device__ __forceinline__ u32x4 load16_tail(const int8_t* p, int64_t left) {
   return v;
 }
 
+// A sum as it goes out: rounded to fp32, scaled, the bias added, three
+// roundings in every kernel (left to itself the compiler makes the last two one
+// in some of them, and a result would hang on the shape that runs).
+__device__ __forceinline__ float scaled(int sum, float scale, bool biased, float bias) {
+#pragma clang fp contract(off)
+  const float v = float(sum) * scale;
+  return biased ? v + bias : v;
+}
+
 // Four consecutive values of row b of Y, weight rows n .. n + 3 (n < rows).
 template <bool YBF16>
 __device__ __forceinline__ void store_row4(const I8Args& a, int64_t b, int64_t n, const float (&v)[4]) {
@@ -131,8 +140,7 @@ __device__ __forceinline__ void store_y4(const I8Args& a, int64_t b, int64_t n, 
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int64_t at = std::min<int64_t>(n + e, a.rows - 1);
-    v[e] = float(acc[e]) * (sx * a.sw[at]);
-    if (a.bias) v[e] += a.bias[at];
+    v[e] = scaled(acc[e], sx * a.sw[at], a.bias, a.bias ? a.bias[at] : 0.f);
   }
   store_row4<YBF16>(a, b, n, v);
 }
@@ -154,7 +162,7 @@ __device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, i
                                                   const i32x4 (&acc)[WI][BJ]) {
   constexpr int kCols = 16 * WI, kSize = YBF16 ? 2 : 4, kPitch = kCols * kSize + 16;
   const int r = lane % 16, q = lane / 16;
-  float sx[BJ], sw[WI][4], bias[WI][4];
+  float sx[BJ], sw[WI][4], bias[WI][4] = {};
 #pragma unroll
   for (int j = 0; j < BJ; ++j) sx[j] = a.sx[std::min<int64_t>(bw0 + 16 * j + r, a.batch - 1)];
 #pragma unroll
@@ -168,10 +176,7 @@ __device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, i
     for (int i = 0; i < WI; ++i) {
       float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = float(acc[i][j][e]) * (sx[j] * sw[i][e]);
-        if (a.bias) v[e] += bias[i][e];
-      }
+      for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][e], sx[j] * sw[i][e], a.bias, bias[i][e]);
       const uint32_t dst = out + uint32_t(r) * kPitch + uint32_t(16 * i + 4 * q) * kSize;
       if (YBF16) st64(dst, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
       else st128(dst, uint4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])});

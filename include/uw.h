@@ -647,7 +647,8 @@ int uw_i8_dequantize(const int8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq,
  * uw_i8_gemm (device) - Y[b, n] = xs[b] * ws[n] * sum_k X[b, k] W[n, k]
  * (+ bias[n]) on the matrix cores.  The sum is exact (32-bit integers), so
  * results do not depend on the shape run; it is rounded to fp32, multiplied by
- * the product of the two scales (formed first, in fp32), and the bias added.
+ * the product of the two scales (formed first, in fp32), and the bias added,
+ * each step rounded to fp32.
  *   d_W   rows x cols integers, row stride ldw >= cols; d_ws rows fp32 scales.
  *   d_X   batch x cols integers, row stride ldx >= cols; d_xs batch scales.
  *   d_bias  rows fp32 values, or NULL.

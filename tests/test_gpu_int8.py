@@ -639,3 +639,34 @@ def test_refusals_name_the_operand():
     uw.uw_rmsnorm(x, None, y, stream=raw)
     uw.uw_rmsnorm(x[:0], None, y[:0])  # no rows: nothing to do
     uw.uw_i8_gemm(q, s, q[:0], s[:0], torch.zeros(0, 4, device=DEV))
+
+
+# -- defined to the bit ----------------------------------------------------------
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("b,rows,cols", [(1, 64, 256), (33, 100, 300), (70, 257, 1025)])
+def test_gemm_bias_to_the_bit_in_every_shape(b, rows, cols, out):
+    """The sum, the scaling and the bias are rounded one after the other, in fp32, whichever shape runs."""
+    W, ws = rand_i8(rows, cols, 11)
+    X, xs = rand_i8(b, cols, 12)
+    bias = torch.randn(rows, device=DEV, generator=torch.Generator(device=DEV).manual_seed(13)) * 1000
+    sums = (X.cpu().numpy().astype(np.int64) @ W.cpu().numpy().astype(np.int64).T).astype(np.float32)
+    step = xs.cpu().numpy()[:, None] * ws.cpu().numpy()[None, :]
+    y = sums * step + bias.cpu().numpy()[None, :]
+    assert y.dtype == np.float32
+    want = torch.from_numpy(y).to(DT[out])
+    for shape in range(uw.uw_i8_gemm_shape_count()):
+        for ypad in (0, 5):  # whole lines or not
+            Y, _ = inside(b, rows, DT[out], ypad + (-rows % 64 if ypad == 0 else 0))
+            if shape:
+                uw.uw_i8_gemm_shaped(W, ws, X, xs, Y, shape, bias=bias)
+            else:
+                uw.uw_i8_gemm(W, ws, X, xs, Y, bias=bias)
+            got = Y.cpu()
+            assert torch.equal(got, want), f"shape {shape}: {(got != want).sum()} of {want.numel()} differ"
+    # operands off 16-byte boundaries
+    W1, _ = inside(rows, cols, torch.int8, 1, 3)
+    W1.copy_(W)
+    Y = torch.empty(b, rows, dtype=DT[out], device=DEV)
+    uw.uw_i8_gemm(W1, ws, X, xs, Y, bias=bias)
+    assert torch.equal(Y.cpu(), want)
