@@ -584,8 +584,11 @@ int uw_sched_gemm(uw_sched* s, int slot, const void* d_X, int64_t batch, int64_t
  * different streams do not disturb each other.  Rows start at any multiple of
  * the element size (strides in elements; a single row has none).  Nothing
  * outside the rows given is written, and nothing outside the 16-byte words
- * that hold them is read.  Outputs may be inputs only where it says so; other
- * overlaps are not allowed.  batch (or rows) == 0 is a no-op.
+ * that hold them is read.  An output may be an input only where it says so,
+ * element for element (same address, type and stride); any other overlap of an
+ * output with an input or another output is refused (UW_ERR_INVALID).  Rows of
+ * one operand may lie between rows of another.  batch (or rows) == 0 is a
+ * no-op.
  */
 
 /*
@@ -596,15 +599,14 @@ int uw_sched_gemm(uw_sched* s, int slot, const void* d_X, int64_t batch, int64_t
  *   d_R      the residual, rows of rt (UW_F32 or UW_BF16), stride ldr, or
  *            NULL (h = x).  h is rounded to rt before it is squared.
  *   d_H      receives h in rt, stride ldh; NULL: not kept.  May be d_R
- *            itself (the stream updated in place, ldh == ldr) or d_X (where
- *            rt == xt and ldh == ldx).  Needs d_R.
+ *            itself (the stream updated in place) or d_X.  Needs d_R.
  *   d_gain   cols elements of gt (UW_F32 or UW_BF16), or NULL (all ones).
  *   eps      positive and finite.
  *   d_Y      receives y in yt, stride ldy >= cols: UW_F32, UW_BF16 (nearest
  *            even), or UW_I8 with d_scale (batch fp32 values; else ignored,
  *            may be NULL): there p = h * gain and the scale is
- *            s / sqrt(mean(h^2) + eps).  May be d_X itself (yt == xt,
- *            ldy == ldx) where d_H is not d_X too.
+ *            s / sqrt(mean(h^2) + eps).  May be d_X or d_R itself where d_H
+ *            is not the same too.
  * A row whose squares sum past the fp32 range comes out as zeros.
  * Errors: UW_ERR_INVALID, UW_ERR_HIP.
  */
@@ -617,7 +619,7 @@ int uw_rmsnorm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int xt
  * arithmetic: a gated MLP's activation.  d_G and d_U hold batch rows of cols
  * elements of xt with strides ldg and ldu (halves of one product's rows, for
  * instance); d_Y, yt, ldy and d_scale as for uw_rmsnorm, and d_Y may be d_G
- * or d_U itself (same type and stride).
+ * or d_U itself.
  * Errors: UW_ERR_INVALID, UW_ERR_HIP.
  */
 int uw_silu_mul(const void* d_G, int64_t ldg, const void* d_U, int64_t ldu, int xt, int64_t batch, int64_t cols,

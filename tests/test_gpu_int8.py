@@ -670,3 +670,57 @@ def test_gemm_bias_to_the_bit_in_every_shape(b, rows, cols, out):
     Y = torch.empty(b, rows, dtype=DT[out], device=DEV)
     uw.uw_i8_gemm(W1, ws, X, xs, Y, bias=bias)
     assert torch.equal(Y.cpu(), want)
+
+
+# -- outputs over inputs -----------------------------------------------------------
+
+@pytest.mark.parametrize("cols", [96, 4096, 34000])
+def test_norm_over_the_residual(cols):
+    """y into the residual, h not kept or kept elsewhere."""
+    for dt in (torch.bfloat16, torch.float32):
+        X, R = rand(3, cols, dt, 1, pad=8), rand(3, cols, dt, 2, pad=3)
+        Y0, H0 = torch.empty(3, cols, dtype=dt, device=DEV), torch.empty(3, cols, dtype=dt, device=DEV)
+        uw.uw_rmsnorm(X, None, Y0, residual=R, residual_out=H0)
+        for keep in (None, "apart", "x"):
+            R1, _ = inside(3, cols, dt, 3)
+            R1.copy_(R)
+            X1 = X.clone()
+            H = None if keep is None else X1 if keep == "x" else torch.empty_like(H0)
+            uw.uw_rmsnorm(X1, None, R1, residual=R1, residual_out=H)
+            assert torch.equal(R1, Y0) and (H is None or torch.equal(H, H0))
+
+
+def test_rows_between_the_rows_of_another_operand():
+    GU = rand(5, 2 * 700, torch.bfloat16, 4)
+    G, V = GU[:, :700], GU[:, 700:]
+    Y = torch.empty(5, 700, dtype=torch.bfloat16, device=DEV)
+    uw.uw_silu_mul(G, V, Y)
+    keep = V.clone()
+    uw.uw_silu_mul(G, V, G)  # the gate's half in place, the other half beside it
+    assert torch.equal(G, Y) and torch.equal(V, keep)
+    # every second row read, every fourth written
+    B = rand(16, 300, torch.float32, 5)
+    X, Y = B[0:8:2], B[1:16:4]
+    want = torch.empty(4, 300, device=DEV)
+    uw.uw_rmsnorm(X.clone(), None, want)
+    rest = B[2:16:4].clone()
+    uw.uw_rmsnorm(X, None, Y)
+    assert torch.equal(Y, want) and torch.equal(B[2:16:4], rest)
+
+
+def test_overlaps_are_refused():
+    x = torch.zeros(4, 64, device=DEV)
+    s = torch.zeros(4, device=DEV)
+    q = x.view(torch.int8)  # rows of 256 integers over x
+    for call in (
+        lambda: uw.uw_rmsnorm(x[:3], None, x[1:]),
+        lambda: uw.uw_rmsnorm(x.clone(), None, q[:, :64], scale=s, residual=x),
+        lambda: uw.uw_rmsnorm(x.clone(), None, torch.zeros_like(x), residual=x[:, :64], residual_out=x.view(-1)[1:].as_strided((4, 64), (63, 1))),
+        lambda: uw.uw_silu_mul(x[:, :32], x[:, 32:], x[:, 16:48]),
+        lambda: uw.uw_i8_quantize(x, q[:, :64], s),
+        lambda: uw.uw_i8_dequantize(q[:, :64], s, x),
+        lambda: uw.uw_i8_gemm(q[:, :64], s, torch.zeros(4, 64, dtype=torch.int8, device=DEV), s.clone(), x[:, :4]),
+    ):
+        with pytest.raises((uw.UwError, ValueError)):
+            call()
+    assert not x.any()

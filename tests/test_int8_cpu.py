@@ -154,3 +154,79 @@ def test_binding_refuses_host_tensors():
         uw.uw_i8_gemm(q, s, q, s, torch.zeros(2, 2))
     with pytest.raises(ValueError):
         uw.Int8Matrix(q, s)
+
+
+# -- overlaps ------------------------------------------------------------------
+# norm() above: 4 rows of 64 bf16, X and R at P, H at P + 4096, Y at P + 8192
+
+@pytest.mark.parametrize("k", [
+    {"H": P, "ldh": 72}, {"H": P, "rt": F32, "R": P + 8192, "Y": P + 65536},   # in place with another stride or type
+    {"H": P + 2}, {"H": P + 128}, {"H": P - 128},                              # one element, one row on
+    {"R": P + 65536, "Y": P, "ldy": 65}, {"R": P + 65536, "Y": P, "yt": F32}, {"Y": P + 64}, {"Y": P - 4, "yt": F32},
+    {"Y": P + 4096 + 510}, {"Y": P + 4096 - 510},                              # the last or first element of H
+    {"R": P + 65536, "Y": P + 65536, "yt": I8, "scale": P + 16384},            # integers over the residual
+    {"yt": I8, "scale": P + 8}, {"yt": I8, "scale": P + 8192 + 252}, {"yt": I8, "scale": P + 4096},
+    {"gain": P + 8192 + 384, "Y": P + 8192}, {"gain": P + 4096}, {"H": None, "gain": P + 8192},
+])
+def test_rmsnorm_refuses_overlaps(k):
+    assert norm(**k) == INV
+    assert "overlap" in uw.uw_last_error()
+
+
+@pytest.mark.parametrize("k", [
+    {"Y": P + 2}, {"Y": P, "ldy": 66}, {"Y": P, "yt": F32}, {"Y": P, "yt": I8, "scale": P + 8192},
+    {"U": P + 4096, "Y": P + 4096 - 510}, {"Y": P + 4096, "yt": I8, "scale": P + 4096 + 252}, {"G": P + 2, "Y": P},
+    {"ldg": 128, "ldu": 128, "U": P + 128, "Y": P + 64, "ldy": 128},           # half of each half
+    {"Y": P + 4096, "yt": I8, "scale": P},
+])
+def test_silu_mul_refuses_overlaps(k):
+    assert silu(**k) == INV
+    assert "overlap" in uw.uw_last_error()
+
+
+@pytest.mark.parametrize("k", [{"scale": P + 8192}, {"Q": P + 8192}, {"Q": P + 511, "scale": P + 8192},
+                               {"Q": P + 8192, "scale": P + 8192 + 255}])
+def test_quantize_refuses_overlaps(k):
+    k = {name: at if name != "scale" else at // 4 * 4 for name, at in k.items()}
+    assert quant(**k) == INV
+    assert "overlap" in uw.uw_last_error()
+
+
+@pytest.mark.parametrize("k", [{}, {"Y": P + 254}, {"Q": P + 4096, "Y": P + 14}, {"Q": P + 4096, "Y": P - 510}])
+def test_dequantize_refuses_overlaps(k):
+    assert dequant(**k) == INV
+    assert "overlap" in uw.uw_last_error()
+
+
+@pytest.mark.parametrize("k", [{}, {"W": P + 8192, "ws": P + 8192, "xs": P + 8192},
+                               {"X": P + 8192, "ws": P + 8192, "xs": P + 8192, "Y": P + 2044},
+                               {"W": P + 8192, "X": P + 16384, "ws": P + 508, "xs": P + 8192},
+                               {"W": P + 8192, "X": P + 16384, "ws": P + 8192, "xs": P + 508},
+                               {"W": P + 8192, "X": P + 16384, "ws": P + 8192, "xs": P + 8192, "bias": P - 124}])
+def test_gemm_refuses_overlaps(k):
+    for shape in (None, 1):
+        assert gemm(shape=shape, **k) == INV
+        assert "overlap" in uw.uw_last_error()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls that are not refused would run on these addresses")
+def test_overlaps_are_refused_exactly():
+    """Against the sets of bytes: refused where two rows share one, and only there (in place, element for element, aside)."""
+    rng = np.random.default_rng(7)
+    seen = {True: 0, False: 0}
+    for _ in range(20000):
+        n, cols = int(rng.integers(1, 6)), int(rng.integers(1, 20))
+        ldg = cols + int(rng.integers(0, 40))
+        ldy = ldg if rng.random() < 0.5 else cols + int(rng.integers(0, 40))
+        at = int(rng.integers(-160, 160))
+        xt, yt = (BF16, F32)[rng.integers(2)], (BF16, F32)[rng.integers(2)]
+        xs, ys = (2 if xt == BF16 else 4), (2 if yt == BF16 else 4)
+        G, Y = P, P + 4 * at
+        x_bytes = {r * ldg * xs + e for r in range(n) for e in range(cols * xs)}
+        y_bytes = {4 * at + r * ldy * ys + e for r in range(n) for e in range(cols * ys)}
+        twin = G == Y and xt == yt and (ldg == ldy or n == 1)
+        want = bool(x_bytes & y_bytes) and not twin
+        rc = uw.library().uw_silu_mul(G, ldg, G, ldg, xt, n, cols, Y, ldy, yt, None, None)
+        assert (rc == INV) == want, (n, cols, ldg, ldy, at, xt, yt)
+        seen[want] += 1
+    assert min(seen.values()) > 3000
