@@ -7,6 +7,7 @@ module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -153,6 +154,33 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _under(stream, device):
+    """A context in which torch allocates for work on `stream` (None, a raw
+    stream or an object with cuda_stream).  Memory allocated under another
+    stream could still be read by that one's earlier work, and would go back
+    to it while the writes here are pending."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    raw = stream if isinstance(stream, int) else getattr(stream, "cuda_stream", None)
+    if raw is None:
+        raise TypeError("stream must be a torch.cuda.Stream, a raw stream or None")
+    if raw == torch.cuda.current_stream(device).cuda_stream:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device))
+
+
+def _output(shape, dtype, device, stream):
+    """An output that the caller of a method left out, allocated under the
+    stream that writes it: work on another stream has to wait for that one
+    before it reads it, as with any tensor made there."""
+    import torch
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with _under(stream, device):
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _dtype_code(t) -> int:
@@ -654,7 +682,8 @@ def i8_rows(rows: int, cols: int, device="cuda"):
 class Int8Matrix:
     """A weight matrix in 8-bit integers with one scale per row, on the
     current CUDA device: gemm takes the int8 activations that uw_rmsnorm,
-    uw_silu_mul or uw_i8_quantize write."""
+    uw_silu_mul or uw_i8_quantize write.  An output that is not passed in is
+    allocated under `stream`; the caller orders other streams behind it."""
 
     def __init__(self, q, scale):
         import torch
@@ -682,14 +711,14 @@ class Int8Matrix:
     def dequantize(self, out=None, out_dtype=None, stream=None):
         import torch
         if out is None:
-            out = torch.empty(self.rows, self.cols, dtype=out_dtype or torch.bfloat16, device=self.q.device)
+            out = _output((self.rows, self.cols), out_dtype or torch.bfloat16, self.q.device, stream)
         uw_i8_dequantize(self.q, self.scale, out, stream)
         return out
 
     def gemm(self, X, x_scale, Y=None, bias=None, out_dtype=None, stream=None):
         import torch
         if Y is None:
-            Y = torch.empty(X.shape[0], self.rows, dtype=out_dtype or torch.float32, device=X.device)
+            Y = _output((X.shape[0], self.rows), out_dtype or torch.float32, X.device, stream)
         uw_i8_gemm(self.q, self.scale, X, x_scale, Y, bias, stream)
         return Y
 
@@ -750,21 +779,21 @@ class CompressedMatrix:
     def decompress(self, out=None, stream=None):
         import torch
         if out is None:
-            out = torch.empty(self.rows, self.cols, dtype=torch.bfloat16, device=self.d_blob.device)
+            out = _output((self.rows, self.cols), torch.bfloat16, self.d_blob.device, stream)
         uw_decompress(self.handle, out, out.stride(0), stream)
         return out
 
     def gemv(self, x, y=None, out_dtype=None, stream=None):
         import torch
         if y is None:
-            y = torch.empty(self.rows, dtype=out_dtype or torch.float32, device=x.device)
+            y = _output((self.rows,), out_dtype or torch.float32, x.device, stream)
         uw_gemv_fused(self.handle, x, y, stream)
         return y
 
     def gemm(self, X, Y=None, variant: int = UW_VARIANT_AUTO, ws=None, out_dtype=None, stream=None):
         import torch
         if Y is None:
-            Y = torch.empty(X.shape[0], self.rows, dtype=out_dtype or torch.float32, device=X.device)
+            Y = _output((X.shape[0], self.rows), out_dtype or torch.float32, X.device, stream)
         uw_gemm_fused(self.handle, X, Y, variant, ws, stream)
         return Y
 
@@ -777,7 +806,8 @@ class CompressedMatrix:
 
     def autotune(self, batch: int, ws=None, stream=None) -> dict:
         if ws is None:
-            ws = self.workspace(batch, autotune=True)
+            with _under(stream, self.d_blob.device):
+                ws = self.workspace(batch, autotune=True)
         return uw_autotune(self.handle, batch, ws, stream)
 
     def transcode_palette(self, attach: bool = True, stream=None) -> "PaletteMatrix":
@@ -788,7 +818,7 @@ class CompressedMatrix:
         n = uw_palette_transcode_size(self.handle)
         if n == 0:
             raise UwError(UW_ERR_UNSUPPORTED, "uw_palette_transcode_size", "this matrix cannot be transcoded")
-        d = torch.empty(n, dtype=torch.uint8, device=self.d_buf.device)
+        d = _output((n,), torch.uint8, self.d_buf.device, stream)
         uw_palette_transcode(self.handle, d, stream)
         p = PaletteMatrix.__new__(PaletteMatrix)
         p.blob = None
@@ -843,21 +873,21 @@ class PaletteMatrix:
     def decompress(self, out=None, stream=None):
         import torch
         if out is None:
-            out = torch.empty(self.rows, self.cols, dtype=torch.bfloat16, device=self.d_blob.device)
+            out = _output((self.rows, self.cols), torch.bfloat16, self.d_blob.device, stream)
         uw_palette_decompress(self.handle, out, out.stride(0), stream)
         return out
 
     def gemv(self, x, y=None, out_dtype=None, stream=None):
         import torch
         if y is None:
-            y = torch.empty(self.rows, dtype=out_dtype or torch.float32, device=x.device)
+            y = _output((self.rows,), out_dtype or torch.float32, x.device, stream)
         uw_palette_gemv(self.handle, x, y, stream)
         return y
 
     def gemm(self, X, Y=None, out_dtype=None, stream=None):
         import torch
         if Y is None:
-            Y = torch.empty(X.shape[0], self.rows, dtype=out_dtype or torch.float32, device=X.device)
+            Y = _output((X.shape[0], self.rows), out_dtype or torch.float32, X.device, stream)
         uw_palette_gemm(self.handle, X, Y, stream)
         return Y
 

@@ -724,3 +724,42 @@ def test_overlaps_are_refused():
         with pytest.raises((uw.UwError, ValueError)):
             call()
     assert not x.any()
+
+
+# -- outputs of calls on another stream ----------------------------------------------
+
+def test_outputs_belong_to_the_stream_that_writes_them():
+    """An output that is not passed in takes no block of the current stream's, and goes back to the other's."""
+    c = uw.CompressedMatrix.from_weights(workloads.weights("gate", rows=768, cols=1024, seed=12), device="cuda:0")
+    p = c.transcode_palette(attach=False)
+    m = uw.Int8Matrix.from_compressed(c)
+    q, qs = rand_i8(37, 1024, 4)
+    x = torch.randn(37, 1024, device=DEV).bfloat16()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    calls = {
+        "int8 gemm": lambda s: m.gemm(q, qs, stream=s), "dequantize": lambda s: m.dequantize(stream=s),
+        "gemm": lambda s: c.gemm(x[:4], stream=s), "gemv": lambda s: c.gemv(x[0], stream=s),
+        "decompress": lambda s: c.decompress(stream=s), "palette gemm": lambda s: p.gemm(x[:4], stream=s),
+        "palette gemv": lambda s: p.gemv(x[0], stream=s), "palette decompress": lambda s: p.decompress(stream=s),
+    }
+    for name, call in calls.items():
+        want = call(None)
+        torch.cuda.synchronize()
+        size, dtype = want.shape, want.dtype
+        for stream in (side, side.cuda_stream):
+            mine = torch.empty(size, dtype=dtype, device=DEV)  # a block that goes back to the current stream
+            at = mine.data_ptr()
+            del mine
+            got = call(stream)
+            assert got.data_ptr() != at, name
+            side.synchronize()
+            assert torch.equal(got, want), name
+            at = got.data_ptr()
+            del got
+            mine = torch.empty(size, dtype=dtype, device=DEV)
+            assert mine.data_ptr() != at, name
+            del mine
+    with pytest.raises(TypeError):
+        m.gemm(q, qs, stream="s")
+    c.close()

@@ -1,5 +1,8 @@
 """The 8-bit activation path without a GPU: the oracle's own pins and the
 library's refusals (every bad call is turned away before any launch)."""
+import contextlib
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -230,3 +233,67 @@ def test_overlaps_are_refused_exactly():
         assert (rc == INV) == want, (n, cols, ldg, ldy, at, xt, yt)
         seen[want] += 1
     assert min(seen.values()) > 3000
+
+
+# -- outputs of calls on another stream ---------------------------------------------
+
+class FakeStreams:
+    """torch's streams and allocations, recorded: which stream each torch.empty was made under."""
+
+    def __init__(self, monkeypatch):
+        self.stack, self.made = [1], []
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: self.stream(self.stack[-1]))
+        monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: self.stream(0))
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device=None: self.stream(raw))
+        monkeypatch.setattr(torch.cuda, "stream", self.under)
+        monkeypatch.setattr(torch, "empty", self.empty)
+
+    def stream(self, raw):
+        return types.SimpleNamespace(cuda_stream=raw)
+
+    @contextlib.contextmanager
+    def under(self, s):
+        self.stack.append(s.cuda_stream)
+        yield
+        self.stack.pop()
+
+    def empty(self, *shape, dtype=None, device=None):
+        self.made.append(self.stack[-1])
+        return types.SimpleNamespace(stride=lambda d: 64, data_ptr=lambda: P, numel=lambda: 64, element_size=lambda: 1)
+
+
+CALLS = {
+    "Int8Matrix.gemm": lambda m, s: m.gemm(types.SimpleNamespace(shape=(4, 64), device="cuda"), None, stream=s),
+    "Int8Matrix.dequantize": lambda m, s: m.dequantize(stream=s),
+    "CompressedMatrix.gemm": lambda m, s: m.gemm(types.SimpleNamespace(shape=(4, 64), device="cuda"), stream=s),
+    "CompressedMatrix.gemv": lambda m, s: m.gemv(types.SimpleNamespace(shape=(64,), device="cuda"), stream=s),
+    "CompressedMatrix.decompress": lambda m, s: m.decompress(stream=s),
+    "CompressedMatrix.autotune": lambda m, s: m.autotune(4, stream=s),
+    "CompressedMatrix.transcode_palette": lambda m, s: m.transcode_palette(attach=False, stream=s),
+    "PaletteMatrix.gemm": lambda m, s: m.gemm(types.SimpleNamespace(shape=(4, 64), device="cuda"), stream=s),
+    "PaletteMatrix.gemv": lambda m, s: m.gemv(types.SimpleNamespace(shape=(64,), device="cuda"), stream=s),
+    "PaletteMatrix.decompress": lambda m, s: m.decompress(stream=s),
+}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_outputs_are_allocated_under_the_stream_that_writes_them(call, monkeypatch):
+    mod = uw.uw
+    fake = FakeStreams(monkeypatch)
+    for name in ("uw_i8_gemm", "uw_i8_dequantize", "uw_gemm_fused", "uw_gemv_fused", "uw_decompress", "uw_autotune",
+                 "uw_palette_transcode", "uw_palette_gemm", "uw_palette_gemv",
+                 "uw_palette_decompress", "uw_workspace_size", "uw_autotune_scratch_size", "uw_palette_transcode_size"):
+        monkeypatch.setattr(mod, name, lambda *a, **k: 256)
+    monkeypatch.setattr(mod, "uw_palette_create_transcoded", lambda *a: None)  # a handle that nothing has to destroy
+    cls = getattr(mod, call.split(".")[0])
+    m = cls.__new__(cls)
+    where = types.SimpleNamespace(device="cuda")
+    m.q = m.scale = m.d_blob = m.d_buf = where
+    m.rows, m.cols, m.handle, m.info = 32, 64, None, {"n_raw_groups": 0}
+    for stream, want in ((None, 1), (fake.stream(1), 1), (fake.stream(7), 7), (9, 9), (0, 0)):
+        fake.made.clear()
+        CALLS[call](m, stream)
+        assert fake.made == [want], f"stream {stream}: made under {fake.made}"
+        assert fake.stack == [1]
+    with pytest.raises(TypeError):
+        CALLS[call](m, "s")
