@@ -1,6 +1,7 @@
 """Build libuw.so in-tree: hipcc for the gfx950 kernels, g++ for the host C++ (no
 library beyond the HIP runtime is linked); and _uw_torch.so, the C++ side of
-the Python binding (torch's headers and libraries, g++).
+the Python binding (torch's headers and libraries, g++), where torch is there:
+C callers need libuw.so alone.
 
     python decode_gemv_canonical_amd/build.py
 
@@ -47,9 +48,12 @@ def _run(cmd: list[str], verbose: bool) -> None:
         print(err, file=sys.stderr)
 
 
-def _binding_command(out: str) -> list[str]:
+def _binding_command(out: str) -> list[str] | None:
     # torch is found without importing it; its import takes longer than this compile
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        return None
+    torch_dir = torch.submodule_search_locations[0]
     inc = os.path.join(torch_dir, "include")
     return ["g++", *CXX_FLAGS, "-DUSE_ROCM", "-shared", "-Wno-sign-compare", f"-isystem{inc}",
             f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-I{sysconfig.get_paths()['include']}",
@@ -71,14 +75,19 @@ def build(verbose: bool = False) -> str:
         else:
             continue
         objs.append(obj)
-    jobs.append(_binding_command(TORCH_LIB + ".tmp"))
+    binding = _binding_command(TORCH_LIB + ".tmp")
+    if binding:
+        jobs.append(binding)
+    else:
+        print("torch is not installed: libuw.so is built without the Python binding's _uw_torch.so", file=sys.stderr)
     with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
         list(ex.map(lambda c: _run(c, verbose), jobs))
     tmp = LIB + ".tmp"
     _run([os.path.join(ROCM, "bin", "hipcc"), "-shared", f"--offload-arch={ARCH}", "-o", tmp, *objs,
           "-lpthread"], verbose)
     os.replace(tmp, LIB)
-    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+    if binding:
+        os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
     return LIB
 
 

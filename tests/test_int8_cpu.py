@@ -1,6 +1,8 @@
 """The 8-bit activation path without a GPU: the oracle's own pins and the
 library's refusals (every bad call is turned away before any launch)."""
 import contextlib
+import importlib.util
+import os
 import types
 
 import numpy as np
@@ -297,3 +299,32 @@ def test_outputs_are_allocated_under_the_stream_that_writes_them(call, monkeypat
         assert fake.stack == [1]
     with pytest.raises(TypeError):
         CALLS[call](m, "s")
+
+
+# -- the build -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("with_torch", [True, False])
+def test_library_builds_without_torch(with_torch, tmp_path, monkeypatch, capsys):
+    """libuw.so needs hipcc and g++ alone; only the Python binding's C++ side needs torch."""
+    path = os.path.join(os.path.dirname(uw.__file__), "build.py")
+    spec = importlib.util.spec_from_file_location("_uw_build_test", path)
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    made = []
+
+    def run(cmd, verbose):
+        made.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+
+    monkeypatch.setattr(b, "_run", run)
+    for name, at in (("BUILD", "o"), ("LIBDIR", "lib"), ("LIB", "lib/libuw.so"), ("TORCH_LIB", "lib/_uw_torch.so")):
+        monkeypatch.setattr(b, name, str(tmp_path / at))
+    if not with_torch:
+        monkeypatch.setattr(b.importlib.util, "find_spec", lambda name: None)
+    b.build()
+    assert os.path.exists(tmp_path / "lib" / "libuw.so")
+    assert os.path.exists(tmp_path / "lib" / "_uw_torch.so") == with_torch
+    assert any("torch" in a for c in made for a in c if a.startswith("-l")) == with_torch
+    assert ("torch" in capsys.readouterr().err) != with_torch
+    assert sorted(os.listdir(tmp_path / "lib")) == (["_uw_torch.so", "libuw.so"] if with_torch else ["libuw.so"])
