@@ -19,10 +19,12 @@
 // A row is held in registers from its one read to its write: chunks of 8
 // values, chunk t + j * NT on thread t, NT threads per row and VPT chunks per
 // thread, so x (and r, u, gain) are read once and every output written once.
-// Every load is issued before the first is used.  Sums are fp32, over at
-// most 32 values per lane before the tree over lanes and waves.  Loads and
-// stores are 16 bytes (8 for the integers) at any element alignment: gfx950
-// takes them unaligned, and a row's last chunk goes element by element.
+// Every load is issued before the first is used.  Sums of squares are fp32:
+// the 8 of a chunk, a lane's chunks (at most 4; any number, in fp64, in the
+// form for long rows), lanes and waves, so that no square passes more than 8 +
+// 3 + 6 + 15 = 32 roundings.  Loads and stores are 16 bytes (8 for the
+// integers) at any element alignment: gfx950 takes them unaligned, and a row's
+// last chunk goes element by element.
 #include <algorithm>
 
 #include "uw_device.h"
@@ -284,7 +286,9 @@ __global__ __launch_bounds__(NT == kWave ? 256 : NT) void row_kernel(RowArgs a) 
   uint32_t top = 0u;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    chunk_p<OP, XT, RT>(a, xr[j], rr[j], gr[j], p[j], h, 8 * (t + int64_t(j) * NT), sum);
+    float part = 0.f;
+    chunk_p<OP, XT, RT>(a, xr[j], rr[j], gr[j], p[j], h, 8 * (t + int64_t(j) * NT), part);
+    sum += part;
     if (I8) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = max(top, f32_bits(p[j][e]) & 0x7FFFFFFFu);
@@ -337,19 +341,20 @@ __global__ __launch_bounds__(1024) void long_row_kernel(RowArgs a) {
   const char* x = a.x + row * a.ldx * kXs;
   const char* r = a.r + row * a.ldr * kRs;
   char* h = a.h ? a.h + row * a.ldh * kRs : nullptr;
-  float sum = 0.f;
+  double squares = 0.;  // a lane's chunks: fp32 lost 220 half steps of y over 2^24 equal values
   uint32_t top = 0u;
   for (int64_t i = 8 * t; i < a.cols; i += 8 * NT) {
     Raw8 rr{}, gr{};
     const Raw8 xr = load8<XT>(x, i, a.cols);
     if (RT != kNone) rr = load8<RT>(r, i, a.cols);
     if (OP == kNorm) gr = load_gain(a, i);
-    float p[8], part = 0.f;  // squares are summed per chunk first: the lane's sum has few addends
+    float p[8], part = 0.f;
     chunk_p<OP, XT, RT>(a, xr, rr, gr, p, h, i, part);
-    sum += part;
+    if (OP == kNorm) squares += double(part);
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, f32_bits(p[e]) & 0x7FFFFFFFu);
   }
+  float sum = float(squares);
   row_reduce<NT>(sum, top);
   const float rstd = OP == kNorm ? 1.f / sqrtf(fmaf(sum, a.inv_cols, a.eps)) : 1.f;
   float s, inv;

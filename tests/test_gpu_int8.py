@@ -763,3 +763,19 @@ def test_outputs_belong_to_the_stream_that_writes_them():
     with pytest.raises(TypeError):
         m.gemm(q, qs, stream="s")
     c.close()
+
+
+# -- long sums ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("value,cols", [(1.2, (1 << 24) + 5), (1.0001, (1 << 22) + 8), (1.37, 1 << 20)])
+def test_norm_of_long_rows_of_equal_values(value, cols):
+    """Equal squares: every addition of a long chain rounds the same way, so a chain in fp32 shows."""
+    X = torch.full((1, cols), value, device=DEV)
+    x = float(X[0, 0])
+    Y, Q, s = torch.empty_like(X), uw.i8_rows(1, cols), torch.empty(1, device=DEV)
+    uw.uw_rmsnorm(X, None, Y, eps=EPS)
+    want = x / np.sqrt(x * x + float(np.float32(EPS)))
+    for at in (0, cols // 2, cols - 1):
+        assert abs(float(Y[0, at]) - want) <= 32 * U * want
+    uw.uw_rmsnorm(X, None, Q, scale=s, eps=EPS)
+    assert (Q == 127).all() and abs(127 * float(s[0]) - want) <= 32 * U * want
