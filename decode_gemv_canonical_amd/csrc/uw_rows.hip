@@ -215,6 +215,19 @@ __device__ __forceinline__ float exp_neg(float g) {
   return fabsf(t) < 126.f ? fmaf(e, d * kLn2, e) : e;
 }
 
+// silu(g) * u for g < kSiluFar, where 1 + exp(-g) nears 2^126 and its
+// reciprocal would be flushed to zero: there g exp(g) u, the exponential held
+// as 2^160 times its value, so that a large u finds all of its bits.
+constexpr float kSiluFar = -87.f;
+__device__ __forceinline__ float silu_far(float g, float u) {
+#pragma clang fp contract(off)  // t is rounded before 160 is added: d is what that rounding lost
+  constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147182f;  // as in exp_neg
+  const float c = fmaxf(g, -300.f);  // exp(-300) * 2^160 is zero in fp32, and t stays finite
+  const float t = c * kHi, d = fmaf(c, kLo, fmaf(c, kHi, -t));
+  const float e = __builtin_amdgcn_exp2f(t + 160.f);  // the sum is exact
+  return __builtin_amdgcn_ldexpf(g * fmaf(e, d * kLn2, e) * (u * 0x1p-64f), -96);
+}
+
 // One chunk's p = h * gain (norm; h is also rounded, kept and squared),
 // silu(g) * u, or x.  Inlined twice: held in registers, or computed again.
 template <int OP, int XT, int RT>
@@ -246,8 +259,17 @@ __device__ __forceinline__ void chunk_p(const RowArgs& a, const Raw8& xr, const 
   } else if (OP == kSilu) {
     float u[8];
     unpack8<XT>(rr, u);
+    uint32_t far = 0u;  // as unsigned numbers, only large negative values (and NaN) lie past kSiluFar
+#pragma unroll
+    for (int e = 0; e < 8; ++e) far = max(far, f32_bits(p[e]));
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] = p[e] * __builtin_amdgcn_rcpf(1.f + exp_neg(p[e])) * u[e];
+    if (far > f32_bits(kSiluFar)) {
+      float g[8];
+      unpack8<XT>(xr, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = g[e] < kSiluFar ? silu_far(g[e], u[e]) : p[e];
+    }
   }
 }
 

@@ -616,10 +616,11 @@ int uw_rmsnorm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int xt
 
 /*
  * uw_silu_mul (device) - p = g / (1 + exp(-g)) * u element by element, fp32
- * arithmetic: a gated MLP's activation.  d_G and d_U hold batch rows of cols
- * elements of xt with strides ldg and ldu (halves of one product's rows, for
- * instance); d_Y, yt, ldy and d_scale as for uw_rmsnorm, and d_Y may be d_G
- * or d_U itself.
+ * arithmetic (within 8 * 2^-24 of the formula's value, also where exp(-g) is
+ * past the fp32 range): a gated MLP's activation.  d_G and d_U hold batch rows
+ * of cols elements of xt with strides ldg and ldu (halves of one product's
+ * rows, for instance); d_Y, yt, ldy and d_scale as for uw_rmsnorm, and d_Y may
+ * be d_G or d_U itself.
  * Errors: UW_ERR_INVALID, UW_ERR_HIP.
  */
 int uw_silu_mul(const void* d_G, int64_t ldg, const void* d_U, int64_t ldu, int xt, int64_t batch, int64_t cols,

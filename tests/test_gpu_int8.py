@@ -779,3 +779,42 @@ def test_norm_of_long_rows_of_equal_values(value, cols):
         assert abs(float(Y[0, at]) - want) <= 32 * U * want
     uw.uw_rmsnorm(X, None, Q, scale=s, eps=EPS)
     assert (Q == 127).all() and abs(127 * float(s[0]) - want) <= 32 * U * want
+
+
+# -- the activation far below zero ------------------------------------------------------------
+
+@pytest.mark.parametrize("x,out", list(itertools.product(("bf16", "f32"), ("f32", "bf16", "i8"))))
+@pytest.mark.parametrize("cols", [400, 14336, 40000])
+def test_silu_far_below_zero(cols, x, out):
+    """exp(-g) near and past the fp32 range, next to values of u that bring the product back into it."""
+    gen = torch.Generator().manual_seed(cols)
+    G = -80 - 140 * torch.rand(6, cols, generator=gen)
+    G[:, ::7] = torch.randn(6, len(range(0, cols, 7)), generator=gen)
+    G[0, :5] = torch.tensor([-87.0, -87.25, -88.0, -88.75, -126.0])
+    scale = torch.tensor([1.0, 1e3, 1e20, 1e30, 3e38, -3e38])[:, None]
+    V = scale * (0.5 + 0.5 * torch.rand(6, cols, generator=gen))
+    V[:, ::7] = torch.randn(6, len(range(0, cols, 7)), generator=gen) * 1e-30
+    G, V = G.to(DT[x]).to(DEV), V.to(DT[x]).to(DEV)
+    p = o8.silu_mul(f64(G), f64(V))
+    tiny = 2.0 ** -149  # one step of a denormal number
+    if out == "i8":
+        Q, s = uw.i8_rows(6, cols), torch.empty(6, device=DEV)
+        uw.uw_silu_mul(G, V, Q, scale=s)
+        step = np.maximum(np.abs(p).max(axis=1) / 127, 2.0 ** -126)
+        check(s, step, 10 * U, torch.float32, "scale", tiny)
+        off = np.abs(Q.cpu().numpy().astype(np.float64) - p / step[:, None])
+        assert (off <= 0.5 + 127 * 20 * U + 2 * tiny / step[:, None]).all(), off.max()
+    else:
+        Y = torch.empty(6, cols, dtype=DT[out], device=DEV)
+        uw.uw_silu_mul(G, V, Y)
+        check(Y, p, 8 * U, DT[out], f"silu {x} {out}", tiny if out == "f32" else 2.0 ** -133)
+
+
+def test_silu_at_the_ends_of_the_range():
+    inf = float("inf")
+    G = torch.tensor([[-3e38, -1e5, -301.0, -inf, -90.0, -90.0, -inf, -3e38]], device=DEV)
+    V = torch.tensor([[3e38, -3e38, 1.0, 1.0, inf, -inf, inf, 0.0]], device=DEV)
+    Y = torch.empty_like(G)
+    uw.uw_silu_mul(G, V, Y)
+    y = Y.cpu().numpy()[0]
+    assert (y[:3] == 0).all() and np.isnan(y[3]) and y[4] == -inf and y[5] == inf and np.isnan(y[6]) and y[7] == 0
