@@ -437,11 +437,15 @@ int run_rows(const RowArgs& a, hipStream_t s) {
   return go(long_row_kernel<OP, XT, RT, I8>, 1024, 1);
 }
 
+// Rows a launch takes where each is spread over per_row workgroups of 256: a
+// launch holds fewer than 2^32 threads.  0: not even one.
+int64_t band_rows(int64_t per_row) { return ((int64_t(1) << 24) - 1) / per_row; }
+
 template <int XT>
 int run_silu(const RowArgs& a, hipStream_t s) {
   constexpr int kXs = XT == kF32 ? 4 : 2;
-  const int64_t per_row = (a.cols + 2047) / 2048;
-  const int64_t band = std::max<int64_t>(1, (int64_t(1) << 23) / per_row);  // under 2^32 threads a launch
+  const int64_t per_row = (a.cols + 2047) / 2048, band = band_rows(per_row);
+  if (band == 0) return fail(UW_ERR_UNSUPPORTED, "uw_silu_mul: a row wider than a launch holds");
   for (int64_t row0 = 0; row0 < a.rows; row0 += band) {
     RowArgs b = a;
     b.rows = std::min(band, a.rows - row0);
@@ -519,8 +523,8 @@ int launch_i8_quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, i
 
 int launch_i8_dequantize(const int8_t* Q, int64_t rows, int64_t cols, int64_t ldq, const float* scale, void* Y,
                          int64_t ldy, int yt, void* stream) {
-  const int64_t per_row = (cols + 4095) / 4096;
-  const int64_t band = std::max<int64_t>(1, (int64_t(1) << 23) / per_row);  // under 2^32 threads a launch
+  const int64_t per_row = (cols + 4095) / 4096, band = band_rows(per_row);
+  if (band == 0) return fail(UW_ERR_UNSUPPORTED, "uw_i8_dequantize: a row wider than a launch holds");
   for (int64_t row0 = 0; row0 < rows; row0 += band) {
     const int64_t n = std::min(band, rows - row0);
     hipLaunchKernelGGL(dequantize_kernel, dim3(unsigned(n * per_row)), dim3(256), 0, static_cast<hipStream_t>(stream),

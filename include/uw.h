@@ -621,7 +621,8 @@ int uw_rmsnorm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int xt
  * of cols elements of xt with strides ldg and ldu (halves of one product's
  * rows, for instance); d_Y, yt, ldy and d_scale as for uw_rmsnorm, and d_Y may
  * be d_G or d_U itself.
- * Errors: UW_ERR_INVALID, UW_ERR_HIP.
+ * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (fp32 or bf16 outputs of more
+ *         than 2^35 - 2048 columns), UW_ERR_HIP.
  */
 int uw_silu_mul(const void* d_G, int64_t ldg, const void* d_U, int64_t ldu, int xt, int64_t batch, int64_t cols,
                 void* d_Y, int64_t ldy, int yt, float* d_scale, void* stream);
@@ -641,7 +642,8 @@ int uw_i8_quantize(const void* d_X, int64_t rows, int64_t cols, int64_t ldx, int
 /*
  * uw_i8_dequantize (device) - the values 8-bit rows stand for, q * scale, in
  * yt (UW_F32, or UW_BF16 rounded to nearest even), stride ldy >= cols.
- * Errors: UW_ERR_INVALID, UW_ERR_HIP.
+ * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (more than 2^36 - 4096 columns),
+ *         UW_ERR_HIP.
  */
 int uw_i8_dequantize(const int8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq, const float* d_scale, void* d_Y,
                      int64_t ldy, int yt, void* stream);

@@ -818,3 +818,45 @@ def test_silu_at_the_ends_of_the_range():
     uw.uw_silu_mul(G, V, Y)
     y = Y.cpu().numpy()[0]
     assert (y[:3] == 0).all() and np.isnan(y[3]) and y[4] == -inf and y[5] == inf and np.isnan(y[6]) and y[7] == 0
+
+
+# -- more rows than a launch takes ---------------------------------------------------------
+
+def test_rows_past_the_bands_of_each_operator():
+    """Rows on both sides of the limit of a launch: 2^24 - 1 for silu and dequantize, 2^21 for the others."""
+    rows, edge = (1 << 24) + 9, (1 << 24) - 1
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    G = torch.randn(rows, 8, device=DEV, generator=gen).bfloat16()
+    V = torch.randn(rows, 8, device=DEV, generator=gen).bfloat16()
+    Y = torch.zeros(rows, 8, dtype=torch.bfloat16, device=DEV)
+    uw.uw_silu_mul(G, V, Y)
+    for at in (slice(0, 5), slice(edge - 4, edge + 4), slice(rows - 5, rows)):
+        check(Y[at], o8.silu_mul(f64(G[at]), f64(V[at])), 8 * U, torch.bfloat16, "silu", 2.0 ** -118)
+    del Y
+    Q = torch.randint(-127, 128, (rows, 8), dtype=torch.int8, device=DEV, generator=gen)
+    s = torch.rand(rows, device=DEV, generator=gen)
+    Y = torch.empty(rows, 8, device=DEV)
+    uw.uw_i8_dequantize(Q, s, Y)
+    assert torch.equal(Y, Q.float() * s[:, None])
+    rows, edge = (1 << 21) + 9, 1 << 21
+    del Y, Q, s
+    G, V = G[:rows].clone(), V[:rows].clone()
+    for out in ("bf16", "i8"):
+        H = torch.zeros(rows, 8, dtype=torch.bfloat16, device=DEV)
+        Y = torch.zeros(rows, 8, dtype=DT[out], device=DEV)
+        s = torch.zeros(rows, device=DEV)
+        uw.uw_rmsnorm(G, None, Y, scale=s if out == "i8" else None, residual=V, residual_out=H)
+        S = torch.zeros(rows, device=DEV)
+        A = torch.zeros(rows, 8, dtype=torch.int8, device=DEV)
+        uw.uw_silu_mul(G, V, A, scale=S)
+        for at in (slice(0, 5), slice(edge - 4, edge + 4), slice(rows - 5, rows)):
+            h = o8.norm_h(f64(G[at]), f64(V[at]), True)
+            assert np.array_equal(f64(H[at]), h)
+            if out == "i8":
+                q, step = o8.quantize(h.astype(np.float32))
+                assert np.array_equal(Y[at].cpu().numpy(), q)
+                check(s[at], step * o8.rstd(h, EPS), 32 * U, torch.float32, "scale")
+            else:
+                check(Y[at], o8.rmsnorm(h, None, EPS), 32 * U, torch.bfloat16, "norm")
+            p = o8.silu_mul(f64(G[at]), f64(V[at]))
+            assert (np.abs(f64(A[at]) * f64(S[at])[:, None] - p) <= f64(S[at])[:, None] * (0.5 + 127 * 20 * U)).all()

@@ -328,3 +328,15 @@ def test_library_builds_without_torch(with_torch, tmp_path, monkeypatch, capsys)
     assert any("torch" in a for c in made for a in c if a.startswith("-l")) == with_torch
     assert ("torch" in capsys.readouterr().err) != with_torch
     assert sorted(os.listdir(tmp_path / "lib")) == (["_uw_torch.so", "libuw.so"] if with_torch else ["libuw.so"])
+
+
+# -- widths ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("cols", [1 << 36, (1 << 39) + 1])
+def test_rows_wider_than_a_launch(cols):
+    """silu's plain outputs and dequantize spread a row over a launch's fewer than 2^32 threads."""
+    Y = 1 << 45
+    for yt in (BF16, F32):
+        assert silu(batch=1, cols=cols, yt=yt, Y=Y) == UNSUP
+        assert dequant(rows=1, cols=cols, yt=yt, Y=Y, scale=1 << 44) == UNSUP
+    assert "wider" in uw.uw_last_error()
