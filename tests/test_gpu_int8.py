@@ -860,3 +860,23 @@ def test_rows_past_the_bands_of_each_operator():
                 check(Y[at], o8.rmsnorm(h, None, EPS), 32 * U, torch.bfloat16, "norm")
             p = o8.silu_mul(f64(G[at]), f64(V[at]))
             assert (np.abs(f64(A[at]) * f64(S[at])[:, None] - p) <= f64(S[at])[:, None] * (0.5 + 127 * 20 * U)).all()
+
+
+# -- slices whose workgroups start inside the row --------------------------------------------
+
+@pytest.mark.parametrize("shape", [0, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("cols,ld", [(4096, 4096), (4090, 4096), (4001, 4096), (257, 4096), (100, 4096), (8190, 8192), (4097, 12288)])
+def test_gemm_slices_at_strides_of_4_kb(cols, ld, shape):
+    """The starts wrap around the end of the row, whose last block is masked wherever in the order it comes."""
+    rows = 1300
+    W, ws = rand_i8(rows, cols, 21, pad=ld - cols)
+    for b in (1, 17, 40):
+        X, xs = rand_i8(b, cols, 22, pad=ld - cols)
+        Y = torch.empty(b, rows, device=DEV)
+        if shape:
+            uw.uw_i8_gemm_shaped(W, ws, X, xs, Y, shape)
+        else:
+            uw.uw_i8_gemm(W, ws, X, xs, Y)
+        sums = (X.cpu().numpy().astype(np.float64) @ W.cpu().numpy().astype(np.float64).T).astype(np.float32)
+        want = sums * (xs.cpu().numpy()[:, None] * ws.cpu().numpy()[None, :])
+        assert np.array_equal(Y.cpu().numpy(), want), f"b={b}"
