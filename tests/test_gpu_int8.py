@@ -19,6 +19,7 @@ Tolerances, u = 2^-24 (half a step of fp32) and 2^-8 half a step of bf16:
            3.1 u |product| + 1.1 u |y|.
 """
 import itertools
+import random
 import sys
 
 import numpy as np
@@ -880,3 +881,40 @@ def test_gemm_slices_at_strides_of_4_kb(cols, ld, shape):
         sums = (X.cpu().numpy().astype(np.float64) @ W.cpu().numpy().astype(np.float64).T).astype(np.float32)
         want = sums * (xs.cpu().numpy()[:, None] * ws.cpu().numpy()[None, :])
         assert np.array_equal(Y.cpu().numpy(), want), f"b={b}"
+
+
+# -- the measured cases ---------------------------------------------------------------------
+
+def measured_cases():
+    from perf import operators as ops
+    rng = random.Random(17)
+    return ops.listed() + [dict(ops.draw(rng), name=f"drawn {i}") for i in range(24)]
+
+
+@pytest.mark.parametrize("case", measured_cases(), ids=lambda c: c["name"])
+def test_measured_cases_against_their_definition(case, monkeypatch):
+    """The calls of perf/operators.py, as they are timed, against its definition in 64 bits.  An integer at a tie may go
+    either way there (the definition in fp32 is checked to the bit above), so 8-bit values may be one step off."""
+    from perf import operators as ops
+    monkeypatch.setattr(ops, "own", True)
+    _say(f"case {case}")
+    state = ops.prepare(case, 5)
+    got, ref = ops.run(state), ops.exact(case, 5)
+    if case["op"] == "gemm":
+        size = ref.abs() + (0 if state["bias"] is None else state["bias"].double().abs())
+        lim = 5 * U * size + (HALF[got.dtype] if got.dtype == torch.bfloat16 else 0) * ref.abs()
+        assert got.shape == ref.shape and bool(((got.double() - ref).abs() <= lim).all())
+        return
+    kept, y = got[0], got[1].double()
+    assert (kept is None) == (ref[0] is None) and (kept is None or torch.equal(kept.double(), ref[0]))
+    assert y.shape == ref[1].shape
+    if case["op"] == "mlp":
+        # each 8-bit operand is half a step off at most on either side; the rest is as in test_mlp_together
+        assert torch.linalg.norm(y - ref[1]) <= 0.05 * torch.linalg.norm(ref[1])
+    elif len(got) == 3:
+        step = ref[2].unsqueeze(1)
+        assert bool(((got[2].double() - ref[2]).abs() <= 40 * U * ref[2]).all())
+        assert bool(((y - ref[1]).abs() <= 1.001 * step + 1.01 * 2.0 ** -8 * ref[1].abs()).all())
+    else:
+        half = HALF[got[1].dtype] if got[1].dtype == torch.bfloat16 else 0
+        assert bool(((y - ref[1]).abs() <= (32 * U * (1 + half) + half) * ref[1].abs() + 2.0 ** -126).all())
