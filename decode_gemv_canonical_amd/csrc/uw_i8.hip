@@ -199,7 +199,7 @@ __device__ __forceinline__ void store_through_lds(const I8Args& a, int64_t n0, i
 // waves split k: wave w takes the 256-byte groups w, w + KS, ... and the
 // partial tiles are summed in LDS.  The next group's loads are issued before
 // this group's products.  Rows may start at any byte; nothing outside a row is
-// read.  1 x 4096 x 4099: 12.1 us, against 16.3 for i8_loose_kernel.
+// read.  1 x 4096 x 4099: 12.4 us, against 17.0 for i8_loose_kernel.
 template <bool YBF16>
 __global__ __launch_bounds__(512) void i8_direct_kernel(I8Args a, int n_groups, int ny, int KS) {
   const int L = int(blockIdx.x);
@@ -559,10 +559,11 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i8_stage_kernel(I8Args a,
 // into the other of two LDS buffers, one block ahead of the products.  Rows
 // may start at any byte; nothing outside a row is read.
 // Bound by the loads: off a 16-byte boundary they take a lane per cycle, 0.5 us
-// per 16 KB and compute unit (4096 x 14336 x 4099: 435 us, against 5865 for 32
-// x 32 tiles in i8_direct_kernel; aligned rows: 209).  Eight waves beat four
-// (64 x 14336 x 4099: 19.9 us against 23.2); two to four blocks ahead changed
-// nothing, nor did words loaded on a 4-byte boundary and shifted.
+// per 16 KB and compute unit (4096 x 14336 x 4099: 427 us, against 5865 for 32
+// x 32 tiles in i8_direct_kernel; at a stride of 4112, staged: 293).  Eight
+// waves beat four (64 x 14336 x 4099, operands partly in the last-level cache:
+// 19.9 us against 23.2; all from memory 27.1); two to four blocks ahead
+// changed nothing, nor did words loaded on a 4-byte boundary and shifted.
 template <int BW, int BB, int WGW, int WGB, bool YBF16>
 __global__ __launch_bounds__(64 * WGW * WGB) void i8_loose_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
   constexpr int NW = WGW * WGB;
@@ -649,11 +650,12 @@ __global__ __launch_bounds__(64 * WGW * WGB) void i8_loose_kernel(I8Args a, int 
 // barrier per step; the slot a step's operands came from is refilled while
 // its products run, so ST steps are in flight.
 // Bound by power: with operands of zeros 4096 x 4096 x 16384 runs in 153 us
-// (3.6 POP/s, 4.0 inside the loop), with random ones in 202 us (2.7 POP/s),
-// the clock falling from 2.3 to about 1.8 GHz; products alone, operands held
-// in registers, reach 3.4 POP/s on random values.  32 x 32 products (twice the
-// accumulator traffic per operation) took 265 us there, four waves with the
-// 16 x 16 form 241 us, the kernel above at 256 x 256 219 us.
+// (3.6 POP/s, 4.0 inside the loop), with random ones in 202 to 227 us (2.7 to
+// 2.4 POP/s from run to run), the clock falling from 2.3 to about 1.8 GHz;
+// products alone, operands held in registers, reach 3.4 POP/s on random
+// values.  Where this took 202 us, 32 x 32 products (twice the accumulator
+// traffic per operation) took 265, four waves with the 16 x 16 form 241, the
+// kernel above at 256 x 256 219.
 template <int BW, int BB, int WGW, int WGB, int ST, bool YBF16, bool NT>
 __global__ __launch_bounds__(64 * WGW * WGB) void i8_wide_kernel(I8Args a, int nw_tiles, int nb_tiles, int per_xcd) {
   constexpr int NW = WGW * WGB;
@@ -880,10 +882,12 @@ bool stage_ok(const I8Args& a) {
 // needs `shared` per block and workgroup it holds; and the operands' bytes come
 // at 5.4 TB/s.  The three limits of the loop add as fourth powers (the largest
 // rules, a near second counts).
-// The constants are fits to the shapes' times on 687 sizes drawn over 1..4096
-// x 64..28672 x 64..14336 (and the MLP's), each on 3 to 8 rotated operand sets;
-// the shapes so chosen take 1.03 of the best shape's time in the mean, against
-// 1.20 for the largest tile that gives 160 workgroups.
+// The constants were fitted to the shapes' times on sizes drawn over 1..4096 x
+// 64..28672 x 64..14336 (and the MLP's), each on 3 to 8 rotated operand sets.
+// Only their order counts: the times themselves are up to a quarter off.  On
+// 2373 other sizes of that range the choice takes 1.026 of the best shape's
+// time in the mean (95 of 100 under 1.15, the worst 2.2: 2618 x 141 x 8032),
+// against 1.47 for the best single shape.
 float expected_us(const I8Shape& s, int64_t rows, int64_t cols, int64_t batch) {
   const float blocks = float((cols + 127) / 128);
   const float n = float((rows + s.bw - 1) / s.bw) * float((batch + s.bb - 1) / s.bb) / kCus;
@@ -897,8 +901,9 @@ float expected_us(const I8Shape& s, int64_t rows, int64_t cols, int64_t batch) {
 
 // Operands that can be staged run the shape expected to be fastest.  Of the
 // others, the smallest tile of which a compute unit gets at most two, or the
-// largest: 1.03 of the best shape's time in the mean of 491 sizes drawn as
-// above at odd strides (always 16 x 16: 2.06, always 64 x 64: 1.13).
+// largest: 1.035 of the best shape's time in the mean of 4034 sizes drawn as
+// above at odd strides (95 of 100 under 1.23, the worst 2.6: 1655 x 64 x 14289;
+// always 64 x 64: 1.16, always 128 x 128: 1.69).
 int pick_shape(int64_t rows, int64_t cols, int64_t batch, bool staged) {
   if (!staged) {
     for (int i = 1; i < kFirstStaged - 1; ++i) {
