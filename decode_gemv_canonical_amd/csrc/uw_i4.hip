@@ -1,0 +1,433 @@
+// Weights in 4-bit integers with a scale (and, in the affine form, an offset)
+// per group of G = 32, 64 or 128 columns: from rows of bf16 or fp32, back, and
+// their product with bf16 activations on the gfx950 matrix cores.
+//
+//   W[n, k] = s[g, n] q[n, k] (+ m[g, n]),   g = k / G,  q in -8 .. 7
+//   Y[b, n] = sum_g s[g, n] (sum_k q[n, k] X[b, k]) + m[g, n] (sum_k X[b, k]) (+ bias[n])
+//
+// A row's integers lie two to a byte as q + 8, the even column in the low
+// half; rows start at multiples of 16 bytes, and the last 16-byte word of a
+// row may be read whole.  Scales and offsets lie group by group, [groups,
+// rows], so that the rows of a tile find theirs side by side.
+//
+// Product: q / 16 is exact in bf16 (v_cvt_off_f32_i4 makes it from a nibble),
+// so is its product with a bf16 activation, and the matrix cores add a group's
+// products in fp32; the group's sum is scaled and added in fp32.  Nothing is
+// rounded to fewer bits before Y.  The factor 16 is applied once at the end.
+// With A = 16 activation rows and B = 16 weight rows, lane (r = lane % 16, q =
+// lane / 16) holds 8 consecutive k of row r, and of the result weight row r for
+// activation rows 4 q .. 4 q + 3: one scale per lane and tile.
+#include <algorithm>
+
+#include "uw_device.h"
+
+namespace uw {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kXcds = 8;
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126
+
+struct I4Args {
+  const uint8_t* W;
+  const char* scale;
+  const char* offset;  // null: none
+  const uint16_t* X;
+  const float* bias;  // may be null
+  char* Y;
+  int64_t rows, cols, ldw, lds, ldo, batch, ldx, ldy;  // ldw in bytes, the others in elements
+  int32_t st, yt;                                      // types of the scales and of Y
+};
+
+__device__ __forceinline__ u32x4 load16_any(const void* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
+__device__ __forceinline__ float load_scale(const char* p, int64_t i, int st) {
+  if (st == UW_F32) return reinterpret_cast<const float*>(p)[i];
+  return bits_f32(uint32_t(reinterpret_cast<const uint16_t*>(p)[i]) << 16);
+}
+
+// q / 16 of eight nibbles q + 8, in bf16, in order.
+__device__ __forceinline__ bf16x8 decode8(uint32_t w) {
+  w ^= 0x88888888u;  // two's complement
+  const uint32_t h = w >> 4;
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = pack_bf16(__builtin_amdgcn_cvt_off_f32_i4(int(w >> (8 * i))), __builtin_amdgcn_cvt_off_f32_i4(int(h >> (8 * i))));
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// Values [k, k + 8) of a row of n bf16 values; those past the end read as zero
+// and are not touched.
+__device__ __forceinline__ u32x4 load_x8(const uint16_t* row, int64_t k, int64_t n) {
+  if (k + 8 <= n) return load16_any(row + k);
+  uint32_t e[7];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) e[i] = k + i < n ? row[k + i] : 0u;
+  return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6]};
+}
+
+__device__ __forceinline__ f32x4 mfma_bf16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// The 4 x 4 transposition of 32-bit words over the wave's four rows of 16
+// lanes: word i of lane (r, q) becomes word q of lane (r, i).
+__device__ __forceinline__ void transpose4(u32x4& v) {
+  // rows 1 and 3 of the first against rows 0 and 2 of the second, then the halves
+  auto a = __builtin_amdgcn_permlane16_swap(v.x, v.y, false, false);
+  auto b = __builtin_amdgcn_permlane16_swap(v.z, v.w, false, false);
+  auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+  auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  v = u32x4{c[0], d[0], c[1], d[1]};
+}
+
+__device__ __forceinline__ void store_y(const I4Args& a, int64_t b, int64_t n, float v) {
+  if (b >= a.batch || n >= a.rows) return;
+  if (a.yt == UW_F32) reinterpret_cast<float*>(a.Y)[b * a.ldy + n] = v;
+  else reinterpret_cast<__bf16*>(a.Y)[b * a.ldy + n] = static_cast<__bf16>(v);
+}
+
+// 16 y as it goes out: scaled, the bias added in a rounding of its own.
+__device__ __forceinline__ float finish(float acc, bool biased, float bias) {
+#pragma clang fp contract(off)
+  const float v = acc * 16.f;
+  return biased ? v + bias : v;
+}
+
+// A workgroup holds 16 weight rows and 16 activation rows; its KS waves split
+// k: wave w takes the blocks of 128 columns w, w + KS, ... and the partial
+// tiles are summed in LDS, wave by wave.  Everything is read straight from
+// global memory; activation rows may start at any element.
+template <int G, bool OFF>
+__global__ __launch_bounds__(512) void i4_direct_kernel(I4Args a, int n_groups, int ny, int KS) {
+  const int L = int(blockIdx.x);
+  const int grp = (L / (kXcds * ny)) * kXcds + L % kXcds;
+  const int y = (L / kXcds) % ny;
+  if (grp >= n_groups) return;  // whole workgroups
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int r = lane % 16, q = lane / 16;
+  const int64_t n = int64_t(grp) * 16 + r, n_in = std::min<int64_t>(n, a.rows - 1);
+  const int64_t b0 = int64_t(y) * 16;
+  const uint8_t* wr = a.W + n_in * a.ldw;
+  const uint16_t* xr = a.X + std::min<int64_t>(b0 + r, a.batch - 1) * a.ldx;
+  const int64_t last = (a.cols - 1) / 32;  // the rows' last 16-byte word
+  const int64_t n_blocks = (a.cols + 127) / 128;
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = zero;
+  for (int64_t kb = wave; kb < n_blocks; kb += KS) {
+    const int64_t k0 = kb * 128;
+    u32x4 w = load16_any(wr + 16 * std::min<int64_t>(4 * kb + q, last));
+    transpose4(w);  // word s: columns k0 + 32 s + 8 q and on
+#pragma unroll
+    for (int g = 0; g < 128 / G; ++g) {
+      if (k0 + g * G >= a.cols) break;
+      f32x4 part = zero, sum = zero;
+#pragma unroll
+      for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
+        const bf16x8 x = __builtin_bit_cast(bf16x8, load_x8(xr, k0 + 32 * s + 8 * q, a.cols));
+        part = mfma_bf16(x, decode8(w[s]), part);
+        if (OFF) sum = mfma_bf16(x, ones, sum);
+      }
+      const int64_t at = k0 / G + g;
+      const float sc = load_scale(a.scale, at * a.lds + n_in, a.st);
+      const float m = OFF ? load_scale(a.offset, at * a.ldo + n_in, a.st) * 0.0625f : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[e] = fmaf(sc, part[e], acc[e]);
+        if (OFF) acc[e] = fmaf(m, sum[e], acc[e]);
+      }
+    }
+  }
+  st128(uint32_t(wave * 1024 + 16 * lane), __builtin_bit_cast(uint4, acc));
+  __syncthreads();
+  if (wave) return;
+  for (int w = 1; w < KS; ++w) {
+    const f32x4 other = __builtin_bit_cast(f32x4, ld128(uint32_t(w * 1024 + 16 * lane)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += other[e];
+  }
+  const float bias = a.bias ? a.bias[n_in] : 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) store_y(a, b0 + 4 * q + e, n, finish(acc[e], a.bias, bias));
+}
+
+// -- rows in 4 bits and back ----------------------------------------------------
+
+// Values [i, i + 8) of a row of n as fp32; those past the end read as `pad`.
+template <bool F32>
+__device__ __forceinline__ void load_f8(const char* row, int64_t i, int64_t n, float pad, float (&f)[8]) {
+  if (i + 8 <= n) {
+    if (F32) {
+      const u32x4 a = load16_any(row + 4 * i), b = load16_any(row + 4 * i + 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = bits_f32(e < 4 ? a[e] : b[e - 4]);
+    } else {
+      const u32x4 a = load16_any(row + 2 * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = bits_f32((e & 1) ? (a[e / 2] & 0xFFFF0000u) : (a[e / 2] << 16));
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    f[e] = pad;
+    if (i + e < n) {
+      if (F32) f[e] = reinterpret_cast<const float*>(row)[i + e];
+      else f[e] = bits_f32(uint32_t(reinterpret_cast<const uint16_t*>(row)[i + e]) << 16);
+    }
+  }
+}
+
+struct Q4Args {
+  const char* X;
+  uint8_t* Q;
+  char* scale;
+  char* offset;
+  int64_t rows, cols, ldx, ldq, lds, ldo;
+  int32_t st;
+  uint32_t per_row;  // workgroups of a row
+};
+
+__device__ __forceinline__ void store_scale(char* p, int64_t i, int st, float v) {
+  if (st == UW_F32) reinterpret_cast<float*>(p)[i] = v;
+  else reinterpret_cast<__bf16*>(p)[i] = static_cast<__bf16>(v);
+}
+
+__device__ __forceinline__ float as_kept(float v, int st) {
+  return st == UW_F32 ? v : static_cast<float>(static_cast<__bf16>(v));
+}
+
+// The integer nearest to the fp32 quotient t / s (ties to even), held to -8 ..
+// 7, plus 8.  inv is 1 / s rounded: the quotient is corrected by its residual,
+// which gives the rounded quotient, and where t itself is infinite (p - m past
+// the fp32 range) stays as it is.  Adding 1.5 * 2^23 + 8 rounds to the nearest
+// integer and leaves it in the low bits.
+__device__ __forceinline__ uint32_t nibble(float t, float s, float inv) {
+#pragma clang fp contract(off)
+  const float q0 = t * inv, q1 = fmaf(fmaf(-q0, s, t), inv, q0);
+  const float q = fminf(fmaxf(fabsf(q0) < 64.f ? q1 : q0, -8.f), 7.f);
+  return f32_bits(q + 12582920.f) & 15u;
+}
+
+// One thread holds 8 columns, G / 8 neighbouring lanes a group.
+template <bool F32, int G, bool OFF>
+__global__ __launch_bounds__(256) void quantize4_kernel(Q4Args a) {
+  const int64_t row = blockIdx.x / a.per_row;
+  const int64_t i = 8 * (int64_t(blockIdx.x % a.per_row) * 256 + threadIdx.x);
+  const char* x = a.X + row * a.ldx * (F32 ? 4 : 2);
+  float f[8];
+  load_f8<F32>(x, i, a.cols, 0.f, f);
+  uint32_t top = 0u;
+  float most = -INFINITY, least = INFINITY;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    top = max(top, f32_bits(f[e]) & 0x7FFFFFFFu);
+    if (OFF && i + e < a.cols) {
+      most = fmaxf(most, f[e]);
+      least = fminf(least, f[e]);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < G / 8; d *= 2) {
+    top = max(top, uint32_t(__shfl_xor(int(top), d, kWave)));
+    if (OFF) {
+      most = fmaxf(most, __shfl_xor(most, d, kWave));
+      least = fminf(least, __shfl_xor(least, d, kWave));
+    }
+  }
+  if (i >= a.cols) return;
+  const bool fine = top < 0x7F800000u;
+  float s, m = 0.f;
+  {
+#pragma clang fp contract(off)
+    if (OFF) {
+      s = as_kept(fmaxf(most / 15.f - least / 15.f, kTiny), a.st);
+      m = as_kept((least * 0.5f + most * 0.5f) + s * 0.5f, a.st);
+    } else {
+      s = as_kept(fmaxf(bits_f32(top) / 7.f, kTiny), a.st);
+    }
+  }
+  // where s nears the denormal range the residual would leave it: both are scaled up (t is at most 8 s)
+  const float up = s < 0x1p-60f ? 0x1p64f : 1.f;
+  const float su = s * up, inv = 1.f / su;
+  uint32_t w = 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = (OFF ? f[e] - m : f[e]) * up;
+    w |= (fine ? nibble(t, su, inv) : 8u) << (4 * e);
+  }
+  uint8_t* q = a.Q + row * a.ldq + i / 2;
+  if (i + 8 <= a.cols) {
+    *reinterpret_cast<uint32_t*>(q) = w;
+  } else {
+    const int left = int(a.cols - i);
+    if (left & 1) w = (w & ~(15u << (4 * left))) | 8u << (4 * left);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (2 * e < left) q[e] = uint8_t(w >> (8 * e));
+  }
+  if (i % G == 0) {
+    const int64_t g = i / G;
+    const float nan = bits_f32(0x7FC00000u);
+    store_scale(a.scale, g * a.lds + row, a.st, fine ? s : nan);
+    if (OFF) store_scale(a.offset, g * a.ldo + row, a.st, fine ? m : nan);
+  }
+}
+
+struct D4Args {
+  const uint8_t* Q;
+  const char* scale;
+  const char* offset;
+  char* Y;
+  int64_t rows, cols, ldq, lds, ldo, ldy;
+  int32_t st, yt, log_group;
+  uint32_t per_row;
+};
+
+// One thread, 8 columns: s q rounded to fp32, the offset added in a rounding
+// of its own, then rounded to Y's type.
+__global__ __launch_bounds__(256) void dequantize4_kernel(D4Args a) {
+#pragma clang fp contract(off)
+  const int64_t row = blockIdx.x / a.per_row;
+  const int64_t i = 8 * (int64_t(blockIdx.x % a.per_row) * 256 + threadIdx.x);
+  if (i >= a.cols) return;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(a.Q + row * a.ldq + i / 2) ^ 0x88888888u;
+  const int64_t g = i >> a.log_group;
+  const float s = load_scale(a.scale, g * a.lds + row, a.st);
+  const float m = a.offset ? load_scale(a.offset, g * a.ldo + row, a.st) : 0.f;
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    f[e] = float(int32_t(w << (28 - 4 * e)) >> 28) * s;
+    if (a.offset) f[e] = f[e] + m;
+  }
+  if (a.yt == UW_F32) {
+    float* y = reinterpret_cast<float*>(a.Y) + row * a.ldy + i;
+    if (i + 8 <= a.cols) {
+      __builtin_memcpy(y, f, 32);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (i + e < a.cols) y[e] = f[e];
+    }
+    return;
+  }
+  uint16_t* y = reinterpret_cast<uint16_t*>(a.Y) + row * a.ldy + i;
+  const uint32_t v[4] = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+  if (i + 8 <= a.cols) {
+    __builtin_memcpy(y, v, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (i + e < a.cols) y[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
+  }
+}
+
+// Rows that a launch takes where each is spread over per_row workgroups of
+// 256: a launch holds fewer than 2^32 threads.
+int64_t band_rows(int64_t per_row) { return ((int64_t(1) << 24) - 1) / per_row; }
+
+// A launch holds fewer than 2^32 threads.  In double: sizes below 2^40 make
+// products past 64 bits.
+int check_launch(int64_t nw, int64_t nb, int threads) {
+  if ((double(nw) * double(nb) + kXcds) * threads < 4294967296.0) return UW_OK;
+  return fail(UW_ERR_UNSUPPORTED, "uw_i4_gemm: too many tiles for one launch");
+}
+
+template <int G, bool OFF>
+int run_direct(const I4Args& a, hipStream_t s) {
+  const int64_t n_groups = (a.rows + 15) / 16, ny = (a.batch + 15) / 16;
+  const int ks = int(std::min<int64_t>(8, (a.cols + 127) / 128));
+  if (int rc = check_launch((n_groups + kXcds - 1) / kXcds * kXcds, ny, ks * kWave)) return rc;
+  const int64_t grid = (n_groups + kXcds - 1) / kXcds * kXcds * ny;
+  hipLaunchKernelGGL((i4_direct_kernel<G, OFF>), dim3(unsigned(grid)), dim3(ks * kWave), size_t(ks) * 1024, s, a,
+                     int(n_groups), int(ny), ks);
+  return hip_check(hipGetLastError(), "i4_direct_kernel launch");
+}
+
+template <int G, bool OFF>
+int run_gemm(const I4Args& a, int shape, hipStream_t s) {
+  (void)shape;
+  return run_direct<G, OFF>(a, s);
+}
+
+template <bool F32, int G, bool OFF>
+int run_quantize(const Q4Args& a, hipStream_t s) {
+  const int64_t per_row = (a.cols + 2047) / 2048, band = band_rows(per_row);
+  if (band == 0) return fail(UW_ERR_UNSUPPORTED, "uw_i4_quantize: a row wider than a launch holds");
+  for (int64_t row0 = 0; row0 < a.rows; row0 += band) {
+    Q4Args b = a;
+    const int64_t es = a.st == UW_F32 ? 4 : 2;
+    b.rows = std::min(band, a.rows - row0);
+    b.per_row = uint32_t(per_row);
+    b.X += row0 * a.ldx * (F32 ? 4 : 2);
+    b.Q += row0 * a.ldq;
+    b.scale += row0 * es;
+    if (OFF) b.offset += row0 * es;
+    hipLaunchKernelGGL((quantize4_kernel<F32, G, OFF>), dim3(unsigned(b.rows * per_row)), dim3(256), 0, s, b);
+    if (int rc = hip_check(hipGetLastError(), "quantize4_kernel launch")) return rc;
+  }
+  return UW_OK;
+}
+
+template <bool F32, int G>
+int run_quantize_form(const Q4Args& a, hipStream_t s) {
+  return a.offset ? run_quantize<F32, G, true>(a, s) : run_quantize<F32, G, false>(a, s);
+}
+
+template <bool F32>
+int run_quantize_group(const Q4Args& a, int group, hipStream_t s) {
+  return group == 32   ? run_quantize_form<F32, 32>(a, s)
+         : group == 64 ? run_quantize_form<F32, 64>(a, s)
+                       : run_quantize_form<F32, 128>(a, s);
+}
+
+}  // namespace
+
+int i4_gemm_shape_count() { return 2; }
+
+int launch_i4_gemm(const uint8_t* W, int64_t rows, int64_t cols, int64_t ldw, int group, const void* scale, int64_t lds,
+                   const void* offset, int64_t ldo, int st, const uint16_t* X, int64_t batch, int64_t ldx,
+                   const float* bias, void* Y, int64_t ldy, int yt, int shape, void* stream) {
+  // a single row has no stride
+  const I4Args a{W, static_cast<const char*>(scale), static_cast<const char*>(offset), X, bias, static_cast<char*>(Y), rows, cols,
+                 rows > 1 ? ldw : 0, lds, ldo, batch, batch > 1 ? ldx : 0, ldy, st, yt};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (group == 32) return offset ? run_gemm<32, true>(a, shape, s) : run_gemm<32, false>(a, shape, s);
+  if (group == 64) return offset ? run_gemm<64, true>(a, shape, s) : run_gemm<64, false>(a, shape, s);
+  return offset ? run_gemm<128, true>(a, shape, s) : run_gemm<128, false>(a, shape, s);
+}
+
+int launch_i4_quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, int xt, int group, uint8_t* Q, int64_t ldq,
+                       void* scale, int64_t lds, void* offset, int64_t ldo, int st, void* stream) {
+  const Q4Args a{static_cast<const char*>(X), Q, static_cast<char*>(scale), static_cast<char*>(offset), rows, cols, ldx, ldq,
+                 lds, ldo, st, 0};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return xt == UW_F32 ? run_quantize_group<true>(a, group, s) : run_quantize_group<false>(a, group, s);
+}
+
+int launch_i4_dequantize(const uint8_t* Q, int64_t rows, int64_t cols, int64_t ldq, int group, const void* scale, int64_t lds,
+                         const void* offset, int64_t ldo, int st, void* Y, int64_t ldy, int yt, void* stream) {
+  const int64_t per_row = (cols + 2047) / 2048, band = band_rows(per_row);
+  if (band == 0) return fail(UW_ERR_UNSUPPORTED, "uw_i4_dequantize: a row wider than a launch holds");
+  const int64_t es = st == UW_F32 ? 4 : 2;
+  for (int64_t row0 = 0; row0 < rows; row0 += band) {
+    const D4Args a{Q + row0 * ldq, static_cast<const char*>(scale) + row0 * es,
+                   offset ? static_cast<const char*>(offset) + row0 * es : nullptr,
+                   static_cast<char*>(Y) + row0 * ldy * int64_t(elem_size(yt)), std::min(band, rows - row0), cols, ldq, lds, ldo,
+                   ldy, st, yt, group == 32 ? 5 : group == 64 ? 6 : 7, uint32_t(per_row)};
+    hipLaunchKernelGGL(dequantize4_kernel, dim3(unsigned(a.rows * per_row)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+    if (int rc = hip_check(hipGetLastError(), "dequantize4_kernel launch")) return rc;
+  }
+  return UW_OK;
+}
+
+}  // namespace uw

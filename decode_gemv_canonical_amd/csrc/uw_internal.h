@@ -186,6 +186,21 @@ int launch_i8_gemm(const int8_t* W, int64_t rows, int64_t cols, int64_t ldw, con
                    int shape, int ks, void* stream);
 int i8_gemm_shape_count();
 bool i8_gemm_shape_ok(const int8_t* W, int64_t rows, int64_t ldw, const int8_t* X, int64_t batch, int64_t ldx, int shape);
+// The norms around a block with its gate and residual (uw_rows.hip), and
+// 4-bit weights (uw_i4.hip).  ldg == 0: one row of gates for every token.
+int launch_block_norm(const void* X, int64_t batch, int64_t cols, int64_t ldx, int xt, bool post_norm, const void* post,
+                      int pt, float post_eps, const void* gate, int64_t ldg, int gt, float block_scale, const void* R,
+                      int64_t ldr, int rt, float residual_scale, void* H, int64_t ldh, const void* gain, int nt, float eps,
+                      void* Y, int64_t ldy, int yt, float* scale, void* stream);
+int launch_i4_quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, int xt, int group, uint8_t* Q, int64_t ldq,
+                       void* scale, int64_t lds, void* offset, int64_t ldo, int st, void* stream);
+int launch_i4_dequantize(const uint8_t* Q, int64_t rows, int64_t cols, int64_t ldq, int group, const void* scale,
+                         int64_t lds, const void* offset, int64_t ldo, int st, void* Y, int64_t ldy, int yt, void* stream);
+// shape: 0 = heuristic, else an index below i4_gemm_shape_count().
+int launch_i4_gemm(const uint8_t* W, int64_t rows, int64_t cols, int64_t ldw, int group, const void* scale, int64_t lds,
+                   const void* offset, int64_t ldo, int st, const uint16_t* X, int64_t batch, int64_t ldx,
+                   const float* bias, void* Y, int64_t ldy, int yt, int shape, void* stream);
+int i4_gemm_shape_count();
 // Cache eviction of the autotuner: read `bytes` (multiple of 16) at src.
 int launch_read_probe(const void* src, size_t bytes, void* sink, void* stream);
 // The allocation-free entry point's scratch (uw_static.hip): its size, the

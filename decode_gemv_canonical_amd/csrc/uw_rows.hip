@@ -160,7 +160,9 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 }
 
 // Sum and maximum over the NT threads of a row; every thread gets both.
-template <int NT>
+// SLOT: a kernel that reduces twice uses two places in LDS, so that no barrier
+// is needed between the reads of one and the writes of the next.
+template <int NT, int SLOT = 0>
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
   sum = wave_sum(sum);
   top = wave_max(top);
@@ -490,6 +492,276 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const int8_t* __restric
   }
 }
 
+// The join of two blocks: the norm after one, its gate, the residual's
+// addition, the norm before the next.
+//   p = x * rstd(x) * post        (the norm after the block; or p = x)
+//   h = keep * r + (branch * gate) * p, rounded to r's type
+//   y = h * rstd(h) * gain        (the norm before the next; or none)
+// with rstd(v) = 1 / sqrt(mean(v^2) + eps), y as in the norm above.  A row is
+// held in registers from its one read of x and r to its writes, with two
+// reductions over it in between.
+struct BlockArgs {  // 112 bytes, as RowArgs
+  const char* x;
+  const char* r;
+  const char* post;
+  const char* gate;
+  const char* gain;
+  char* h;  // may be null
+  char* y;  // may be null
+  float* scale;
+  int32_t rows, cols;
+  uint32_t ldx, ldr, ldg, ldh, ldy;  // in elements; ldg 0: one row for all
+  float post_eps, eps, keep, branch;
+  uint8_t pt, gt, nt, flags;
+};
+static_assert(sizeof(BlockArgs) == 112, "kernel arguments");
+enum BlockFlags { kPostNorm = 1, kYF32 = 2, kStreamPastCaches = 4 };
+
+__device__ __forceinline__ void load_as(const char* row, int type, int64_t i, int64_t n, float (&f)[8]) {
+  if (type == UW_F32) unpack8<kF32>(load8<kF32>(row, i, n), f);
+  else unpack8<kBf16>(load8<kBf16>(row, i, n), f);
+}
+
+// h of one chunk from x (in p) and r; p receives h as it is kept.
+template <int RT>
+__device__ __forceinline__ void join8(const BlockArgs& a, float rstd, const char* gate, int64_t i, const Raw8& rr, float (&p)[8]) {
+  float v[8];
+  if (a.flags & kPostNorm) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] *= rstd;
+    if (a.post) {
+      load_as(a.post, a.pt, i, a.cols, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] *= v[e];
+    }
+  }
+  if (gate) {
+    load_as(gate, a.gt, i, a.cols, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] *= a.branch * v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] *= a.branch;
+  }
+  unpack8<RT>(rr, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = fmaf(a.keep, v[e], p[e]);
+  if (RT == kBf16) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = static_cast<float>(static_cast<__bf16>(p[e]));
+  }
+}
+
+template <int XT, int RT, bool I8, int NT, int VPT>
+__global__ __launch_bounds__(NT == kWave ? 256 : NT) void block_kernel(BlockArgs a) {
+  constexpr int kRowsPer = NT == kWave ? 4 : 1;
+  constexpr int kXs = XT == kF32 ? 4 : 2, kRs = RT == kF32 ? 4 : 2;
+  const int t = int(threadIdx.x) % NT;
+  const int64_t row = int64_t(blockIdx.x) * kRowsPer + (NT == kWave ? int(threadIdx.x) / kWave : 0);
+  if (row >= a.rows) return;  // whole waves, and no barrier follows where a workgroup holds several rows
+  const char* x = a.x + row * a.ldx * kXs;
+  const char* r = a.r + row * a.ldr * kRs;
+  const char* gate = a.gate ? a.gate + row * a.ldg * (a.gt == UW_F32 ? 4 : 2) : nullptr;
+  char* h = a.h ? a.h + row * a.ldh * kRs : nullptr;
+  Raw8 xr[VPT], rr[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int64_t i = 8 * (t + int64_t(j) * NT);
+    xr[j] = load8<XT>(x, i, a.cols);
+    rr[j] = load8<RT>(r, i, a.cols);
+  }
+  float p[VPT][8];
+  float sum = 0.f, rstd = 1.f;
+  uint32_t top = 0u;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    float part = 0.f;
+    unpack8<XT>(xr[j], p[j]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part = fmaf(p[j][e], p[j][e], part);
+    sum += part;
+  }
+  const float n = float(a.cols);
+  if (a.flags & kPostNorm) {
+    row_reduce<NT, 0>(sum, top);
+    rstd = 1.f / sqrtf(fmaf(sum, 1.f / n, a.post_eps));
+  }
+  sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int64_t i = 8 * (t + int64_t(j) * NT);
+    join8<RT>(a, rstd, gate, i, rr[j], p[j]);
+    if (h) store8(h, RT, i, a.cols, p[j], a.flags & kStreamPastCaches);
+  }
+  if (!a.y) return;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int64_t i = 8 * (t + int64_t(j) * NT);
+    float part = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // past the end x and r read as zero, but a product may be NaN where the row's rstd is
+      if (i + e >= a.cols) p[j][e] = 0.f;
+      part = fmaf(p[j][e], p[j][e], part);
+    }
+    sum += part;
+    if (a.gain) {
+      float g[8];
+      load_as(a.gain, a.nt, i, a.cols, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[j][e] *= g[e];
+    }
+    if (I8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, f32_bits(p[j][e]) & 0x7FFFFFFFu);
+    }
+  }
+  row_reduce<NT, 1>(sum, top);
+  rstd = 1.f / sqrtf(fmaf(sum, 1.f / n, a.eps));
+  if (I8) {
+    float s, inv;
+    const bool fine = row_scale(top, s, inv);
+    int8_t* q = reinterpret_cast<int8_t*>(a.y) + row * a.ldy;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) store_q8(q, 8 * (t + int64_t(j) * NT), a.cols, p[j], inv, fine);
+    if (t == 0) a.scale[row] = fine ? s * rstd : bits_f32(0x7FC00000u);
+  } else {
+    const int yt = a.flags & kYF32 ? UW_F32 : UW_BF16;
+    char* y = a.y + row * a.ldy * (yt == UW_F32 ? 4 : 2);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[j][e] *= rstd;
+      store8(y, yt, 8 * (t + int64_t(j) * NT), a.cols, p[j]);
+    }
+  }
+}
+
+// Rows past the register form's 32768 values: a pass for the first norm's sum,
+// one that writes h, and one for y, which reads h back where it was kept and
+// computes it again where not.
+template <int XT, int RT, bool I8>
+__global__ __launch_bounds__(1024) void long_block_kernel(BlockArgs a) {
+  constexpr int NT = 1024;
+  constexpr int kXs = XT == kF32 ? 4 : 2, kRs = RT == kF32 ? 4 : 2;
+  const int64_t row = blockIdx.x, cols = a.cols;
+  const int t = threadIdx.x;
+  const char* x = a.x + row * a.ldx * kXs;
+  const char* r = a.r + row * a.ldr * kRs;
+  const char* gate = a.gate ? a.gate + row * a.ldg * (a.gt == UW_F32 ? 4 : 2) : nullptr;
+  char* h = a.h ? a.h + row * a.ldh * kRs : nullptr;
+  const float n = float(a.cols);
+  float p[8], rstd = 1.f, sum;
+  uint32_t top = 0u;
+  if (a.flags & kPostNorm) {
+    double squares = 0.;
+    for (int64_t i = 8 * t; i < cols; i += 8 * NT) {
+      unpack8<XT>(load8<XT>(x, i, cols), p);
+      float part = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part = fmaf(p[e], p[e], part);
+      squares += double(part);
+    }
+    sum = float(squares);
+    row_reduce<NT, 0>(sum, top);
+    rstd = 1.f / sqrtf(fmaf(sum, 1.f / n, a.post_eps));
+  }
+  // h of a chunk, times the gain; its squares
+  auto chunk = [&](int64_t i, bool kept, float& part) {
+    if (kept) {
+      unpack8<RT>(load8<RT>(h, i, cols), p);
+    } else {
+      unpack8<XT>(load8<XT>(x, i, cols), p);
+      join8<RT>(a, rstd, gate, i, load8<RT>(r, i, cols), p);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (i + e >= cols) p[e] = 0.f;
+      part = fmaf(p[e], p[e], part);
+    }
+  };
+  auto times_gain = [&](int64_t i) {
+    if (!a.gain) return;
+    float g[8];
+    load_as(a.gain, a.nt, i, cols, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] *= g[e];
+  };
+  double squares = 0.;
+  for (int64_t i = 8 * t; i < cols; i += 8 * NT) {
+    float part = 0.f;
+    chunk(i, false, part);
+    if (h) store8(h, RT, i, cols, p, a.flags & kStreamPastCaches);
+    squares += double(part);
+    if (!a.y) continue;
+    times_gain(i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, f32_bits(p[e]) & 0x7FFFFFFFu);
+  }
+  if (!a.y) return;
+  sum = float(squares);
+  row_reduce<NT, 1>(sum, top);
+  const float rstd2 = 1.f / sqrtf(fmaf(sum, 1.f / n, a.eps));
+  float s, inv, unused = 0.f;
+  const bool fine = row_scale(top, s, inv);
+  for (int64_t i = 8 * t; i < cols; i += 8 * NT) {
+    chunk(i, h != nullptr, unused);
+    times_gain(i);
+    if (I8) {
+      store_q8(reinterpret_cast<int8_t*>(a.y) + row * a.ldy, i, cols, p, inv, fine);
+    } else {
+      const int yt = a.flags & kYF32 ? UW_F32 : UW_BF16;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] *= rstd2;
+      store8(a.y + row * a.ldy * (yt == UW_F32 ? 4 : 2), yt, i, cols, p);
+    }
+  }
+  if (I8 && t == 0) a.scale[row] = fine ? s * rstd2 : bits_f32(0x7FC00000u);
+}
+
+// Strides and the row count of a band pass through 32 bits; pointers do not.
+struct BlockRows {
+  BlockArgs a;
+  int64_t rows, ldx, ldr, ldg, ldh, ldy;
+};
+
+template <int XT, int RT, bool I8>
+int run_block(const BlockRows& b, hipStream_t s) {
+  constexpr int64_t kBand = int64_t(1) << 21;  // as run_rows
+  constexpr int kXs = XT == kF32 ? 4 : 2, kRs = RT == kF32 ? 4 : 2;
+  const int64_t chunks = (int64_t(b.a.cols) + 7) / 8;
+  auto go = [&](auto kern, int threads, int rows_per) {
+    for (int64_t row0 = 0; row0 < b.rows; row0 += kBand) {
+      BlockArgs a = b.a;
+      a.rows = int32_t(std::min(kBand, b.rows - row0));
+      a.x += row0 * b.ldx * kXs;
+      a.r += row0 * b.ldr * kRs;
+      if (a.gate) a.gate += row0 * b.ldg * int64_t(elem_size(a.gt));
+      if (a.h) a.h += row0 * b.ldh * kRs;
+      if (a.y) a.y += row0 * b.ldy * (I8 ? 1 : a.flags & kYF32 ? 4 : 2);
+      if (I8) a.scale += row0;
+      hipLaunchKernelGGL(kern, dim3(unsigned((a.rows + rows_per - 1) / rows_per)), dim3(threads), 0, s, a);
+      if (int rc = hip_check(hipGetLastError(), "block_kernel launch")) return rc;
+    }
+    return int(UW_OK);
+  };
+  // the norm's threads and chunks (run_rows)
+  if (chunks <= 64) return go(block_kernel<XT, RT, I8, 64, 1>, 256, 4);
+  if (chunks <= 128) return go(block_kernel<XT, RT, I8, 64, 2>, 256, 4);
+  if (chunks <= 256) return go(block_kernel<XT, RT, I8, 256, 1>, 256, 1);
+  if (chunks <= 512 && b.rows > 1024) return go(block_kernel<XT, RT, I8, 256, 2>, 256, 1);
+  if (chunks <= 512) return go(block_kernel<XT, RT, I8, 512, 1>, 512, 1);
+  if (chunks <= 1024) return go(block_kernel<XT, RT, I8, 1024, 1>, 1024, 1);
+  if (chunks <= 2048) return go(block_kernel<XT, RT, I8, 1024, 2>, 1024, 1);
+  if (chunks <= 4096) return go(block_kernel<XT, RT, I8, 1024, 4>, 1024, 1);
+  return go(long_block_kernel<XT, RT, I8>, 1024, 1);
+}
+
+template <int XT, int RT>
+int run_block_out(const BlockRows& b, bool i8, hipStream_t s) {
+  return i8 ? run_block<XT, RT, true>(b, s) : run_block<XT, RT, false>(b, s);
+}
+
 }  // namespace
 
 int launch_rmsnorm(const void* X, int64_t batch, int64_t cols, int64_t ldx, int xt, const void* R, int64_t ldr, int rt,
@@ -533,6 +805,27 @@ int launch_i8_dequantize(const int8_t* Q, int64_t rows, int64_t cols, int64_t ld
     if (int rc = hip_check(hipGetLastError(), "dequantize_kernel launch")) return rc;
   }
   return UW_OK;
+}
+
+int launch_block_norm(const void* X, int64_t batch, int64_t cols, int64_t ldx, int xt, bool post_norm, const void* post,
+                      int pt, float post_eps, const void* gate, int64_t ldg, int gt, float block_scale, const void* R,
+                      int64_t ldr, int rt, float residual_scale, void* H, int64_t ldh, const void* gain, int nt, float eps,
+                      void* Y, int64_t ldy, int yt, float* scale, void* stream) {
+  // a single row has no stride
+  if (batch == 1) ldx = ldr = ldg = ldh = ldy = 0;
+  if (cols >= (int64_t(1) << 31) || std::max({ldx, ldr, ldg, ldh, ldy}) >= (int64_t(1) << 32))
+    return fail(UW_ERR_UNSUPPORTED, "uw_block_norm: rows of 2^31 columns or strides of 2^32 elements");
+  const bool i8 = Y && yt == UW_I8;
+  const bool past = batch * cols * int64_t(elem_size(rt)) >= kStreamPast;
+  const BlockArgs a{static_cast<const char*>(X), static_cast<const char*>(R), static_cast<const char*>(post),
+                    static_cast<const char*>(gate), static_cast<const char*>(gain), static_cast<char*>(H),
+                    static_cast<char*>(Y), scale, 0, int32_t(cols), uint32_t(ldx), uint32_t(ldr), uint32_t(ldg),
+                    uint32_t(ldh), uint32_t(ldy), post_eps, eps, residual_scale, block_scale, uint8_t(pt), uint8_t(gt),
+                    uint8_t(nt), uint8_t((post_norm ? kPostNorm : 0) | (Y && yt == UW_F32 ? kYF32 : 0) | (past ? kStreamPastCaches : 0))};
+  const BlockRows b{a, batch, ldx, ldr, ldg, ldh, ldy};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rt == UW_F32) return xt == UW_F32 ? run_block_out<kF32, kF32>(b, i8, s) : run_block_out<kBf16, kF32>(b, i8, s);
+  return xt == UW_F32 ? run_block_out<kF32, kBf16>(b, i8, s) : run_block_out<kBf16, kBf16>(b, i8, s);
 }
 
 }  // namespace uw

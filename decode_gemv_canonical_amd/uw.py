@@ -116,6 +116,13 @@ def _load() -> ctypes.CDLL:
         "uw_i8_gemm": (I, [P, I64, I64, I64, P, P, I64, I64, P, P, P, I64, I, P]),
         "uw_i8_gemm_shaped": (I, [P, I64, I64, I64, P, P, I64, I64, P, P, P, I64, I, I, I, P]),
         "uw_i8_gemm_shape_count": (I, []),
+        "uw_block_norm": (I, [P, I64, I64, I64, I, I, P, I, ctypes.c_float, P, I64, I, ctypes.c_float, P, I64, I,
+                              ctypes.c_float, P, I64, P, I, ctypes.c_float, P, I64, I, P, P]),
+        "uw_i4_quantize": (I, [P, I64, I64, I64, I, I, P, I64, P, I64, P, I64, I, P]),
+        "uw_i4_dequantize": (I, [P, I64, I64, I64, I, P, I64, P, I64, I, P, I64, I, P]),
+        "uw_i4_gemm": (I, [P, I64, I64, I64, I, P, I64, P, I64, I, P, I64, I64, P, P, I64, I, P]),
+        "uw_i4_gemm_shaped": (I, [P, I64, I64, I64, I, P, I64, P, I64, I, P, I64, I64, P, P, I64, I, I, P]),
+        "uw_i4_gemm_shape_count": (I, []),
         "uw_sched_create": (I, [P, SZ, I, I, ctypes.POINTER(P)]),
         "uw_sched_destroy": (None, [P]),
         "uw_sched_decode_cus": (I, [P]),
@@ -616,7 +623,8 @@ def _ops():
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_uw_torch", loader))
         loader.exec_module(mod)
         mod.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
-            "uw_rmsnorm", "uw_silu_mul", "uw_i8_quantize", "uw_i8_dequantize", "uw_i8_gemm", "uw_i8_gemm_shaped")))
+            "uw_rmsnorm", "uw_silu_mul", "uw_i8_quantize", "uw_i8_dequantize", "uw_i8_gemm", "uw_i8_gemm_shaped",
+            "uw_block_norm", "uw_i4_quantize", "uw_i4_dequantize", "uw_i4_gemm", "uw_i4_gemm_shaped")))
         _torch_side = mod
     return _torch_side
 
@@ -721,6 +729,117 @@ class Int8Matrix:
             Y = _output((X.shape[0], self.rows), out_dtype or torch.float32, X.device, stream)
         uw_i8_gemm(self.q, self.scale, X, x_scale, Y, bias, stream)
         return Y
+
+
+# -- the norms around a block, and 4-bit weights ---------------------------------
+
+def uw_block_norm(X, residual, post_gain=None, gate=None, residual_out=None, gain=None, Y=None, scale=None,
+                  post_norm: bool = True, block_scale: float = 1.0, residual_scale: float = 1.0, eps: float = 1e-5,
+                  post_eps: float | None = None, stream=None) -> None:
+    """The join of two blocks: p = X / sqrt(mean(X^2) + post_eps) * post_gain
+    (p = X without post_norm), h = residual_scale * residual + block_scale *
+    gate * p, Y = h / sqrt(mean(h^2) + eps) * gain, per row.  gate is a vector
+    (one for every token) or a row per token; gains and gate may be None (all
+    ones).  residual_out receives h in the residual's dtype (the residual itself
+    updates the stream in place); Y and `scale` as for uw_rmsnorm, or None: no
+    norm follows.  post_eps defaults to eps."""
+    rc = (_torch_side or _ops()).block_norm(X, residual, post_norm, post_gain, eps if post_eps is None else post_eps, gate,
+                                            block_scale, residual_scale, residual_out, gain, eps, Y, scale, stream)
+    if rc:
+        _check(rc, "uw_block_norm")
+
+
+def uw_i4_quantize(X, Q, scale, offset=None, group: int = 128, stream=None) -> None:
+    """Rows of X (float32 or bfloat16) as 4-bit integers, two to a byte of Q
+    (uint8 [rows, ceil(cols / 2)], rows at multiples of 16 bytes: i4_rows), with
+    scale [ceil(cols / group), rows], and offset like it in the affine form,
+    float32 or bfloat16; group is 32, 64 or 128 columns."""
+    rc = (_torch_side or _ops()).quantize4(X, Q, scale, offset, group, stream)
+    if rc:
+        _check(rc, "uw_i4_quantize")
+
+
+def uw_i4_dequantize(Q, scale, Y, offset=None, group: int = 128, stream=None) -> None:
+    """Y = scale * q (+ offset), float32 or bfloat16."""
+    rc = (_torch_side or _ops()).dequantize4(Q, scale, Y, offset, group, stream)
+    if rc:
+        _check(rc, "uw_i4_dequantize")
+
+
+def uw_i4_gemm(W, scale, X, Y, offset=None, group: int = 128, bias=None, stream=None) -> None:
+    """Y[b, n] = sum_k X[b, k] W[n, k] (+ bias[n]) over 4-bit weights as
+    uw_i4_quantize writes them, bfloat16 X [batch, cols], float32 bias, Y float32
+    or bfloat16."""
+    rc = (_torch_side or _ops()).gemm4(W, scale, X, Y, offset, group, bias, stream)
+    if rc:
+        _check(rc, "uw_i4_gemm")
+
+
+def uw_i4_gemm_shaped(W, scale, X, Y, shape: int, offset=None, group: int = 128, bias=None, stream=None) -> None:
+    rc = (_torch_side or _ops()).gemm4_shaped(W, scale, X, Y, offset, group, bias, shape, stream)
+    if rc:
+        _check(rc, "uw_i4_gemm_shaped")
+
+
+def uw_i4_gemm_shape_count() -> int:
+    return _lib.uw_i4_gemm_shape_count()
+
+
+def i4_rows(rows: int, cols: int, device="cuda"):
+    """An uninitialised uint8 [rows, ceil(cols / 2)] for packed 4-bit rows of
+    cols integers: rows start at multiples of 16 bytes and hold whole 16-byte
+    words."""
+    import torch
+    return torch.empty(rows, (cols + 31) // 32 * 16, dtype=torch.uint8, device=device)[:, : (cols + 1) // 2]
+
+
+class Int4Matrix:
+    """A weight matrix in 4 bits with a scale (and an offset, where the form is
+    affine) per group of columns, on the current CUDA device.  An output that is
+    not passed in is allocated under `stream`."""
+
+    def __init__(self, q, scale, offset=None, cols: int | None = None, group: int = 128):
+        self.q, self.scale, self.offset, self.group = q, scale, offset, group
+        self.rows, self.cols = q.shape[0], 2 * q.shape[1] if cols is None else cols
+
+    @classmethod
+    def from_weights(cls, W, group: int = 128, affine: bool = False, scale_dtype=None) -> "Int4Matrix":
+        """From a float32 or bfloat16 [rows, cols] on the device; scales are
+        bfloat16 unless scale_dtype says float32."""
+        import torch
+        rows, cols = W.shape
+        q = i4_rows(rows, cols, device=W.device)
+        scale = torch.empty((cols + group - 1) // group, rows, dtype=scale_dtype or torch.bfloat16, device=W.device)
+        offset = torch.empty_like(scale) if affine else None
+        uw_i4_quantize(W, q, scale, offset, group)
+        return cls(q, scale, offset, cols, group)
+
+    @classmethod
+    def from_compressed(cls, m, group: int = 128, affine: bool = False, scale_dtype=None) -> "Int4Matrix":
+        """From a CompressedMatrix or PaletteMatrix (decompressed once, on the current stream)."""
+        return cls.from_weights(m.decompress(), group, affine, scale_dtype)
+
+    def dequantize(self, out=None, out_dtype=None, stream=None):
+        import torch
+        if out is None:
+            out = _output((self.rows, self.cols), out_dtype or torch.bfloat16, self.q.device, stream)
+        uw_i4_dequantize(self.q, self.scale, out, self.offset, self.group, stream)
+        return out
+
+    def gemm(self, X, Y=None, bias=None, out_dtype=None, stream=None):
+        import torch
+        if Y is None:
+            Y = _output((X.shape[0], self.rows), out_dtype or torch.float32, X.device, stream)
+        uw_i4_gemm(self.q, self.scale, X, Y, self.offset, self.group, bias, stream)
+        return Y
+
+    def gemv(self, x, y=None, bias=None, out_dtype=None, stream=None):
+        """One token: x of cols elements, y of rows elements."""
+        import torch
+        if y is None:
+            y = _output((self.rows,), out_dtype or torch.float32, x.device, stream)
+        uw_i4_gemm(self.q, self.scale, x.unsqueeze(0), y.unsqueeze(0), self.offset, self.group, bias, stream)
+        return y
 
 
 class DecodeAhead:

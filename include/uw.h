@@ -687,6 +687,115 @@ int uw_i8_gemm_shaped(const int8_t* d_W, int64_t rows, int64_t cols, int64_t ldw
 /* Number of shape ids of uw_i8_gemm_shaped (shape 0 is the automatic one). */
 int uw_i8_gemm_shape_count(void);
 
+/*
+ * uw_block_norm (device) - the join of two blocks in one pass: the norm after a
+ * block, its gate, the residual's addition, and the norm before the next.
+ *   p = x / sqrt(mean(x^2) + post_eps) * post   (post_norm != 0; else p = x)
+ *   h = residual_scale * r + block_scale * gate * p
+ *   y = h / sqrt(mean(h^2) + eps) * gain
+ * row by row in fp32 arithmetic; h is rounded to the residual's type before it
+ * is squared.  uw_rmsnorm is its case without the first norm, gate and scales.
+ *   d_X      the block's output: batch rows of cols >= 1 elements of xt (UW_F32
+ *            or UW_BF16), row stride ldx.
+ *   d_post   cols elements of pt, or NULL (all ones); needs post_norm.
+ *   post_eps positive and finite where post_norm is set, else ignored.
+ *   d_gate   rows of cols elements of gt, stride ldg, a row per token; with
+ *            ldg == 0 one row for every token; or NULL (all ones).
+ *   block_scale, residual_scale  finite.
+ *   d_R      the residual, rows of rt, stride ldr.
+ *   d_H      receives h in rt, stride ldh; NULL: not kept.  May be d_R itself
+ *            (the stream updated in place) or d_X.
+ *   d_Y      receives y in yt, stride ldy, with d_scale, as for uw_rmsnorm; may
+ *            be d_X or d_R itself where d_H is not the same too.  NULL: no norm
+ *            follows (then eps, yt and d_scale are ignored, and d_gain must be
+ *            NULL).  d_H or d_Y has to be given.
+ *   d_gain   cols elements of nt, or NULL (all ones).
+ * Gains and gates are UW_F32 or UW_BF16.  A row whose squares sum past the fp32
+ * range comes out of its norm as zeros.
+ * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (2^31 columns or more, strides of
+ *         2^32 or more), UW_ERR_HIP.
+ */
+int uw_block_norm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int xt, int post_norm, const void* d_post,
+                  int pt, float post_eps, const void* d_gate, int64_t ldg, int gt, float block_scale, const void* d_R,
+                  int64_t ldr, int rt, float residual_scale, void* d_H, int64_t ldh, const void* d_gain, int nt, float eps,
+                  void* d_Y, int64_t ldy, int yt, float* d_scale, void* stream);
+
+/*
+ * Weights in 4 bits: integers q in -8 .. 7 with a scale, and in the affine form
+ * an offset, per row and group of 32, 64 or 128 columns:
+ *   W[n, k] = scale[k / group, n] * q[n, k] (+ offset[k / group, n])
+ * (the last group of a row may be short).  A row's integers lie two to a byte
+ * as q + 8, the even column in the low half; rows start at 16-byte boundaries
+ * (d_Q 16-byte aligned, ldq in bytes, a multiple of 16 and at least 16 *
+ * ceil(cols / 32)), and whole 16-byte words of a row are read, whatever lies
+ * past its last column.  Scales and offsets lie group by group: ceil(cols /
+ * group) rows of `rows` elements of st (UW_F32 or UW_BF16) with strides lds and
+ * ldo.  So the weights of a row-major [rows, cols / 8] int32 matrix of unsigned
+ * nibbles u with scales s and zero points z are d_Q as it is, s, and
+ * offset = s * (8 - z).
+ *
+ * The remarks on the 8-bit path above hold here: no handle, no workspace, and
+ * outputs that overlap an input are refused.
+ */
+
+/*
+ * uw_i4_quantize (device) - rows of xt (UW_F32 or UW_BF16) in 4 bits.  Of a
+ * group p, in fp32, each step rounded:
+ *   d_offset NULL: s = max(max|p| / 7, 2^-126);
+ *   else: s = max(max p / 15 - min p / 15, 2^-126), m = (min p / 2 + max p / 2) + s / 2;
+ * s is rounded to st before it is used, and so is m; q is the quotient p / s
+ * (or (p - m) / s) rounded to nearest, ties to even, and held to -8 .. 7.
+ * A group that holds an infinity or a NaN gets q = 0 and NaN for its scale and
+ * offset.  The byte that holds the last column of an odd number has 8 in its
+ * other half; nothing is written past it.
+ * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (more than 2^35 - 2048 columns),
+ *         UW_ERR_HIP.
+ */
+int uw_i4_quantize(const void* d_X, int64_t rows, int64_t cols, int64_t ldx, int xt, int group, uint8_t* d_Q, int64_t ldq,
+                   void* d_scale, int64_t lds, void* d_offset, int64_t ldo, int st, void* stream);
+
+/*
+ * uw_i4_dequantize (device) - the values 4-bit rows stand for, in yt (UW_F32, or
+ * UW_BF16 rounded to nearest even), stride ldy >= cols: scale * q rounded to
+ * fp32, the offset added in a rounding of its own.  d_offset may be NULL.
+ * Errors: as uw_i4_quantize.
+ */
+int uw_i4_dequantize(const uint8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq, int group, const void* d_scale,
+                     int64_t lds, const void* d_offset, int64_t ldo, int st, void* d_Y, int64_t ldy, int yt, void* stream);
+
+/*
+ * uw_i4_gemm (device) - Y[b, n] = sum_k X[b, k] W[n, k] (+ bias[n]) over 4-bit
+ * weights, on the matrix cores, for any number of tokens:
+ *   Y = sum over groups of scale * (sum of q x) + offset * (sum of x).
+ * Products are exact, every sum is fp32; only Y is rounded further.
+ *   d_W, ldw, group, scales and offsets as above (d_offset may be NULL).
+ *   d_X   batch rows of cols bf16 elements, stride ldx >= cols; rows on
+ *         16-byte boundaries (ldx a multiple of 8) are read fastest.
+ *   d_bias  rows fp32 values, or NULL.
+ *   d_Y   batch rows of `rows` elements of yt (UW_F32 or UW_BF16), stride ldy.
+ * Results depend on the batch and the sizes (the order of the sum), not on
+ * anything else; an infinity or a NaN in a token shows in that token's row
+ * alone.  With offsets an infinite activation may give NaN where scale * q +
+ * offset times it is infinite.
+ * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (more tiles than a launch holds),
+ *         UW_ERR_HIP.
+ */
+int uw_i4_gemm(const uint8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, int group, const void* d_scale, int64_t lds,
+               const void* d_offset, int64_t ldo, int st, const uint16_t* d_X, int64_t batch, int64_t ldx,
+               const float* d_bias, void* d_Y, int64_t ldy, int yt, void* stream);
+
+/*
+ * uw_i4_gemm_shaped (device) - uw_i4_gemm with a given shape: shape in
+ * [1, uw_i4_gemm_shape_count()) picks the weight and batch rows a workgroup
+ * holds and how the operands reach the matrix cores.
+ * Errors: as uw_i4_gemm; UW_ERR_INVALID for an unknown shape.
+ */
+int uw_i4_gemm_shaped(const uint8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, int group, const void* d_scale,
+                      int64_t lds, const void* d_offset, int64_t ldo, int st, const uint16_t* d_X, int64_t batch,
+                      int64_t ldx, const float* d_bias, void* d_Y, int64_t ldy, int yt, int shape, void* stream);
+/* Number of shape ids of uw_i4_gemm_shaped (shape 0 is the automatic one). */
+int uw_i4_gemm_shape_count(void);
+
 #ifdef __cplusplus
 }
 #endif
