@@ -119,6 +119,32 @@ __device__ inline void load_lds16_stream(const void* src, uint32_t dst) {
   __builtin_amdgcn_global_load_lds((global_void*)(const_cast<void*>(src)), (lds_void*)(size_t(dst)), 16, 0, 2);
 }
 
+// 16 bytes per lane from the buffer resource at byte voff + soff into LDS at
+// m0 + 16 * lane (all lanes active).  NT: non-temporal, for operands that are
+// read once.
+template <bool NT>
+__device__ __forceinline__ void stage_load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t m0) {
+  if (NT) {
+    asm volatile(
+        "s_nop 4\n"
+        "s_mov_b32 m0, %[m]\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %[v], %[r], %[s] offen nt lds"
+        :
+        : [m] "s"(__builtin_amdgcn_readfirstlane(m0)), [v] "v"(voff), [r] "s"(r), [s] "s"(__builtin_amdgcn_readfirstlane(soff))
+        : "memory");
+  } else {
+    asm volatile(
+        "s_nop 4\n"
+        "s_mov_b32 m0, %[m]\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %[v], %[r], %[s] offen lds"
+        :
+        : [m] "s"(__builtin_amdgcn_readfirstlane(m0)), [v] "v"(voff), [r] "s"(r), [s] "s"(__builtin_amdgcn_readfirstlane(soff))
+        : "memory");
+  }
+}
+
 // Words read by the whole wave go through the constant address space so they
 // become scalar loads.
 typedef __attribute__((address_space(4))) const uint32_t const_word;

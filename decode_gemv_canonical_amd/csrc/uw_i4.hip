@@ -52,14 +52,17 @@ __device__ __forceinline__ float load_scale(const char* p, int64_t i, int st) {
   return bits_f32(uint32_t(reinterpret_cast<const uint16_t*>(p)[i]) << 16);
 }
 
-// q / 16 of eight nibbles q + 8, in bf16, in order.
+// q / 16 of eight nibbles q + 8, in bf16, in order: 14 operations.  The odd
+// nibbles' word is kept apart, so that the conversions take their bytes from
+// the two words by themselves instead of shifting each (18 operations).
 __device__ __forceinline__ bf16x8 decode8(uint32_t w) {
   w ^= 0x88888888u;  // two's complement
-  const uint32_t h = w >> 4;
+  uint32_t h = w >> 4;
+  asm("" : "+v"(h));
   u32x4 v;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    v[i] = pack_bf16(__builtin_amdgcn_cvt_off_f32_i4(int(w >> (8 * i))), __builtin_amdgcn_cvt_off_f32_i4(int(h >> (8 * i))));
+    v[i] = pack_bf16(__builtin_amdgcn_cvt_off_f32_i4(int(w >> (8 * i) & 255u)), __builtin_amdgcn_cvt_off_f32_i4(int(h >> (8 * i) & 255u)));
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -157,6 +160,399 @@ __global__ __launch_bounds__(512) void i4_direct_kernel(I4Args a, int n_groups, 
   const float bias = a.bias ? a.bias[n_in] : 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) store_y(a, b0 + 4 * q + e, n, finish(acc[e], a.bias, bias));
+}
+
+// 16 bytes past the caches' replacement (bytes read once).
+template <bool NT>
+__device__ __forceinline__ u32x4 load_w16(const uint8_t* p) {
+  if (NT) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return *reinterpret_cast<const u32x4*>(p);
+}
+
+// A scale as its bits in fp32, from a vector of type st.
+__device__ __forceinline__ uint32_t scale_bits(const char* p, int64_t i, int st) {
+  if (st == UW_F32) return reinterpret_cast<const uint32_t*>(p)[i];
+  return uint32_t(reinterpret_cast<const uint16_t*>(p)[i]) << 16;
+}
+
+constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
+
+// Few tokens: bound by the weights' read.  A workgroup holds 16 WI weight rows
+// and 16 BJ activation rows, and its KW waves split k: wave w takes the blocks
+// of 128 columns w, w + KW, ...  A wave keeps D blocks in flight in registers
+// (weights, activations and scales), each refilled as soon as it is used, and
+// meets the others only to add the partial tiles at the end.  Lanes of tokens
+// that are not there load nothing.  NT: the weights are read by this
+// workgroup alone.
+template <int G, bool OFF, int WI, int BJ, int KW, int D, bool NT>
+__global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tiles, int nb_tiles) {
+  constexpr int GB = 128 / G;  // groups of a block
+  // the batch tiles of one weight tile run back to back on one XCD
+  const int id = int(blockIdx.x);
+  const int wt = (id / (kXcds * nb_tiles)) * kXcds + id % kXcds, y = (id / kXcds) % nb_tiles;
+  if (wt >= nw_tiles) return;  // whole workgroups
+  const int64_t row0 = int64_t(wt) * 16 * WI, b0 = int64_t(y) * 16 * BJ;
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int r = lane % 16, q = lane / 16;
+  const uint8_t* wr[WI];
+  int64_t nr[WI];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) {
+    nr[i] = std::min<int64_t>(row0 + 16 * i + r, a.rows - 1);
+    wr[i] = a.W + nr[i] * a.ldw;
+  }
+  const uint16_t* xr[BJ];
+  bool live[BJ];
+#pragma unroll
+  for (int j = 0; j < BJ; ++j) {
+    live[j] = b0 + 16 * j + r < a.batch;
+    xr[j] = a.X + std::min<int64_t>(b0 + 16 * j + r, a.batch - 1) * a.ldx;
+  }
+  const int64_t last = (a.cols - 1) / 32, groups = (a.cols + G - 1) / G;
+  const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
+  struct Block {
+    u32x4 w[WI], x[BJ][4];
+    uint32_t s[WI][GB], m[WI][GB];
+  };
+  Block ring[D];
+  auto load = [&](Block& b, int i) {
+    const int64_t kb = wave + int64_t(KW) * i, k0 = kb * 128;
+    const int64_t at = 16 * std::min<int64_t>(4 * kb + q, last);
+#pragma unroll
+    for (int t = 0; t < WI; ++t) b.w[t] = load_w16<NT>(wr[t] + at);
+#pragma unroll
+    for (int t = 0; t < WI; ++t)
+#pragma unroll
+      for (int g = 0; g < GB; ++g) {
+        const int64_t gi = std::min<int64_t>(k0 / G + g, groups - 1);
+        b.s[t][g] = scale_bits(a.scale + gi * a.lds * (a.st == UW_F32 ? 4 : 2), nr[t], a.st);
+        if (OFF) b.m[t][g] = scale_bits(a.offset + gi * a.ldo * (a.st == UW_F32 ? 4 : 2), nr[t], a.st);
+      }
+#pragma unroll
+    for (int j = 0; j < BJ; ++j)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
+        const int64_t k = k0 + (G == 128 ? 32 * q + 8 * s : 32 * s + 8 * q);
+        b.x[j][s] = u32x4{0u, 0u, 0u, 0u};
+        if (live[j]) b.x[j][s] = load_x8(xr[j], k, a.cols);
+      }
+  };
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{kOnes, kOnes, kOnes, kOnes});
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[WI][BJ];
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) acc[i][j] = zero;
+  auto multiply = [&](Block& b) {
+    if (G != 128) {
+#pragma unroll
+      for (int i = 0; i < WI; ++i) transpose4(b.w[i]);
+    }
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      f32x4 part[WI][BJ], sum[BJ];
+#pragma unroll
+      for (int s = 0; s < 4 / GB; ++s) {
+        const int at = g * (4 / GB) + s;
+#pragma unroll
+        for (int i = 0; i < WI; ++i) {
+          const bf16x8 w = decode8(b.w[i][at]);
+#pragma unroll
+          for (int j = 0; j < BJ; ++j) part[i][j] = mfma_bf16(__builtin_bit_cast(bf16x8, b.x[j][at]), w, s ? part[i][j] : zero);
+        }
+        if (OFF) {
+#pragma unroll
+          for (int j = 0; j < BJ; ++j) sum[j] = mfma_bf16(__builtin_bit_cast(bf16x8, b.x[j][at]), ones, s ? sum[j] : zero);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < WI; ++i) {
+        const float sc = bits_f32(b.s[i][g]), m = OFF ? bits_f32(b.m[i][g]) * 0.0625f : 0.f;
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[i][j][e] = fmaf(sc, part[i][j][e], acc[i][j][e]);
+            if (OFF) acc[i][j][e] = fmaf(m, sum[j][e], acc[i][j][e]);
+          }
+      }
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (d < n) load(ring[d], d);
+  for (int i = 0; i < n; i += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (i + d < n) multiply(ring[d]);
+      if (i + d + D < n) load(ring[d], i + d + D);
+    }
+  }
+  // partial tile (i, j) of wave w at (w WI BJ + i BJ + j) KB
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int j = 0; j < BJ; ++j)
+      if (b0 + 16 * j + 4 * q < a.batch)
+        st128(uint32_t(((wave * WI + i) * BJ + j) * 1024 + 16 * lane), __builtin_bit_cast(uint4, acc[i][j]));
+  __syncthreads();
+  for (int t = wave; t < WI * BJ; t += KW) {
+    const int64_t b = b0 + 16 * (t % BJ) + 4 * q, nn = row0 + 16 * (t / BJ) + r;
+    if (b >= a.batch || nn >= a.rows) continue;
+    f32x4 total = zero;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const f32x4 v = __builtin_bit_cast(f32x4, ld128(uint32_t((w * WI * BJ + t) * 1024 + 16 * lane)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) total[e] += v[e];
+    }
+    const float bias = a.bias ? a.bias[nn] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) store_y(a, b + e, nn, finish(total[e], a.bias, bias));
+  }
+}
+
+// A tile of an operand as a buffer: `rows` rows of `bytes` bytes (the end of
+// the last one rounded up to 4), ld bytes apart; rows past the last are that
+// row again.  The values are the same in every lane; readfirstlane keeps them
+// in scalar registers.
+struct Staged4 {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int last;
+
+  __device__ __forceinline__ Staged4(const void* tile, int64_t rows, int64_t bytes, int64_t ld, int tile_rows)
+      : last(__builtin_amdgcn_readfirstlane(int(std::min<int64_t>(tile_rows, rows)) - 1)) {
+    const uint64_t p = reinterpret_cast<uint64_t>(tile);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(p)), hi = __builtin_amdgcn_readfirstlane(uint32_t(p >> 32));
+    const int size = __builtin_amdgcn_readfirstlane(int(int64_t(last) * ld + (bytes + 3) / 4 * 4));
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uint64_t(hi) << 32 | lo), int16_t(0), size, 0x00020000);
+  }
+};
+
+// Mask of 8 bf16 values of which the first `left` lie inside their row.
+__device__ __forceinline__ u32x4 tail_mask8(int left) {
+  u32x4 m;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) m[d] = left >= 2 * d + 2 ? ~0u : left == 2 * d + 1 ? 0xFFFFu : 0u;
+  return m;
+}
+
+// Many tokens.  The packed weights and the activations of a block of 128
+// columns are staged in LDS for the whole workgroup, one block ahead of the
+// products: BW = 16 WI WGW weight rows (64 bytes each) and BB = 16 BJ WGB
+// activation rows (256 bytes each), whose WGW x WGB waves each hold WI x BJ
+// tiles of 16 x 16.  A wave decodes its WI x 128 weights of a block into
+// registers once and runs them against one tile of tokens after another, so
+// that a group's sums live for one tile only.  KG groups of such waves, each
+// with its own two stages, take every KG-th block and add their sums in LDS at
+// the end.
+//
+// In LDS the 16-byte chunk c of an activation row r lies at chunk c ^ (r % 16),
+// that of a weight row at c ^ (r / 4 % 4): the 8 lanes that a read serves at a
+// time fall into different banks.  In the last block, lanes past the last
+// chunk of their row read that chunk again; what lies past `cols` is then
+// cleared in the activations.
+template <int G, bool OFF, int WGW, int WGB, int WI, int BJ, int KG>
+__global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a, int nw_tiles, int nb_tiles, int per_xcd) {
+  constexpr int NW = WGW * WGB, GB = 128 / G;
+  constexpr int BW = 16 * WI * WGW, BB = 16 * BJ * WGB;
+  constexpr int LW = BW / 16, LB = BB / 4;  // 1 KB loads of a stage
+  constexpr uint32_t kWBytes = BW * 64, kStage = BW * 64 + BB * 256;
+  constexpr int kPartial = NW * WI * BJ * 1024;  // a group's sums
+  static_assert((KG - 1) * kPartial <= KG * 2 * int(kStage), "LDS");
+  // workgroups are dealt to the XCDs round-robin: each XCD takes a run of
+  // tiles, 4 activation tiles deep, so that its L2 serves the rereads
+  const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
+  if (id >= nw_tiles * nb_tiles) return;  // whole workgroups
+  constexpr int kDeep = 4;
+  const int strip = id / (kDeep * nw_tiles);
+  const int deep = min(kDeep, nb_tiles - strip * kDeep);
+  const int in = id - strip * kDeep * nw_tiles;
+  const int64_t row0 = int64_t(in / deep) * BW, b0 = (int64_t(strip) * kDeep + in % deep) * BB;
+  const int lane = int(threadIdx.x) % kWave, w_all = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int group = w_all / NW, wave = w_all % NW;
+  const int r = lane % 16, q = lane / 16;
+  const int ww = wave / WGB, wb = wave % WGB;
+  const Staged4 tw(a.W + row0 * a.ldw, a.rows - row0, (a.cols + 31) / 32 * 16, a.ldw, BW);
+  const Staged4 tx(a.X + b0 * a.ldx, a.batch - b0, 2 * a.cols, 2 * a.ldx, BB);
+  const int nkb = int((a.cols + 127) / 128), n = (nkb - group + KG - 1) / KG;
+  const uint32_t ring = uint32_t(group) * (2 * kStage);
+  // a lane's rows and chunks of each load; chunks are the same for all of them
+  static_assert(NW % 4 == 0, "rows of a load");
+  constexpr int LWN = (LW + NW - 1) / NW, LBN = (LB + NW - 1) / NW;
+  const int wchunk = (lane % 4) ^ (lane / 16), xchunk = r ^ (4 * (wave % 4) + q);
+  uint32_t wvo[LWN], xvo[LBN];
+#pragma unroll
+  for (int u = 0; u < LWN; ++u) wvo[u] = uint32_t(min(16 * (u * NW + wave) + lane / 4, tw.last)) * uint32_t(a.ldw) + 16 * wchunk;
+#pragma unroll
+  for (int u = 0; u < LBN; ++u) xvo[u] = uint32_t(min(4 * (u * NW + wave) + q, tx.last)) * uint32_t(2 * a.ldx) + 16 * xchunk;
+  // in the last block, how far a lane's chunk lies past the row's last one
+  const int wlast = int((a.cols - 1) / 32) % 4, xlast = int((a.cols - 1) / 8) % 16;
+  const uint32_t wover = 16 * max(0, wchunk - wlast), xover = 16 * max(0, xchunk - xlast);
+  auto issue = [&](int i) {
+    const int kb = i * KG + group;
+    const uint32_t base = ring + uint32_t(i & 1) * kStage;
+    const bool end = kb == nkb - 1;
+#pragma unroll
+    for (int u = 0; u < LWN; ++u)
+      if (LW % NW == 0 || u * NW + wave < LW)
+        stage_load<false>(tw.rsrc, wvo[u] - (end ? wover : 0u), uint32_t(kb) * 64, base + uint32_t(u * NW + wave) * 1024);
+#pragma unroll
+    for (int u = 0; u < LBN; ++u)
+      if (LB % NW == 0 || u * NW + wave < LB)
+        stage_load<false>(tx.rsrc, xvo[u] - (end ? xover : 0u), uint32_t(kb) * 256, base + kWBytes + uint32_t(u * NW + wave) * 1024);
+  };
+  // what the last block holds past `cols` is cleared by the group's threads
+  auto clear_tail = [&](int i) {
+    const int left = int(a.cols - int64_t(nkb - 1) * 128);
+    for (int at = wave * kWave + lane; at < BB * 16; at += NW * kWave) {
+      const int row = at / 16, chunk = at % 16;
+      if (8 * chunk + 8 <= left) continue;
+      const uint32_t p = ring + uint32_t(i & 1) * kStage + kWBytes + uint32_t(row) * 256 + uint32_t(chunk ^ (row % 16)) * 16;
+      st128(p, __builtin_bit_cast(uint4, __builtin_bit_cast(u32x4, ld128(p)) & tail_mask8(left - 8 * chunk)));
+    }
+  };
+  int64_t nr[WI];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) nr[i] = std::min<int64_t>(row0 + 16 * (ww * WI + i) + r, a.rows - 1);
+  const int64_t groups = (a.cols + G - 1) / G;
+  uint32_t sn[WI][GB], mn[WI][GB];  // the next block's scales and offsets
+  auto scales = [&](int i) {
+    const int64_t g0 = (int64_t(i) * KG + group) * GB;
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      const int64_t gi = std::min<int64_t>(g0 + g, groups - 1);
+#pragma unroll
+      for (int t = 0; t < WI; ++t) {
+        sn[t][g] = scale_bits(a.scale + gi * a.lds * (a.st == UW_F32 ? 4 : 2), nr[t], a.st);
+        if (OFF) mn[t][g] = scale_bits(a.offset + gi * a.ldo * (a.st == UW_F32 ? 4 : 2), nr[t], a.st);
+      }
+    }
+  };
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{kOnes, kOnes, kOnes, kOnes});
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[WI][BJ];
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) acc[i][j] = zero;
+  const uint32_t wat = uint32_t(ww * WI * 16 + r) * 64 + uint32_t(q ^ (r / 4)) * 16;
+  const uint32_t xat = kWBytes + uint32_t(wb * BJ * 16 + r) * 256;
+  auto multiply = [&](int i, const uint32_t (&sc)[WI][GB], const uint32_t (&mc)[WI][GB]) {
+    const uint32_t base = ring + uint32_t(i & 1) * kStage;
+    bf16x8 w[WI][4];
+#pragma unroll
+    for (int t = 0; t < WI; ++t) {
+      u32x4 v = __builtin_bit_cast(u32x4, ld128(base + wat + uint32_t(t) * 1024));
+      if (G != 128) transpose4(v);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) w[t][s] = decode8(v[s]);
+    }
+    // one tile of tokens at a time: the next one's operands are read and the last one's sums are scaled while this one's
+    // products run; the barriers keep the compiler from holding more tiles than that in registers
+    bf16x8 x[2][4];
+    f32x4 part[2][WI], sum[2];
+    auto read = [&](int j, bf16x8 (&to)[4]) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int chunk = G == 128 ? 4 * q + s : 4 * s + q;
+        to[s] = __builtin_bit_cast(bf16x8, ld128(base + xat + uint32_t(j) * 4096 + uint32_t(chunk ^ r) * 16));
+      }
+    };
+    auto fold = [&](int j, int g, const f32x4 (&pt)[WI], const f32x4& sm) {
+#pragma unroll
+      for (int t = 0; t < WI; ++t) {
+        const float f = bits_f32(sc[t][g]), m = OFF ? bits_f32(mc[t][g]) * 0.0625f : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[t][j][e] = fmaf(f, pt[t][e], acc[t][j][e]);
+          if (OFF) acc[t][j][e] = fmaf(m, sm[e], acc[t][j][e]);
+        }
+      }
+    };
+    read(0, x[0]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) {
+      if (j + 1 < BJ) read(j + 1, x[(j + 1) & 1]);
+#pragma unroll
+      for (int g = 0; g < GB; ++g) {
+        const int now = (j * GB + g) & 1;
+#pragma unroll
+        for (int s = 0; s < 4 / GB; ++s) {
+          const int at = g * (4 / GB) + s;
+#pragma unroll
+          for (int t = 0; t < WI; ++t) part[now][t] = mfma_bf16(x[j & 1][at], w[t][at], s ? part[now][t] : zero);
+          if (OFF) sum[now] = mfma_bf16(x[j & 1][at], ones, s ? sum[now] : zero);
+        }
+        if (j * GB + g > 0) fold((j * GB + g - 1) / GB, (j * GB + g - 1) % GB, part[now ^ 1], sum[now ^ 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    fold(BJ - 1, GB - 1, part[(BJ * GB - 1) & 1], sum[(BJ * GB - 1) & 1]);
+  };
+  if (n > 0) {
+    issue(0);
+    scales(0);
+  }
+  // every wave takes part in the barriers of the first group's blocks
+  const int steps = (nkb + KG - 1) / KG;
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    wait_vmcnt<0>();  // this wave's loads of block i (and its scales) have landed
+    lds_barrier();    // every wave's have; block i - 1 is no longer read
+    if (i == steps - 1 && a.cols % 128) {
+      if (i * KG + group == nkb - 1) clear_tail(i);
+      lds_barrier();
+    }
+    uint32_t sc[WI][GB], mc[WI][GB];
+#pragma unroll
+    for (int t = 0; t < WI; ++t)
+#pragma unroll
+      for (int g = 0; g < GB; ++g) {
+        sc[t][g] = sn[t][g];
+        mc[t][g] = OFF ? mn[t][g] : 0u;
+      }
+    if (i + 1 < n) {
+      issue(i + 1);
+      scales(i + 1);
+    }
+    if (KG == 1 || i < n) multiply(i, sc, mc);
+  }
+  if (KG > 1) {
+    __syncthreads();  // no wave reads the rings any more
+    const uint32_t mine = uint32_t(wave) * (WI * BJ * 1024) + 16 * lane;
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < WI; ++i)
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+          st128(uint32_t((group - 1) * kPartial) + mine + uint32_t(i * BJ + j) * 1024, __builtin_bit_cast(uint4, acc[i][j]));
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < WI; ++i)
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) {
+          const f32x4 v = __builtin_bit_cast(f32x4, ld128(uint32_t(g * kPartial) + mine + uint32_t(i * BJ + j) * 1024));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += v[e];
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < WI; ++i) {
+    const int64_t nn = row0 + 16 * (ww * WI + i) + r;
+    const float bias = a.bias ? a.bias[nr[i]] : 0.f;
+#pragma unroll
+    for (int j = 0; j < BJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) store_y(a, b0 + 16 * (wb * BJ + j) + 4 * q + e, nn, finish(acc[i][j][e], a.bias, bias));
+  }
 }
 
 // -- rows in 4 bits and back ----------------------------------------------------
@@ -353,10 +749,57 @@ int run_direct(const I4Args& a, hipStream_t s) {
   return hip_check(hipGetLastError(), "i4_direct_kernel launch");
 }
 
+template <int G, bool OFF, int WI, int BJ, int KW, int D>
+int run_slice(const I4Args& a, hipStream_t s) {
+  const int64_t nw = (a.rows + 16 * WI - 1) / (16 * WI), nb = (a.batch + 16 * BJ - 1) / (16 * BJ);
+  if (int rc = check_launch((nw + kXcds - 1) / kXcds * kXcds, nb, KW * kWave)) return rc;
+  const int64_t grid = (nw + kXcds - 1) / kXcds * kXcds * nb;
+  auto kern = nb == 1 ? i4_slice_kernel<G, OFF, WI, BJ, KW, D, true> : i4_slice_kernel<G, OFF, WI, BJ, KW, D, false>;
+  constexpr size_t kLds = size_t(KW) * WI * BJ * 1024;
+  static_assert(kLds <= kLdsLimit, "LDS");
+  allow_full_lds(kern);
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(KW * kWave), kLds, s, a, int(nw), int(nb));
+  return hip_check(hipGetLastError(), "i4_slice_kernel launch");
+}
+
+template <int G, bool OFF, int WGW, int WGB, int WI, int BJ, int KG>
+int run_stage(const I4Args& a, hipStream_t s) {
+  constexpr int BW = 16 * WI * WGW, BB = 16 * BJ * WGB, kThreads = 64 * WGW * WGB * KG;
+  const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
+  if (int rc = check_launch(nw, nb, kThreads)) return rc;
+  const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
+  auto kern = i4_stage_kernel<G, OFF, WGW, WGB, WI, BJ, KG>;
+  constexpr size_t kLds = size_t(KG) * 2 * (BW * 64 + BB * 256);
+  static_assert(kLds <= kLdsLimit, "LDS");
+  allow_full_lds(kern);
+  hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), kLds, s, a, int(nw), int(nb), int(per_xcd));
+  return hip_check(hipGetLastError(), "i4_stage_kernel launch");
+}
+
+bool stage_ok(const I4Args& a) {
+  // 16-byte chunks of the activations, and 32-bit offsets inside a tile of 256 rows
+  return reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 8 == 0 && a.ldx < (int64_t(1) << 21) &&
+         a.ldw < (int64_t(1) << 22);
+}
+
+constexpr int kShapes = 11;
+constexpr int kFirstStaged = 6;
+
 template <int G, bool OFF>
 int run_gemm(const I4Args& a, int shape, hipStream_t s) {
-  (void)shape;
-  return run_direct<G, OFF>(a, s);
+  if (shape <= 0) shape = a.batch <= 16 ? (a.rows >= 8192 ? 2 : 3) : a.batch <= 32 ? 4 : !stage_ok(a) ? 1 : a.batch <= 64 ? 5 : a.batch <= 1024 ? 8 : 10;
+  switch (shape) {
+    case 1: return run_direct<G, OFF>(a, s);
+    case 2: return run_slice<G, OFF, G == 32 ? 2 : 4, 1, 8, 2>(a, s);
+    case 3: return run_slice<G, OFF, 1, 1, 16, 2>(a, s);
+    case 4: return run_slice<G, OFF, 2, 2, 8, 1>(a, s);
+    case 5: return run_slice<G, OFF, G == 32 ? 1 : 2, 4, 8, 1>(a, s);
+    case 6: return run_stage<G, OFF, 2, 2, 2, 2, 1>(a, s);   // 64 x 64
+    case 7: return run_stage<G, OFF, 4, 1, 2, 4, 2>(a, s);   // 128 x 64, 2 groups
+    case 8: return run_stage<G, OFF, 2, 2, 4, 4, 1>(a, s);   // 128 x 128
+    case 9: return run_stage<G, OFF, 4, 2, 4, 6, 1>(a, s);   // 256 x 192
+    default: return run_stage<G, OFF, 4, 2, 3, 8, 1>(a, s);  // 192 x 256
+  }
 }
 
 template <bool F32, int G, bool OFF>
@@ -392,7 +835,15 @@ int run_quantize_group(const Q4Args& a, int group, hipStream_t s) {
 
 }  // namespace
 
-int i4_gemm_shape_count() { return 2; }
+int i4_gemm_shape_count() { return kShapes; }
+
+bool i4_gemm_shape_ok(int64_t rows, int64_t ldw, const uint16_t* X, int64_t batch, int64_t ldx, int shape) {
+  I4Args a{};
+  a.X = X;
+  a.ldw = rows > 1 ? ldw : 0;
+  a.ldx = batch > 1 ? ldx : 0;
+  return shape < kFirstStaged || stage_ok(a);
+}
 
 int launch_i4_gemm(const uint8_t* W, int64_t rows, int64_t cols, int64_t ldw, int group, const void* scale, int64_t lds,
                    const void* offset, int64_t ldo, int st, const uint16_t* X, int64_t batch, int64_t ldx,

@@ -254,32 +254,6 @@ __global__ __launch_bounds__(512) void i8_direct_kernel(I8Args a, int n_groups, 
   store_y4<YBF16>(a, b0 + r, row0 + 4 * q, acc);
 }
 
-// 16 bytes per lane from the buffer resource at byte voff + soff into LDS at
-// m0 + 16 * lane (all lanes active).  NT: non-temporal, for operands that are
-// read once.
-template <bool NT>
-__device__ __forceinline__ void stage_load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t m0) {
-  if (NT) {
-    asm volatile(
-        "s_nop 4\n"
-        "s_mov_b32 m0, %[m]\n"
-        "s_nop 0\n"
-        "buffer_load_dwordx4 %[v], %[r], %[s] offen nt lds"
-        :
-        : [m] "s"(__builtin_amdgcn_readfirstlane(m0)), [v] "v"(voff), [r] "s"(r), [s] "s"(__builtin_amdgcn_readfirstlane(soff))
-        : "memory");
-  } else {
-    asm volatile(
-        "s_nop 4\n"
-        "s_mov_b32 m0, %[m]\n"
-        "s_nop 0\n"
-        "buffer_load_dwordx4 %[v], %[r], %[s] offen lds"
-        :
-        : [m] "s"(__builtin_amdgcn_readfirstlane(m0)), [v] "v"(voff), [r] "s"(r), [s] "s"(__builtin_amdgcn_readfirstlane(soff))
-        : "memory");
-  }
-}
-
 // Staging of an operand's tile: rows of 128 bytes of k in LDS, the 16-byte
 // chunk c of row r at chunk c ^ (r % 8), so that the 8 rows an operand read
 // touches at a time lie in 8 different bank groups.  One load moves 8 rows:

@@ -788,7 +788,9 @@ int uw_i4_gemm(const uint8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, int 
  * uw_i4_gemm_shaped (device) - uw_i4_gemm with a given shape: shape in
  * [1, uw_i4_gemm_shape_count()) picks the weight and batch rows a workgroup
  * holds and how the operands reach the matrix cores.
- * Errors: as uw_i4_gemm; UW_ERR_INVALID for an unknown shape.
+ * Errors: as uw_i4_gemm; UW_ERR_INVALID for an unknown shape,
+ *         UW_ERR_UNSUPPORTED for a staged shape on activation rows off 16-byte
+ *         boundaries (or strides of 2^22 bytes or more).
  */
 int uw_i4_gemm_shaped(const uint8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, int group, const void* d_scale,
                       int64_t lds, const void* d_offset, int64_t ldo, int st, const uint16_t* d_X, int64_t batch,
