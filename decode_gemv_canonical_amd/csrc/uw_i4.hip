@@ -169,11 +169,14 @@ __device__ __forceinline__ u32x4 load_w16(const uint8_t* p) {
   return *reinterpret_cast<const u32x4*>(p);
 }
 
-// A scale as its bits in fp32, from a vector of type st.
-__device__ __forceinline__ uint32_t scale_bits(const char* p, int64_t i, int st) {
-  if (st == UW_F32) return reinterpret_cast<const uint32_t*>(p)[i];
-  return uint32_t(reinterpret_cast<const uint16_t*>(p)[i]) << 16;
+// A scale as it lies in memory, and its value: apart, so that a load is not
+// waited for before the value is used.  half: 0 where scales are fp32, 16
+// where they are bf16.
+__device__ __forceinline__ uint32_t scale_raw(const char* p, int64_t i, int half) {
+  if (!half) return reinterpret_cast<const uint32_t*>(p)[i];
+  return reinterpret_cast<const uint16_t*>(p)[i];
 }
+__device__ __forceinline__ float scale_value(uint32_t raw, int half) { return bits_f32(raw << half); }
 
 constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
 
@@ -209,6 +212,7 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
     xr[j] = a.X + std::min<int64_t>(b0 + 16 * j + r, a.batch - 1) * a.ldx;
   }
   const int64_t last = (a.cols - 1) / 32, groups = (a.cols + G - 1) / G;
+  const int half = a.st == UW_F32 ? 0 : 16;
   const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
   struct Block {
     u32x4 w[WI], x[BJ][4];
@@ -225,8 +229,8 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
 #pragma unroll
       for (int g = 0; g < GB; ++g) {
         const int64_t gi = std::min<int64_t>(k0 / G + g, groups - 1);
-        b.s[t][g] = scale_bits(a.scale + gi * a.lds * (a.st == UW_F32 ? 4 : 2), nr[t], a.st);
-        if (OFF) b.m[t][g] = scale_bits(a.offset + gi * a.ldo * (a.st == UW_F32 ? 4 : 2), nr[t], a.st);
+        b.s[t][g] = scale_raw(a.scale, gi * a.lds + nr[t], half);
+        if (OFF) b.m[t][g] = scale_raw(a.offset, gi * a.ldo + nr[t], half);
       }
 #pragma unroll
     for (int j = 0; j < BJ; ++j)
@@ -269,7 +273,7 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
       }
 #pragma unroll
       for (int i = 0; i < WI; ++i) {
-        const float sc = bits_f32(b.s[i][g]), m = OFF ? bits_f32(b.m[i][g]) * 0.0625f : 0.f;
+        const float sc = scale_value(b.s[i][g], half), m = OFF ? scale_value(b.m[i][g], half) * 0.0625f : 0.f;
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
 #pragma unroll
@@ -311,6 +315,70 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
     const float bias = a.bias ? a.bias[nn] : 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) store_y(a, b + e, nn, finish(total[e], a.bias, bias));
+  }
+}
+
+// 16 bytes of row b of Y from column n on: 16 / SIZE values.  NT: whole lines
+// are written, past the caches.
+template <int SIZE, bool NT>
+__device__ __forceinline__ void store_row16(const I4Args& a, int64_t b, int64_t n, const uint4& v) {
+  if (b >= a.batch || n >= a.rows) return;
+  char* y = a.Y + (b * a.ldy + n) * SIZE;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int m = int(std::min<int64_t>(16 / SIZE, a.rows - n));
+  if (m == 16 / SIZE) {
+    if (NT) __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(y));
+    else __builtin_memcpy(y, w, 16);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 16 / SIZE - 1; ++e) {
+    if (e >= m) continue;
+    if (SIZE == 4) {
+      __builtin_memcpy(y + 4 * e, &w[e], 4);
+    } else {
+      const uint16_t h = uint16_t(w[e / 2] >> (16 * (e & 1)));
+      __builtin_memcpy(y + 2 * e, &h, 2);
+    }
+  }
+}
+
+template <int WI>
+constexpr int epilogue_bytes = 16 * (16 * WI * 4 + 16);
+
+// Epilogue of a wave's WI x BJ tiles at (n0, b0), through LDS: 16 activation
+// rows at a time as the wave's 16 WI columns, so that rows go out in runs of
+// 32 WI bytes (bf16) or twice that.  out: the wave's place in LDS,
+// epilogue_bytes<WI> that nothing else uses any more.
+template <int WI, int BJ, bool YBF16, bool NT>
+__device__ __forceinline__ void store_through_lds(const I4Args& a, int64_t n0, int64_t b0, uint32_t out, int lane,
+                                                  const f32x4 (&acc)[WI][BJ]) {
+  constexpr int kCols = 16 * WI, kSize = YBF16 ? 2 : 4, kPitch = kCols * kSize + 16;
+  const int r = lane % 16, q = lane / 16;
+  float bias[WI];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) bias[i] = a.bias ? a.bias[std::min<int64_t>(n0 + 16 * i + r, a.rows - 1)] : 0.f;
+#pragma unroll
+  for (int j = 0; j < BJ; ++j) {
+#pragma unroll
+    for (int i = 0; i < WI; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = finish(acc[i][j][e], a.bias, bias[i]);
+        const uint32_t dst = out + uint32_t(4 * q + e) * kPitch + uint32_t(16 * i + r) * kSize;
+        if (YBF16) st16(dst, pack_bf16(v, 0.f));
+        else st32(dst, f32_bits(v));
+      }
+    wave_lds_fence();
+    constexpr int kPer = 16 / kSize, kLanes = kCols / kPer;  // values a lane stores; lanes of a row
+    constexpr int kChunks = 16 * kLanes;                     // of the 16 rows
+#pragma unroll
+    for (int c0 = 0; c0 < kChunks; c0 += kWave) {
+      const int at = c0 + lane, br = at / kLanes, c = at % kLanes * kPer;
+      if (kChunks % kWave == 0 || at < kChunks)
+        store_row16<kSize, NT>(a, b0 + 16 * j + br, n0 + c, ld128(out + uint32_t(br) * kPitch + uint32_t(c) * kSize));
+    }
+    wave_lds_fence();
   }
 }
 
@@ -361,7 +429,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
   constexpr int LW = BW / 16, LB = BB / 4;  // 1 KB loads of a stage
   constexpr uint32_t kWBytes = BW * 64, kStage = BW * 64 + BB * 256;
   constexpr int kPartial = NW * WI * BJ * 1024;  // a group's sums
-  static_assert((KG - 1) * kPartial <= KG * 2 * int(kStage), "LDS");
+  static_assert((KG - 1) * kPartial + NW * epilogue_bytes<WI> <= KG * 2 * int(kStage), "LDS");
   // workgroups are dealt to the XCDs round-robin: each XCD takes a run of
   // tiles, 4 activation tiles deep, so that its L2 serves the rereads
   const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
@@ -418,6 +486,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
 #pragma unroll
   for (int i = 0; i < WI; ++i) nr[i] = std::min<int64_t>(row0 + 16 * (ww * WI + i) + r, a.rows - 1);
   const int64_t groups = (a.cols + G - 1) / G;
+  const int half = a.st == UW_F32 ? 0 : 16;
   uint32_t sn[WI][GB], mn[WI][GB];  // the next block's scales and offsets
   auto scales = [&](int i) {
     const int64_t g0 = (int64_t(i) * KG + group) * GB;
@@ -426,8 +495,8 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
       const int64_t gi = std::min<int64_t>(g0 + g, groups - 1);
 #pragma unroll
       for (int t = 0; t < WI; ++t) {
-        sn[t][g] = scale_bits(a.scale + gi * a.lds * (a.st == UW_F32 ? 4 : 2), nr[t], a.st);
-        if (OFF) mn[t][g] = scale_bits(a.offset + gi * a.ldo * (a.st == UW_F32 ? 4 : 2), nr[t], a.st);
+        sn[t][g] = scale_raw(a.scale, gi * a.lds + nr[t], half);
+        if (OFF) mn[t][g] = scale_raw(a.offset, gi * a.ldo + nr[t], half);
       }
     }
   };
@@ -440,7 +509,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     for (int j = 0; j < BJ; ++j) acc[i][j] = zero;
   const uint32_t wat = uint32_t(ww * WI * 16 + r) * 64 + uint32_t(q ^ (r / 4)) * 16;
   const uint32_t xat = kWBytes + uint32_t(wb * BJ * 16 + r) * 256;
-  auto multiply = [&](int i, const uint32_t (&sc)[WI][GB], const uint32_t (&mc)[WI][GB]) {
+  auto multiply = [&](int i, const float (&sc)[WI][GB], const float (&mc)[WI][GB]) {
     const uint32_t base = ring + uint32_t(i & 1) * kStage;
     bf16x8 w[WI][4];
 #pragma unroll
@@ -464,11 +533,10 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     auto fold = [&](int j, int g, const f32x4 (&pt)[WI], const f32x4& sm) {
 #pragma unroll
       for (int t = 0; t < WI; ++t) {
-        const float f = bits_f32(sc[t][g]), m = OFF ? bits_f32(mc[t][g]) * 0.0625f : 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          acc[t][j][e] = fmaf(f, pt[t][e], acc[t][j][e]);
-          if (OFF) acc[t][j][e] = fmaf(m, sm[e], acc[t][j][e]);
+          acc[t][j][e] = fmaf(sc[t][g], pt[t][e], acc[t][j][e]);
+          if (OFF) acc[t][j][e] = fmaf(mc[t][g], sm[e], acc[t][j][e]);
         }
       }
     };
@@ -499,6 +567,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
   }
   // every wave takes part in the barriers of the first group's blocks
   const int steps = (nkb + KG - 1) / KG;
+  if (w_all >= 4) __builtin_amdgcn_s_setprio(1);
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
     wait_vmcnt<0>();  // this wave's loads of block i (and its scales) have landed
@@ -507,13 +576,13 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
       if (i * KG + group == nkb - 1) clear_tail(i);
       lds_barrier();
     }
-    uint32_t sc[WI][GB], mc[WI][GB];
+    float sc[WI][GB], mc[WI][GB];
 #pragma unroll
     for (int t = 0; t < WI; ++t)
 #pragma unroll
       for (int g = 0; g < GB; ++g) {
-        sc[t][g] = sn[t][g];
-        mc[t][g] = OFF ? mn[t][g] : 0u;
+        sc[t][g] = scale_value(sn[t][g], half);
+        mc[t][g] = OFF ? scale_value(mn[t][g], half) * 0.0625f : 0.f;
       }
     if (i + 1 < n) {
       issue(i + 1);
@@ -521,8 +590,8 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     }
     if (KG == 1 || i < n) multiply(i, sc, mc);
   }
+  __syncthreads();  // no wave reads the rings any more
   if (KG > 1) {
-    __syncthreads();  // no wave reads the rings any more
     const uint32_t mine = uint32_t(wave) * (WI * BJ * 1024) + 16 * lane;
     if (group > 0) {
 #pragma unroll
@@ -544,15 +613,10 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
           for (int e = 0; e < 4; ++e) acc[i][j][e] += v[e];
         }
   }
-#pragma unroll
-  for (int i = 0; i < WI; ++i) {
-    const int64_t nn = row0 + 16 * (ww * WI + i) + r;
-    const float bias = a.bias ? a.bias[nr[i]] : 0.f;
-#pragma unroll
-    for (int j = 0; j < BJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) store_y(a, b0 + 16 * (wb * BJ + j) + 4 * q + e, nn, finish(acc[i][j][e], a.bias, bias));
-  }
+  const int64_t n0 = row0 + 16 * ww * WI, bw0 = b0 + 16 * wb * BJ;
+  const uint32_t out = uint32_t((KG - 1) * kPartial + wave * epilogue_bytes<WI>);
+  if (a.yt == UW_F32) store_through_lds<WI, BJ, false, false>(a, n0, bw0, out, lane, acc);
+  else store_through_lds<WI, BJ, true, false>(a, n0, bw0, out, lane, acc);
 }
 
 // -- rows in 4 bits and back ----------------------------------------------------
