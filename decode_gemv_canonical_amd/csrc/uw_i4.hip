@@ -162,21 +162,42 @@ __global__ __launch_bounds__(512) void i4_direct_kernel(I4Args a, int n_groups, 
   for (int e = 0; e < 4; ++e) store_y(a, b0 + 4 * q + e, n, finish(acc[e], a.bias, bias));
 }
 
-// 16 bytes past the caches' replacement (bytes read once).
-template <bool NT>
-__device__ __forceinline__ u32x4 load_w16(const uint8_t* p) {
-  if (NT) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-  return *reinterpret_cast<const u32x4*>(p);
+// A buffer over an operand: addresses in it are 32-bit offsets, of which the
+// part that a wave shares stays in a scalar register; nothing past `bytes` is
+// read (it reads as zero).  The values are the same in every lane;
+// readfirstlane keeps them in scalar registers.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_over(const void* p, int64_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v)), hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uint64_t(hi) << 32 | lo), int16_t(0),
+                                           __builtin_amdgcn_readfirstlane(int(bytes)), 0x00020000);
 }
 
-// A scale as it lies in memory, and its value: apart, so that a load is not
-// waited for before the value is used.  half: 0 where scales are fp32, 16
-// where they are bf16.
-__device__ __forceinline__ uint32_t scale_raw(const char* p, int64_t i, int half) {
-  if (!half) return reinterpret_cast<const uint32_t*>(p)[i];
-  return reinterpret_cast<const uint16_t*>(p)[i];
+// 16 bytes; NT: non-temporally, for weights that one workgroup reads.
+template <bool NT>
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, int(voff), int(soff), NT ? 2 : 0);
 }
-__device__ __forceinline__ float scale_value(uint32_t raw, int half) { return bits_f32(raw << half); }
+
+// Scales and offsets of a tile's rows: as they lie in memory, so that a load is
+// not waited for before its value is used.
+struct GroupRows {
+  __amdgpu_buffer_rsrc_t rsrc;
+  uint32_t step;  // bytes between groups
+  int shift;      // log2 of an element's bytes: 1 (bf16) or 2 (fp32)
+
+  __device__ __forceinline__ GroupRows(const char* p, int64_t ld, int st, int64_t groups, int64_t rows, int64_t row0)
+      : shift(st == UW_F32 ? 2 : 1) {
+    step = __builtin_amdgcn_readfirstlane(uint32_t(ld << shift));
+    rsrc = buffer_over(p + (row0 << shift), ((groups - 1) * ld + rows - row0) << shift);
+  }
+  __device__ __forceinline__ uint32_t load(uint32_t g, uint32_t row) const {
+    const int voff = int(row << shift), soff = int(__builtin_amdgcn_readfirstlane(g) * step);
+    if (shift == 2) return uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rsrc, voff, soff, 0));
+    return uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rsrc, voff, soff, 0));
+  }
+  __device__ __forceinline__ float value(uint32_t raw) const { return bits_f32(shift == 2 ? raw : raw << 16); }
+};
 
 constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
 
@@ -197,22 +218,24 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
   const int64_t row0 = int64_t(wt) * 16 * WI, b0 = int64_t(y) * 16 * BJ;
   const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int r = lane % 16, q = lane / 16;
-  const uint8_t* wr[WI];
-  int64_t nr[WI];
+  const uint32_t wlast = uint32_t(std::min<int64_t>(16 * WI, a.rows - row0)) - 1;  // rows past the last are that row again
+  const auto wbuf = buffer_over(a.W + row0 * a.ldw, int64_t(wlast) * a.ldw + (a.cols + 31) / 32 * 16);
+  const int64_t groups = (a.cols + G - 1) / G;
+  const GroupRows scale(a.scale, a.lds, a.st, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, a.st, groups, a.rows, row0);
+  uint32_t wr[WI], wvo[WI];
 #pragma unroll
   for (int i = 0; i < WI; ++i) {
-    nr[i] = std::min<int64_t>(row0 + 16 * i + r, a.rows - 1);
-    wr[i] = a.W + nr[i] * a.ldw;
+    wr[i] = min(uint32_t(16 * i + r), wlast);
+    wvo[i] = wr[i] * uint32_t(a.ldw) + 16 * q;
   }
   const uint16_t* xr[BJ];
   bool live[BJ];
 #pragma unroll
   for (int j = 0; j < BJ; ++j) {
     live[j] = b0 + 16 * j + r < a.batch;
+    // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
     xr[j] = a.X + std::min<int64_t>(b0 + 16 * j + r, a.batch - 1) * a.ldx;
   }
-  const int64_t last = (a.cols - 1) / 32, groups = (a.cols + G - 1) / G;
-  const int half = a.st == UW_F32 ? 0 : 16;
   const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
   struct Block {
     u32x4 w[WI], x[BJ][4];
@@ -220,23 +243,24 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
   };
   Block ring[D];
   auto load = [&](Block& b, int i) {
-    const int64_t kb = wave + int64_t(KW) * i, k0 = kb * 128;
-    const int64_t at = 16 * std::min<int64_t>(4 * kb + q, last);
+    const int kb = wave + KW * i;
+    const int64_t k0 = int64_t(kb) * 128;
+    // past a row's last word comes the next row: whole numbers against activations of zero
 #pragma unroll
-    for (int t = 0; t < WI; ++t) b.w[t] = load_w16<NT>(wr[t] + at);
+    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16<NT>(wbuf, wvo[t], uint32_t(kb) * 64);
 #pragma unroll
-    for (int t = 0; t < WI; ++t)
+    for (int g = 0; g < GB; ++g) {
+      const uint32_t gi = min(uint32_t(kb * GB + g), uint32_t(groups - 1));
 #pragma unroll
-      for (int g = 0; g < GB; ++g) {
-        const int64_t gi = std::min<int64_t>(k0 / G + g, groups - 1);
-        b.s[t][g] = scale_raw(a.scale, gi * a.lds + nr[t], half);
-        if (OFF) b.m[t][g] = scale_raw(a.offset, gi * a.ldo + nr[t], half);
+      for (int t = 0; t < WI; ++t) {
+        b.s[t][g] = scale.load(gi, wr[t]);
+        if (OFF) b.m[t][g] = offset.load(gi, wr[t]);
       }
+    }
 #pragma unroll
     for (int j = 0; j < BJ; ++j)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
         const int64_t k = k0 + (G == 128 ? 32 * q + 8 * s : 32 * s + 8 * q);
         b.x[j][s] = u32x4{0u, 0u, 0u, 0u};
         if (live[j]) b.x[j][s] = load_x8(xr[j], k, a.cols);
@@ -273,7 +297,7 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
       }
 #pragma unroll
       for (int i = 0; i < WI; ++i) {
-        const float sc = scale_value(b.s[i][g], half), m = OFF ? scale_value(b.m[i][g], half) * 0.0625f : 0.f;
+        const float sc = scale.value(b.s[i][g]), m = OFF ? offset.value(b.m[i][g]) * 0.0625f : 0.f;
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
 #pragma unroll
@@ -382,20 +406,140 @@ __device__ __forceinline__ void store_through_lds(const I4Args& a, int64_t n0, i
   }
 }
 
+// The fewest tokens (at most 16, whose activations fit in LDS): a workgroup
+// holds 16 WI weight rows; the activations are put into LDS once, while the
+// first weights are on their way, and each of the KW waves takes the blocks of
+// 128 columns w, w + KW, ... with D of them in flight in registers.
+// An activation row starts 16 bytes further into the banks than the one before
+// it; lanes of tokens that are not there read the last one's again, into
+// results that are not written.
+template <int G, bool OFF, int WI, int KW, int D>
+__global__ __launch_bounds__(64 * KW) void i4_resident_kernel(I4Args a, int nw_tiles, uint32_t pitch) {
+  constexpr int GB = 128 / G;  // groups of a block
+  const int wt = int(blockIdx.x);
+  if (wt >= nw_tiles) return;
+  const int64_t row0 = int64_t(wt) * 16 * WI;
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int r = lane % 16, q = lane / 16, batch = int(a.batch);
+  const uint32_t wlast = uint32_t(std::min<int64_t>(16 * WI, a.rows - row0)) - 1;  // rows past the last are that row again
+  const auto wbuf = buffer_over(a.W + row0 * a.ldw, int64_t(wlast) * a.ldw + (a.cols + 31) / 32 * 16);
+  const int64_t groups = (a.cols + G - 1) / G;
+  const GroupRows scale(a.scale, a.lds, a.st, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, a.st, groups, a.rows, row0);
+  uint32_t wr[WI], wvo[WI];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) {
+    wr[i] = min(uint32_t(16 * i + r), wlast);
+    wvo[i] = wr[i] * uint32_t(a.ldw) + 16 * q;
+  }
+  const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
+  struct Block {
+    u32x4 w[WI];
+    uint32_t s[WI][GB], m[WI][GB];
+  };
+  Block ring[D];
+  auto load = [&](Block& b, int i) {
+    const int kb = wave + KW * i;
+    // past a row's last word comes the next row: whole numbers against activations of zero
+#pragma unroll
+    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16<true>(wbuf, wvo[t], uint32_t(kb) * 64);
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      const uint32_t gi = min(uint32_t(kb * GB + g), uint32_t(groups - 1));
+#pragma unroll
+      for (int t = 0; t < WI; ++t) {
+        b.s[t][g] = scale.load(gi, wr[t]);
+        if (OFF) b.m[t][g] = offset.load(gi, wr[t]);
+      }
+    }
+  };
+  // the activations: chunk c of 8 columns of row b at b pitch + 16 c, zeros past the last column
+  const int chunks = 16 * nkb;
+  u32x4 first{0u, 0u, 0u, 0u};
+  const int t0 = int(threadIdx.x);
+  if (t0 < batch * chunks) first = load_x8(a.X + int64_t(t0 / chunks) * a.ldx, 8 * int64_t(t0 % chunks), a.cols);
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (d < n) load(ring[d], d);
+  if (t0 < batch * chunks) st128(uint32_t(t0 / chunks) * pitch + uint32_t(t0 % chunks) * 16, __builtin_bit_cast(uint4, first));
+  for (int at = t0 + 64 * KW; at < batch * chunks; at += 64 * KW)
+    st128(uint32_t(at / chunks) * pitch + uint32_t(at % chunks) * 16,
+          __builtin_bit_cast(uint4, load_x8(a.X + int64_t(at / chunks) * a.ldx, 8 * int64_t(at % chunks), a.cols)));
+  lds_barrier();
+  const uint32_t xat = uint32_t(min(r, batch - 1)) * pitch;
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{kOnes, kOnes, kOnes, kOnes});
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[WI];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) acc[i] = zero;
+  auto multiply = [&](Block& b, int i) {
+    const uint32_t at = xat + uint32_t(wave + KW * i) * 256;
+    bf16x8 x[4];
+    // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
+#pragma unroll
+    for (int s = 0; s < 4; ++s) x[s] = __builtin_bit_cast(bf16x8, ld128(at + uint32_t(G == 128 ? 4 * q + s : 4 * s + q) * 16));
+    if (G != 128) {
+#pragma unroll
+      for (int t = 0; t < WI; ++t) transpose4(b.w[t]);
+    }
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      f32x4 part[WI], sum;
+#pragma unroll
+      for (int s = 0; s < 4 / GB; ++s) {
+        const int k = g * (4 / GB) + s;
+#pragma unroll
+        for (int t = 0; t < WI; ++t) part[t] = mfma_bf16(x[k], decode8(b.w[t][k]), s ? part[t] : zero);
+        if (OFF) sum = mfma_bf16(x[k], ones, s ? sum : zero);
+      }
+#pragma unroll
+      for (int t = 0; t < WI; ++t) {
+        const float sc = scale.value(b.s[t][g]), m = OFF ? offset.value(b.m[t][g]) * 0.0625f : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[t][e] = fmaf(sc, part[t][e], acc[t][e]);
+          if (OFF) acc[t][e] = fmaf(m, sum[e], acc[t][e]);
+        }
+      }
+    }
+  };
+  for (int i = 0; i < n; i += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (i + d < n) multiply(ring[d], i + d);
+      if (i + d + D < n) load(ring[d], i + d + D);
+    }
+  }
+  __syncthreads();  // no wave reads the activations any more
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+    if (4 * q < batch) st128(uint32_t((wave * WI + i) * 1024 + 16 * lane), __builtin_bit_cast(uint4, acc[i]));
+  __syncthreads();
+  for (int t = wave; t < WI; t += KW) {
+    const int64_t nn = row0 + 16 * t + r;
+    if (4 * q >= batch || nn >= a.rows) continue;
+    f32x4 total = zero;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const f32x4 v = __builtin_bit_cast(f32x4, ld128(uint32_t((w * WI + t) * 1024 + 16 * lane)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) total[e] += v[e];
+    }
+    const float bias = a.bias ? a.bias[nn] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) store_y(a, 4 * q + e, nn, finish(total[e], a.bias, bias));
+  }
+}
+
 // A tile of an operand as a buffer: `rows` rows of `bytes` bytes (the end of
 // the last one rounded up to 4), ld bytes apart; rows past the last are that
-// row again.  The values are the same in every lane; readfirstlane keeps them
-// in scalar registers.
+// row again.
 struct Staged4 {
   __amdgpu_buffer_rsrc_t rsrc;
   int last;
 
   __device__ __forceinline__ Staged4(const void* tile, int64_t rows, int64_t bytes, int64_t ld, int tile_rows)
       : last(__builtin_amdgcn_readfirstlane(int(std::min<int64_t>(tile_rows, rows)) - 1)) {
-    const uint64_t p = reinterpret_cast<uint64_t>(tile);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(p)), hi = __builtin_amdgcn_readfirstlane(uint32_t(p >> 32));
-    const int size = __builtin_amdgcn_readfirstlane(int(int64_t(last) * ld + (bytes + 3) / 4 * 4));
-    rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uint64_t(hi) << 32 | lo), int16_t(0), size, 0x00020000);
+    rsrc = buffer_over(tile, int64_t(last) * ld + (bytes + 3) / 4 * 4);
   }
 };
 
@@ -482,21 +626,19 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
       st128(p, __builtin_bit_cast(uint4, __builtin_bit_cast(u32x4, ld128(p)) & tail_mask8(left - 8 * chunk)));
     }
   };
-  int64_t nr[WI];
-#pragma unroll
-  for (int i = 0; i < WI; ++i) nr[i] = std::min<int64_t>(row0 + 16 * (ww * WI + i) + r, a.rows - 1);
   const int64_t groups = (a.cols + G - 1) / G;
-  const int half = a.st == UW_F32 ? 0 : 16;
+  const GroupRows scale(a.scale, a.lds, a.st, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, a.st, groups, a.rows, row0);
   uint32_t sn[WI][GB], mn[WI][GB];  // the next block's scales and offsets
   auto scales = [&](int i) {
-    const int64_t g0 = (int64_t(i) * KG + group) * GB;
+    const uint32_t g0 = uint32_t(i * KG + group) * GB;
 #pragma unroll
     for (int g = 0; g < GB; ++g) {
-      const int64_t gi = std::min<int64_t>(g0 + g, groups - 1);
+      const uint32_t gi = min(g0 + g, uint32_t(groups - 1));
 #pragma unroll
       for (int t = 0; t < WI; ++t) {
-        sn[t][g] = scale_raw(a.scale, gi * a.lds + nr[t], half);
-        if (OFF) mn[t][g] = scale_raw(a.offset, gi * a.ldo + nr[t], half);
+        const uint32_t row = min(uint32_t(16 * (ww * WI + t) + r), uint32_t(tw.last));
+        sn[t][g] = scale.load(gi, row);
+        if (OFF) mn[t][g] = offset.load(gi, row);
       }
     }
   };
@@ -581,8 +723,8 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     for (int t = 0; t < WI; ++t)
 #pragma unroll
       for (int g = 0; g < GB; ++g) {
-        sc[t][g] = scale_value(sn[t][g], half);
-        mc[t][g] = OFF ? scale_value(mn[t][g], half) * 0.0625f : 0.f;
+        sc[t][g] = scale.value(sn[t][g]);
+        mc[t][g] = OFF ? offset.value(mn[t][g]) * 0.0625f : 0.f;
       }
     if (i + 1 < n) {
       issue(i + 1);
@@ -813,6 +955,23 @@ int run_direct(const I4Args& a, hipStream_t s) {
   return hip_check(hipGetLastError(), "i4_direct_kernel launch");
 }
 
+// LDS of the resident kernel: its activation rows, then its partial tiles.
+uint32_t resident_pitch(const I4Args& a) { return uint32_t((a.cols + 127) / 128 * 256 + 16); }
+bool resident_ok(const I4Args& a) {
+  return a.batch <= 16 && a.cols <= 65536 && a.batch * int64_t(resident_pitch(a)) <= kLdsLimit;
+}
+
+template <int G, bool OFF, int WI, int KW, int D>
+int run_resident(const I4Args& a, hipStream_t s) {
+  const int64_t nw = (a.rows + 16 * WI - 1) / (16 * WI);
+  if (int rc = check_launch(nw, 1, KW * kWave)) return rc;
+  auto kern = i4_resident_kernel<G, OFF, WI, KW, D>;
+  allow_full_lds(kern);
+  const size_t lds = std::max(size_t(a.batch) * resident_pitch(a), size_t(KW) * WI * 1024);
+  hipLaunchKernelGGL(kern, dim3(unsigned(nw)), dim3(KW * kWave), lds, s, a, int(nw), resident_pitch(a));
+  return hip_check(hipGetLastError(), "i4_resident_kernel launch");
+}
+
 template <int G, bool OFF, int WI, int BJ, int KW, int D>
 int run_slice(const I4Args& a, hipStream_t s) {
   const int64_t nw = (a.rows + 16 * WI - 1) / (16 * WI), nb = (a.batch + 16 * BJ - 1) / (16 * BJ);
@@ -840,29 +999,53 @@ int run_stage(const I4Args& a, hipStream_t s) {
   return hip_check(hipGetLastError(), "i4_stage_kernel launch");
 }
 
-bool stage_ok(const I4Args& a) {
-  // 16-byte chunks of the activations, and 32-bit offsets inside a tile of 256 rows
-  return reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 8 == 0 && a.ldx < (int64_t(1) << 21) &&
-         a.ldw < (int64_t(1) << 22);
+// 32-bit offsets inside a tile of 256 rows, and over the scales.
+bool offsets_ok(const I4Args& a, int group) {
+  const int64_t span = (a.cols + group - 1) / group * (a.st == UW_F32 ? 4 : 2), most = int64_t(1) << 31;
+  return a.ldx < (int64_t(1) << 21) && a.ldw < (int64_t(1) << 22) && span * a.lds < most && span * a.ldo < most &&
+         a.rows * 4 < most;
+}
+// 16-byte chunks of the activations.
+bool aligned_ok(const I4Args& a) { return reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 8 == 0; }
+
+constexpr int kShapes = 15;
+enum Kind { kDirect, kResident, kSlice, kStage };
+constexpr Kind kKinds[kShapes] = {kDirect, kDirect, kResident, kResident, kResident, kSlice, kSlice, kSlice, kSlice,
+                                  kStage, kStage, kStage, kStage, kStage, kStage};
+
+bool shape_ok(const I4Args& a, int group, int shape) {
+  if (kKinds[shape] == kDirect) return true;
+  if (!offsets_ok(a, group)) return false;
+  return kKinds[shape] == kResident ? resident_ok(a) : kKinds[shape] == kStage ? aligned_ok(a) : true;
 }
 
-constexpr int kShapes = 11;
-constexpr int kFirstStaged = 6;
+int pick_shape(const I4Args& a, int group) {
+  if (!offsets_ok(a, group)) return 1;
+  if (resident_ok(a)) return a.rows >= 8192 ? 2 : a.rows > 4096 ? 3 : 4;
+  if (a.batch <= 16) return a.rows >= 8192 ? 5 : 6;
+  if (a.batch <= 32) return 7;
+  if (!aligned_ok(a)) return 8;
+  return a.batch <= 64 ? 9 : a.batch <= 1024 ? 12 : 14;
+}
 
 template <int G, bool OFF>
 int run_gemm(const I4Args& a, int shape, hipStream_t s) {
-  if (shape <= 0) shape = a.batch <= 16 ? (a.rows >= 8192 ? 2 : 3) : a.batch <= 32 ? 4 : !stage_ok(a) ? 1 : a.batch <= 64 ? 5 : a.batch <= 1024 ? 8 : 10;
+  if (shape <= 0) shape = pick_shape(a, G);
   switch (shape) {
     case 1: return run_direct<G, OFF>(a, s);
-    case 2: return run_slice<G, OFF, G == 32 ? 2 : 4, 1, 8, 2>(a, s);
-    case 3: return run_slice<G, OFF, 1, 1, 16, 2>(a, s);
-    case 4: return run_slice<G, OFF, 2, 2, 8, 1>(a, s);
-    case 5: return run_slice<G, OFF, G == 32 ? 1 : 2, 4, 8, 1>(a, s);
-    case 6: return run_stage<G, OFF, 2, 2, 2, 2, 1>(a, s);   // 64 x 64
-    case 7: return run_stage<G, OFF, 4, 1, 2, 4, 2>(a, s);   // 128 x 64, 2 groups
-    case 8: return run_stage<G, OFF, 2, 2, 4, 4, 1>(a, s);   // 128 x 128
-    case 9: return run_stage<G, OFF, 4, 2, 4, 6, 1>(a, s);   // 256 x 192
-    default: return run_stage<G, OFF, 4, 2, 3, 8, 1>(a, s);  // 192 x 256
+    case 2: return run_resident<G, OFF, 4, 8, G == 128 ? 4 : 2>(a, s);
+    case 3: return run_resident<G, OFF, 2, 16, G == 128 ? 4 : 2>(a, s);
+    case 4: return run_resident<G, OFF, 1, 16, G == 128 ? 7 : 4>(a, s);
+    case 5: return run_slice<G, OFF, G == 32 ? 2 : 4, 1, 8, 2>(a, s);
+    case 6: return run_slice<G, OFF, 1, 1, 16, G == 32 ? 2 : 4>(a, s);
+    case 7: return run_slice<G, OFF, 2, 2, 8, 1>(a, s);
+    case 8: return run_slice<G, OFF, G == 32 ? 1 : 2, 4, 8, 1>(a, s);
+    case 9: return run_stage<G, OFF, 2, 2, 2, 2, 1>(a, s);    // 64 x 64
+    case 10: return run_stage<G, OFF, 4, 1, 2, 4, 2>(a, s);   // 128 x 64, 2 groups
+    case 11: return run_stage<G, OFF, 2, 2, 4, 4, 2>(a, s);   // 128 x 128, 2 groups
+    case 12: return run_stage<G, OFF, 2, 2, 4, 4, 1>(a, s);   // 128 x 128
+    case 13: return run_stage<G, OFF, 4, 2, 4, 6, 1>(a, s);   // 256 x 192
+    default: return run_stage<G, OFF, 4, 2, 3, 8, 1>(a, s);   // 192 x 256
   }
 }
 
@@ -901,20 +1084,28 @@ int run_quantize_group(const Q4Args& a, int group, hipStream_t s) {
 
 int i4_gemm_shape_count() { return kShapes; }
 
-bool i4_gemm_shape_ok(int64_t rows, int64_t ldw, const uint16_t* X, int64_t batch, int64_t ldx, int shape) {
+bool i4_gemm_shape_ok(int64_t rows, int64_t cols, int64_t ldw, int group, int64_t lds, int64_t ldo, int st, const uint16_t* X,
+                      int64_t batch, int64_t ldx, int shape) {
   I4Args a{};
   a.X = X;
+  a.rows = rows;
+  a.cols = cols;
+  a.batch = batch;
   a.ldw = rows > 1 ? ldw : 0;
   a.ldx = batch > 1 ? ldx : 0;
-  return shape < kFirstStaged || stage_ok(a);
+  a.lds = cols <= group ? 0 : lds;
+  a.ldo = cols <= group ? 0 : ldo;
+  a.st = st;
+  return shape_ok(a, group, shape);
 }
 
 int launch_i4_gemm(const uint8_t* W, int64_t rows, int64_t cols, int64_t ldw, int group, const void* scale, int64_t lds,
                    const void* offset, int64_t ldo, int st, const uint16_t* X, int64_t batch, int64_t ldx,
                    const float* bias, void* Y, int64_t ldy, int yt, int shape, void* stream) {
   // a single row has no stride
+  const bool one = cols <= group;
   const I4Args a{W, static_cast<const char*>(scale), static_cast<const char*>(offset), X, bias, static_cast<char*>(Y), rows, cols,
-                 rows > 1 ? ldw : 0, lds, ldo, batch, batch > 1 ? ldx : 0, ldy, st, yt};
+                 rows > 1 ? ldw : 0, one ? 0 : lds, one || !offset ? 0 : ldo, batch, batch > 1 ? ldx : 0, ldy, st, yt};
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (group == 32) return offset ? run_gemm<32, true>(a, shape, s) : run_gemm<32, false>(a, shape, s);
   if (group == 64) return offset ? run_gemm<64, true>(a, shape, s) : run_gemm<64, false>(a, shape, s);

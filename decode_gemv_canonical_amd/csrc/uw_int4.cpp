@@ -122,8 +122,8 @@ int uw_i4_gemm_shaped(const uint8_t* d_W, int64_t rows, int64_t cols, int64_t ld
     return rc;
   if (shape < 1 || shape >= i4_gemm_shape_count()) return bad(where, "unknown shape");
   if (batch == 0) return UW_OK;
-  if (!i4_gemm_shape_ok(rows, ldw, d_X, batch, ldx, shape))
-    return fail(UW_ERR_UNSUPPORTED, std::string(where) + ": a staged shape needs 16-byte aligned activation rows and strides below 2^22 bytes");
+  if (!i4_gemm_shape_ok(rows, cols, ldw, group, lds, d_offset ? ldo : 0, st, d_X, batch, ldx, shape))
+    return fail(UW_ERR_UNSUPPORTED, std::string(where) + ": the shape does not take these operands (their alignment, strides or number of tokens)");
   return launch_i4_gemm(d_W, rows, cols, ldw, group, d_scale, lds, d_offset, ldo, st, d_X, batch, ldx, d_bias, d_Y, ldy, yt,
                         shape, stream);
 }

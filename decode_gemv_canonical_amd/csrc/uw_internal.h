@@ -201,7 +201,8 @@ int launch_i4_gemm(const uint8_t* W, int64_t rows, int64_t cols, int64_t ldw, in
                    const void* offset, int64_t ldo, int st, const uint16_t* X, int64_t batch, int64_t ldx,
                    const float* bias, void* Y, int64_t ldy, int yt, int shape, void* stream);
 int i4_gemm_shape_count();
-bool i4_gemm_shape_ok(int64_t rows, int64_t ldw, const uint16_t* X, int64_t batch, int64_t ldx, int shape);
+bool i4_gemm_shape_ok(int64_t rows, int64_t cols, int64_t ldw, int group, int64_t lds, int64_t ldo, int st, const uint16_t* X,
+                      int64_t batch, int64_t ldx, int shape);
 // Cache eviction of the autotuner: read `bytes` (multiple of 16) at src.
 int launch_read_probe(const void* src, size_t bytes, void* sink, void* stream);
 // The allocation-free entry point's scratch (uw_static.hip): its size, the
