@@ -10,10 +10,14 @@
 // row may be read whole.  Scales and offsets lie group by group, [groups,
 // rows], so that the rows of a tile find theirs side by side.
 //
-// Product: q / 16 is exact in bf16 (v_cvt_off_f32_i4 makes it from a nibble),
-// so is its product with a bf16 activation, and the matrix cores add a group's
-// products in fp32; the group's sum is scaled and added in fp32.  Nothing is
-// rounded to fewer bits before Y.  The factor 16 is applied once at the end.
+// Product: u = q + 8 as an 8-bit float code (e4m3: the codes 0 .. 15 stand for
+// 0 .. 15 times 2^-9) is converted to bf16 two at a time, exactly; its product
+// with a bf16 activation is exact too, and the matrix cores add a group's
+// products in fp32.  The sum starts from -8 times the group's sum of
+// activations, so that it ends as sum q x; it is scaled and added in fp32.
+// Nothing is rounded to fewer bits before Y.  (q itself, from
+// v_cvt_off_f32_i4 and a packing, takes 15 operations per 8 weights instead of
+// 9, and the products leave time for 2 operations each.)
 // With A = 16 activation rows and B = 16 weight rows, lane (r = lane % 16, q =
 // lane / 16) holds 8 consecutive k of row r, and of the result weight row r for
 // activation rows 4 q .. 4 q + 3: one scale per lane and tile.
@@ -28,6 +32,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kXcds = 8;
+constexpr int kCus = 256;
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 struct I4Args {
@@ -55,7 +60,7 @@ __device__ __forceinline__ float load_scale(const char* p, int64_t i, int st) {
 // q / 16 of eight nibbles q + 8, in bf16, in order: 14 operations.  The odd
 // nibbles' word is kept apart, so that the conversions take their bytes from
 // the two words by themselves instead of shifting each (18 operations).
-__device__ __forceinline__ bf16x8 decode8(uint32_t w) {
+__device__ __forceinline__ bf16x8 decode_q8(uint32_t w) {
   w ^= 0x88888888u;  // two's complement
   uint32_t h = w >> 4;
   asm("" : "+v"(h));
@@ -64,6 +69,15 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t w) {
   for (int i = 0; i < 4; ++i)
     v[i] = pack_bf16(__builtin_amdgcn_cvt_off_f32_i4(int(w >> (8 * i) & 255u)), __builtin_amdgcn_cvt_off_f32_i4(int(h >> (8 * i) & 255u)));
   return __builtin_bit_cast(bf16x8, v);
+}
+
+// Eight nibbles u in bf16, in order: 9 operations.
+__device__ __forceinline__ bf16x8 decode_u8(uint32_t w) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = w >> 4 & 0x0F0F0F0Fu;
+  const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+  const bf16x2_t v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false), v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true);
+  const bf16x2_t v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false), v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true);
+  return bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
 
 // Values [k, k + 8) of a row of n bf16 values; those past the end read as zero
@@ -97,12 +111,14 @@ __device__ __forceinline__ void store_y(const I4Args& a, int64_t b, int64_t n, f
   else reinterpret_cast<__bf16*>(a.Y)[b * a.ldy + n] = static_cast<__bf16>(v);
 }
 
-// 16 y as it goes out: scaled, the bias added in a rounding of its own.
-__device__ __forceinline__ float finish(float acc, bool biased, float bias) {
-#pragma clang fp contract(off)
-  const float v = acc * 16.f;
-  return biased ? v + bias : v;
+// Eight times -8, whose product with the activations is what the sums start from.
+__device__ __forceinline__ bf16x8 minus_eights() {
+  constexpr uint32_t k = 0xC100C100u;
+  return __builtin_bit_cast(bf16x8, u32x4{k, k, k, k});
 }
+
+// An offset against -8 sum x.
+__device__ __forceinline__ float against_eights(float m) { return m * -0.125f; }
 
 // A workgroup holds 16 weight rows and 16 activation rows; its KS waves split
 // k: wave w takes the blocks of 128 columns w, w + KS, ... and the partial
@@ -122,7 +138,7 @@ __global__ __launch_bounds__(512) void i4_direct_kernel(I4Args a, int n_groups, 
   const uint16_t* xr = a.X + std::min<int64_t>(b0 + r, a.batch - 1) * a.ldx;
   const int64_t last = (a.cols - 1) / 32;  // the rows' last 16-byte word
   const int64_t n_blocks = (a.cols + 127) / 128;
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+  const bf16x8 eights = minus_eights();
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
   f32x4 acc = zero;
   for (int64_t kb = wave; kb < n_blocks; kb += KS) {
@@ -132,16 +148,19 @@ __global__ __launch_bounds__(512) void i4_direct_kernel(I4Args a, int n_groups, 
 #pragma unroll
     for (int g = 0; g < 128 / G; ++g) {
       if (k0 + g * G >= a.cols) break;
-      f32x4 part = zero, sum = zero;
+      bf16x8 x[G / 32];
+      f32x4 sum = zero;
 #pragma unroll
-      for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
-        const bf16x8 x = __builtin_bit_cast(bf16x8, load_x8(xr, k0 + 32 * s + 8 * q, a.cols));
-        part = mfma_bf16(x, decode8(w[s]), part);
-        if (OFF) sum = mfma_bf16(x, ones, sum);
+      for (int s = 0; s < G / 32; ++s) {
+        x[s] = __builtin_bit_cast(bf16x8, load_x8(xr, k0 + g * G + 32 * s + 8 * q, a.cols));
+        sum = mfma_bf16(x[s], eights, sum);
       }
+      f32x4 part = sum;
+#pragma unroll
+      for (int s = 0; s < G / 32; ++s) part = mfma_bf16(x[s], decode_u8(w[g * (G / 32) + s]), part);
       const int64_t at = k0 / G + g;
       const float sc = load_scale(a.scale, at * a.lds + n_in, a.st);
-      const float m = OFF ? load_scale(a.offset, at * a.ldo + n_in, a.st) * 0.0625f : 0.f;
+      const float m = OFF ? against_eights(load_scale(a.offset, at * a.ldo + n_in, a.st)) : 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         acc[e] = fmaf(sc, part[e], acc[e]);
@@ -159,7 +178,7 @@ __global__ __launch_bounds__(512) void i4_direct_kernel(I4Args a, int n_groups, 
   }
   const float bias = a.bias ? a.bias[n_in] : 0.f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) store_y(a, b0 + 4 * q + e, n, finish(acc[e], a.bias, bias));
+  for (int e = 0; e < 4; ++e) store_y(a, b0 + 4 * q + e, n, a.bias ? acc[e] + bias : acc[e]);
 }
 
 // A buffer over an operand: addresses in it are 32-bit offsets, of which the
@@ -191,15 +210,14 @@ struct GroupRows {
     step = __builtin_amdgcn_readfirstlane(uint32_t(ld << shift));
     rsrc = buffer_over(p + (row0 << shift), ((groups - 1) * ld + rows - row0) << shift);
   }
-  __device__ __forceinline__ uint32_t load(uint32_t g, uint32_t row) const {
-    const int voff = int(row << shift), soff = int(__builtin_amdgcn_readfirstlane(g) * step);
+  // group g, row `row` (of the lane) + base
+  __device__ __forceinline__ uint32_t load(uint32_t g, uint32_t row, uint32_t base = 0) const {
+    const int voff = int(row << shift), soff = int(__builtin_amdgcn_readfirstlane(g * step + (base << shift)));
     if (shift == 2) return uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rsrc, voff, soff, 0));
     return uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rsrc, voff, soff, 0));
   }
   __device__ __forceinline__ float value(uint32_t raw) const { return bits_f32(shift == 2 ? raw : raw << 16); }
 };
-
-constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
 
 // Few tokens: bound by the weights' read.  A workgroup holds 16 WI weight rows
 // and 16 BJ activation rows, and its KW waves split k: wave w takes the blocks
@@ -266,7 +284,7 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
         if (live[j]) b.x[j][s] = load_x8(xr[j], k, a.cols);
       }
   };
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{kOnes, kOnes, kOnes, kOnes});
+  const bf16x8 eights = minus_eights();
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
   f32x4 acc[WI][BJ];
 #pragma unroll
@@ -282,22 +300,22 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
     for (int g = 0; g < GB; ++g) {
       f32x4 part[WI][BJ], sum[BJ];
 #pragma unroll
+      for (int s = 0; s < 4 / GB; ++s)
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) sum[j] = mfma_bf16(__builtin_bit_cast(bf16x8, b.x[j][g * (4 / GB) + s]), eights, s ? sum[j] : zero);
+#pragma unroll
       for (int s = 0; s < 4 / GB; ++s) {
         const int at = g * (4 / GB) + s;
 #pragma unroll
         for (int i = 0; i < WI; ++i) {
-          const bf16x8 w = decode8(b.w[i][at]);
+          const bf16x8 w = decode_u8(b.w[i][at]);
 #pragma unroll
-          for (int j = 0; j < BJ; ++j) part[i][j] = mfma_bf16(__builtin_bit_cast(bf16x8, b.x[j][at]), w, s ? part[i][j] : zero);
-        }
-        if (OFF) {
-#pragma unroll
-          for (int j = 0; j < BJ; ++j) sum[j] = mfma_bf16(__builtin_bit_cast(bf16x8, b.x[j][at]), ones, s ? sum[j] : zero);
+          for (int j = 0; j < BJ; ++j) part[i][j] = mfma_bf16(__builtin_bit_cast(bf16x8, b.x[j][at]), w, s ? part[i][j] : sum[j]);
         }
       }
 #pragma unroll
       for (int i = 0; i < WI; ++i) {
-        const float sc = scale.value(b.s[i][g]), m = OFF ? offset.value(b.m[i][g]) * 0.0625f : 0.f;
+        const float sc = scale.value(b.s[i][g]), m = OFF ? against_eights(offset.value(b.m[i][g])) : 0.f;
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
 #pragma unroll
@@ -338,7 +356,7 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
     }
     const float bias = a.bias ? a.bias[nn] : 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) store_y(a, b + e, nn, finish(total[e], a.bias, bias));
+    for (int e = 0; e < 4; ++e) store_y(a, b + e, nn, a.bias ? total[e] + bias : total[e]);
   }
 }
 
@@ -369,6 +387,13 @@ __device__ __forceinline__ void store_row16(const I4Args& a, int64_t b, int64_t 
 
 template <int WI>
 constexpr int epilogue_bytes = 16 * (16 * WI * 4 + 16);
+
+// 16 y as it goes out, the bias added in a rounding of its own.
+__device__ __forceinline__ float finish(float acc, bool biased, float bias) {
+#pragma clang fp contract(off)
+  const float v = acc * 16.f;
+  return biased ? v + bias : v;
+}
 
 // Epilogue of a wave's WI x BJ tiles at (n0, b0), through LDS: 16 activation
 // rows at a time as the wave's 16 WI columns, so that rows go out in runs of
@@ -406,50 +431,51 @@ __device__ __forceinline__ void store_through_lds(const I4Args& a, int64_t n0, i
   }
 }
 
-// The fewest tokens (at most 16, whose activations fit in LDS): a workgroup
-// holds 16 WI weight rows; the activations are put into LDS once, while the
-// first weights are on their way, and each of the KW waves takes the blocks of
-// 128 columns w, w + KW, ... with D of them in flight in registers.
+// The fewest tokens (at most 16, whose activations fit in LDS): bound by the
+// weights' read, which has to run on without a pause.  A workgroup stays on its
+// compute unit and takes the tiles of 16 weight rows blockIdx, blockIdx + grid,
+// ...  It puts the activations into LDS once.  Of every tile, wave w takes the
+// blocks of 128 columns w, w + KW, ..., with D of them in flight in registers,
+// those of the next tiles among them; at a tile's end the waves put their sums
+// into LDS, and one of them adds them up while the others go on.
 // An activation row starts 16 bytes further into the banks than the one before
 // it; lanes of tokens that are not there read the last one's again, into
 // results that are not written.
-template <int G, bool OFF, int WI, int KW, int D>
-__global__ __launch_bounds__(64 * KW) void i4_resident_kernel(I4Args a, int nw_tiles, uint32_t pitch) {
+// LDS: activations; -8 times their sums, per group and token; the waves' sums
+// of two tiles, of the tokens that are there.
+template <int G, bool OFF, int KW, int D>
+__global__ __launch_bounds__(64 * KW) void i4_stream_kernel(I4Args a, int n_tiles, uint32_t pitch) {
   constexpr int GB = 128 / G;  // groups of a block
-  const int wt = int(blockIdx.x);
-  if (wt >= nw_tiles) return;
-  const int64_t row0 = int64_t(wt) * 16 * WI;
   const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int r = lane % 16, q = lane / 16, batch = int(a.batch);
-  const uint32_t wlast = uint32_t(std::min<int64_t>(16 * WI, a.rows - row0)) - 1;  // rows past the last are that row again
-  const auto wbuf = buffer_over(a.W + row0 * a.ldw, int64_t(wlast) * a.ldw + (a.cols + 31) / 32 * 16);
-  const int64_t groups = (a.cols + G - 1) / G;
-  const GroupRows scale(a.scale, a.lds, a.st, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, a.st, groups, a.rows, row0);
-  uint32_t wr[WI], wvo[WI];
-#pragma unroll
-  for (int i = 0; i < WI; ++i) {
-    wr[i] = min(uint32_t(16 * i + r), wlast);
-    wvo[i] = wr[i] * uint32_t(a.ldw) + 16 * q;
-  }
-  const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
+  const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks of a tile
+  const int grid = int(gridDim.x), tiles = (n_tiles - int(blockIdx.x) + grid - 1) / grid;
+  const uint32_t groups = uint32_t((a.cols + G - 1) / G);
+  const uint32_t sums = uint32_t(batch) * pitch, parts = sums + uint32_t(nkb) * (GB * 64);
+  const uint32_t part_bytes = uint32_t((batch + 3) / 4) * 256;  // of a wave
+  // past a row's last word comes the next row, past the last row nothing: zeros
+  const auto wbuf = buffer_over(a.W, (a.rows - 1) * a.ldw + (a.cols + 31) / 32 * 16);
+  const GroupRows scale(a.scale, a.lds, a.st, groups, a.rows, 0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, a.st, groups, a.rows, 0);
+  const uint32_t wvo = uint32_t(r) * uint32_t(a.ldw) + 16 * q;
   struct Block {
-    u32x4 w[WI];
-    uint32_t s[WI][GB], m[WI][GB];
+    u32x4 w;
+    uint32_t s[GB], m[GB];
   };
   Block ring[D];
-  auto load = [&](Block& b, int i) {
-    const int kb = wave + KW * i;
-    // past a row's last word comes the next row: whole numbers against activations of zero
-#pragma unroll
-    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16<true>(wbuf, wvo[t], uint32_t(kb) * 64);
+  int lt = int(blockIdx.x), lb = 0, left = tiles * n;  // the next block to load: its tile and place; how many are left
+  auto load = [&](Block& b) {
+    const int kb = wave + KW * lb;
+    b.w = buffer_load16<false>(wbuf, wvo, uint32_t(lt) * 16 * uint32_t(a.ldw) + uint32_t(kb) * 64);
 #pragma unroll
     for (int g = 0; g < GB; ++g) {
-      const uint32_t gi = min(uint32_t(kb * GB + g), uint32_t(groups - 1));
-#pragma unroll
-      for (int t = 0; t < WI; ++t) {
-        b.s[t][g] = scale.load(gi, wr[t]);
-        if (OFF) b.m[t][g] = offset.load(gi, wr[t]);
-      }
+      const uint32_t gi = min(uint32_t(kb * GB + g), groups - 1);
+      b.s[g] = scale.load(gi, r, uint32_t(lt) * 16);
+      if (OFF) b.m[g] = offset.load(gi, r, uint32_t(lt) * 16);
+    }
+    --left;
+    if (++lb == n) {
+      lb = 0;
+      lt += grid;
     }
   };
   // the activations: chunk c of 8 columns of row b at b pitch + 16 c, zeros past the last column
@@ -459,74 +485,85 @@ __global__ __launch_bounds__(64 * KW) void i4_resident_kernel(I4Args a, int nw_t
   if (t0 < batch * chunks) first = load_x8(a.X + int64_t(t0 / chunks) * a.ldx, 8 * int64_t(t0 % chunks), a.cols);
 #pragma unroll
   for (int d = 0; d < D; ++d)
-    if (d < n) load(ring[d], d);
+    if (left > 0) load(ring[d]);
   if (t0 < batch * chunks) st128(uint32_t(t0 / chunks) * pitch + uint32_t(t0 % chunks) * 16, __builtin_bit_cast(uint4, first));
   for (int at = t0 + 64 * KW; at < batch * chunks; at += 64 * KW)
     st128(uint32_t(at / chunks) * pitch + uint32_t(at % chunks) * 16,
           __builtin_bit_cast(uint4, load_x8(a.X + int64_t(at / chunks) * a.ldx, 8 * int64_t(at % chunks), a.cols)));
   lds_barrier();
   const uint32_t xat = uint32_t(min(r, batch - 1)) * pitch;
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{kOnes, kOnes, kOnes, kOnes});
+  // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
+  auto read_x = [&](int kb, int s) {
+    return __builtin_bit_cast(bf16x8, ld128(xat + uint32_t(kb) * 256 + uint32_t(G == 128 ? 4 * q + s : 4 * s + q) * 16));
+  };
+  const bf16x8 eights = minus_eights();
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
-  f32x4 acc[WI];
+  for (int kb = wave; kb < nkb; kb += KW) {
+    f32x4 sum[GB];
 #pragma unroll
-  for (int i = 0; i < WI; ++i) acc[i] = zero;
-  auto multiply = [&](Block& b, int i) {
-    const uint32_t at = xat + uint32_t(wave + KW * i) * 256;
+    for (int s = 0; s < 4; ++s) sum[s / (4 / GB)] = mfma_bf16(read_x(kb, s), eights, s % (4 / GB) ? sum[s / (4 / GB)] : zero);
+#pragma unroll
+    for (int g = 0; g < GB; ++g)
+      if (r == 0) st128(sums + uint32_t(kb * GB + g) * 64 + 16 * q, __builtin_bit_cast(uint4, sum[g]));
+  }
+  wave_lds_fence();
+  f32x4 acc = zero;
+  auto multiply = [&](Block& b, int kb) {
     bf16x8 x[4];
-    // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
 #pragma unroll
-    for (int s = 0; s < 4; ++s) x[s] = __builtin_bit_cast(bf16x8, ld128(at + uint32_t(G == 128 ? 4 * q + s : 4 * s + q) * 16));
-    if (G != 128) {
-#pragma unroll
-      for (int t = 0; t < WI; ++t) transpose4(b.w[t]);
-    }
+    for (int s = 0; s < 4; ++s) x[s] = read_x(kb, s);
+    if (G != 128) transpose4(b.w);
 #pragma unroll
     for (int g = 0; g < GB; ++g) {
-      f32x4 part[WI], sum;
+      const f32x4 sum = __builtin_bit_cast(f32x4, ld128(sums + uint32_t(kb * GB + g) * 64 + 16 * q));
+      f32x4 part = sum;
 #pragma unroll
-      for (int s = 0; s < 4 / GB; ++s) {
-        const int k = g * (4 / GB) + s;
+      for (int s = 0; s < 4 / GB; ++s) part = mfma_bf16(x[g * (4 / GB) + s], decode_u8(b.w[g * (4 / GB) + s]), part);
+      const float sc = scale.value(b.s[g]), m = OFF ? against_eights(offset.value(b.m[g])) : 0.f;
 #pragma unroll
-        for (int t = 0; t < WI; ++t) part[t] = mfma_bf16(x[k], decode8(b.w[t][k]), s ? part[t] : zero);
-        if (OFF) sum = mfma_bf16(x[k], ones, s ? sum : zero);
-      }
-#pragma unroll
-      for (int t = 0; t < WI; ++t) {
-        const float sc = scale.value(b.s[t][g]), m = OFF ? offset.value(b.m[t][g]) * 0.0625f : 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[t][e] = fmaf(sc, part[t][e], acc[t][e]);
-          if (OFF) acc[t][e] = fmaf(m, sum[e], acc[t][e]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        acc[e] = fmaf(sc, part[e], acc[e]);
+        if (OFF) acc[e] = fmaf(m, sum[e], acc[e]);
       }
     }
   };
-  for (int i = 0; i < n; i += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (i + d < n) multiply(ring[d], i + d);
-      if (i + d + D < n) load(ring[d], i + d + D);
-    }
-  }
-  __syncthreads();  // no wave reads the activations any more
-#pragma unroll
-  for (int i = 0; i < WI; ++i)
-    if (4 * q < batch) st128(uint32_t((wave * WI + i) * 1024 + 16 * lane), __builtin_bit_cast(uint4, acc[i]));
-  __syncthreads();
-  for (int t = wave; t < WI; t += KW) {
-    const int64_t nn = row0 + 16 * t + r;
-    if (4 * q >= batch || nn >= a.rows) continue;
+  // the end of a tile: every wave's sums, added by one of them
+  auto finish_tile = [&](int t) {
+    const uint32_t at = parts + uint32_t(t & 1) * (KW * part_bytes);
+    if (4 * q < batch) st128(at + uint32_t(wave) * part_bytes + 16 * lane, __builtin_bit_cast(uint4, acc));
+    acc = zero;
+    lds_barrier();
+    const int64_t nn = (int64_t(blockIdx.x) + int64_t(t) * grid) * 16 + r;
+    if (wave != t % KW || 4 * q >= batch || nn >= a.rows) return;
     f32x4 total = zero;
 #pragma unroll
     for (int w = 0; w < KW; ++w) {
-      const f32x4 v = __builtin_bit_cast(f32x4, ld128(uint32_t((w * WI + t) * 1024 + 16 * lane)));
+      const f32x4 v = __builtin_bit_cast(f32x4, ld128(at + uint32_t(w) * part_bytes + 16 * lane));
 #pragma unroll
       for (int e = 0; e < 4; ++e) total[e] += v[e];
     }
     const float bias = a.bias ? a.bias[nn] : 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) store_y(a, 4 * q + e, nn, finish(total[e], a.bias, bias));
+    for (int e = 0; e < 4; ++e) store_y(a, 4 * q + e, nn, a.bias ? total[e] + bias : total[e]);
+  };
+  if (n == 0) {
+    for (int t = 0; t < tiles; ++t) finish_tile(t);
+    return;
+  }
+  int t = 0, at = 0;  // the tile and the place of the block at hand
+  while (t < tiles) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (t < tiles) {
+        multiply(ring[d], wave + KW * at);
+        if (left > 0) load(ring[d]);
+        if (++at == n) {
+          finish_tile(t);
+          at = 0;
+          ++t;
+        }
+      }
+    }
   }
 }
 
@@ -642,6 +679,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
       }
     }
   };
+  constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
   const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{kOnes, kOnes, kOnes, kOnes});
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
   f32x4 acc[WI][BJ];
@@ -659,7 +697,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
       u32x4 v = __builtin_bit_cast(u32x4, ld128(base + wat + uint32_t(t) * 1024));
       if (G != 128) transpose4(v);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) w[t][s] = decode8(v[s]);
+      for (int s = 0; s < 4; ++s) w[t][s] = decode_q8(v[s]);
     }
     // one tile of tokens at a time: the next one's operands are read and the last one's sums are scaled while this one's
     // products run; the barriers keep the compiler from holding more tiles than that in registers
@@ -955,21 +993,23 @@ int run_direct(const I4Args& a, hipStream_t s) {
   return hip_check(hipGetLastError(), "i4_direct_kernel launch");
 }
 
-// LDS of the resident kernel: its activation rows, then its partial tiles.
-uint32_t resident_pitch(const I4Args& a) { return uint32_t((a.cols + 127) / 128 * 256 + 16); }
-bool resident_ok(const I4Args& a) {
-  return a.batch <= 16 && a.cols <= 65536 && a.batch * int64_t(resident_pitch(a)) <= kLdsLimit;
+// LDS of the stream kernel.
+uint32_t stream_pitch(int64_t cols) { return uint32_t((cols + 127) / 128 * 256 + 16); }
+int64_t stream_lds(const I4Args& a, int group, int kw) {
+  return a.batch * int64_t(stream_pitch(a.cols)) + (a.cols + 127) / 128 * (128 / group) * 64 + int64_t(2) * kw * (a.batch + 3) / 4 * 256;
+}
+bool stream_ok(const I4Args& a, int group, int kw) {
+  return a.batch <= 16 && a.cols <= 65536 && (a.rows + 16) * a.ldw < (int64_t(1) << 31) && stream_lds(a, group, kw) <= kLdsLimit;
 }
 
-template <int G, bool OFF, int WI, int KW, int D>
-int run_resident(const I4Args& a, hipStream_t s) {
-  const int64_t nw = (a.rows + 16 * WI - 1) / (16 * WI);
-  if (int rc = check_launch(nw, 1, KW * kWave)) return rc;
-  auto kern = i4_resident_kernel<G, OFF, WI, KW, D>;
+template <int G, bool OFF, int KW, int D>
+int run_stream(const I4Args& a, hipStream_t s) {
+  const int64_t tiles = (a.rows + 15) / 16, lds = stream_lds(a, G, KW);
+  const int64_t grid = std::min<int64_t>(tiles, kCus * std::max<int64_t>(1, std::min<int64_t>(16 / KW, kLdsLimit / lds)));
+  auto kern = i4_stream_kernel<G, OFF, KW, D>;
   allow_full_lds(kern);
-  const size_t lds = std::max(size_t(a.batch) * resident_pitch(a), size_t(KW) * WI * 1024);
-  hipLaunchKernelGGL(kern, dim3(unsigned(nw)), dim3(KW * kWave), lds, s, a, int(nw), resident_pitch(a));
-  return hip_check(hipGetLastError(), "i4_resident_kernel launch");
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(KW * kWave), size_t(lds), s, a, int(tiles), stream_pitch(a.cols));
+  return hip_check(hipGetLastError(), "i4_stream_kernel launch");
 }
 
 template <int G, bool OFF, int WI, int BJ, int KW, int D>
@@ -1009,19 +1049,19 @@ bool offsets_ok(const I4Args& a, int group) {
 bool aligned_ok(const I4Args& a) { return reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 8 == 0; }
 
 constexpr int kShapes = 15;
-enum Kind { kDirect, kResident, kSlice, kStage };
-constexpr Kind kKinds[kShapes] = {kDirect, kDirect, kResident, kResident, kResident, kSlice, kSlice, kSlice, kSlice,
+enum Kind { kDirect, kStream, kSlice, kStage };
+constexpr Kind kKinds[kShapes] = {kDirect, kDirect, kStream, kStream, kStream, kSlice, kSlice, kSlice, kSlice,
                                   kStage, kStage, kStage, kStage, kStage, kStage};
 
 bool shape_ok(const I4Args& a, int group, int shape) {
   if (kKinds[shape] == kDirect) return true;
   if (!offsets_ok(a, group)) return false;
-  return kKinds[shape] == kResident ? resident_ok(a) : kKinds[shape] == kStage ? aligned_ok(a) : true;
+  return kKinds[shape] == kStream ? stream_ok(a, group, shape == 2 ? 16 : 8) : kKinds[shape] == kStage ? aligned_ok(a) : true;
 }
 
 int pick_shape(const I4Args& a, int group) {
   if (!offsets_ok(a, group)) return 1;
-  if (resident_ok(a)) return a.rows >= 8192 ? 2 : a.rows > 4096 ? 3 : 4;
+  if (shape_ok(a, group, 2)) return 2;
   if (a.batch <= 16) return a.rows >= 8192 ? 5 : 6;
   if (a.batch <= 32) return 7;
   if (!aligned_ok(a)) return 8;
@@ -1033,11 +1073,11 @@ int run_gemm(const I4Args& a, int shape, hipStream_t s) {
   if (shape <= 0) shape = pick_shape(a, G);
   switch (shape) {
     case 1: return run_direct<G, OFF>(a, s);
-    case 2: return run_resident<G, OFF, 4, 8, G == 128 ? 4 : 2>(a, s);
-    case 3: return run_resident<G, OFF, 2, 16, G == 128 ? 4 : 2>(a, s);
-    case 4: return run_resident<G, OFF, 1, 16, G == 128 ? 7 : 4>(a, s);
+    case 2: return run_stream<G, OFF, 16, 4>(a, s);
+    case 3: return run_stream<G, OFF, 8, 8>(a, s);
+    case 4: return run_stream<G, OFF, 8, 4>(a, s);
     case 5: return run_slice<G, OFF, G == 32 ? 2 : 4, 1, 8, 2>(a, s);
-    case 6: return run_slice<G, OFF, 1, 1, 16, G == 32 ? 2 : 4>(a, s);
+    case 6: return run_slice<G, OFF, 1, 1, 16, 2>(a, s);
     case 7: return run_slice<G, OFF, 2, 2, 8, 1>(a, s);
     case 8: return run_slice<G, OFF, G == 32 ? 1 : 2, 4, 8, 1>(a, s);
     case 9: return run_stage<G, OFF, 2, 2, 2, 2, 1>(a, s);    // 64 x 64

@@ -728,7 +728,7 @@ int uw_block_norm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int
  * as q + 8, the even column in the low half; rows start at 16-byte boundaries
  * (d_Q 16-byte aligned, ldq in bytes, a multiple of 16 and at least 16 *
  * ceil(cols / 32)), and whole 16-byte words of a row are read, whatever lies
- * past its last column.  Scales and offsets lie group by group: ceil(cols /
+ * past its last column, and bytes between two rows may be.  Scales and offsets lie group by group: ceil(cols /
  * group) rows of `rows` elements of st (UW_F32 or UW_BF16) with strides lds and
  * ldo.  So the weights of a row-major [rows, cols / 8] int32 matrix of unsigned
  * nibbles u with scales s and zero points z are d_Q as it is, s, and
@@ -767,16 +767,16 @@ int uw_i4_dequantize(const uint8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq
  * uw_i4_gemm (device) - Y[b, n] = sum_k X[b, k] W[n, k] (+ bias[n]) over 4-bit
  * weights, on the matrix cores, for any number of tokens:
  *   Y = sum over groups of scale * (sum of q x) + offset * (sum of x).
- * Products are exact, every sum is fp32; only Y is rounded further.
+ * Products are exact, every sum is fp32; only Y is rounded further.  (For few
+ * tokens a group's sum of q x is formed as that of (q + 8) x and -8 x.)
  *   d_W, ldw, group, scales and offsets as above (d_offset may be NULL).
  *   d_X   batch rows of cols bf16 elements, stride ldx >= cols; rows on
  *         16-byte boundaries (ldx a multiple of 8) are read fastest.
  *   d_bias  rows fp32 values, or NULL.
  *   d_Y   batch rows of `rows` elements of yt (UW_F32 or UW_BF16), stride ldy.
  * Results depend on the batch and the sizes (the order of the sum), not on
- * anything else; an infinity or a NaN in a token shows in that token's row
- * alone.  With offsets an infinite activation may give NaN where scale * q +
- * offset times it is infinite.
+ * anything else.  A token that holds an infinity or a NaN gets no finite value
+ * in its row, and the others nothing of it.
  * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (more tiles than a launch holds),
  *         UW_ERR_HIP.
  */

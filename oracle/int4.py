@@ -88,10 +88,11 @@ def dequantize_f32(q: np.ndarray, scale: np.ndarray, offset, group: int) -> np.n
 
 
 def gemm(q, scale, offset, group, x, bias=None):
-    """(y, mass) in fp64: the product, and the sum of the terms' magnitudes, which its rounding errors go by."""
+    """(y, mass) in fp64: the product, and what its rounding errors go by: the
+    sum of the magnitudes of (q + 8) x s, -8 x s and m x."""
     x = np.asarray(x, np.float64)
     y = x @ values(q, scale, offset, group).T
-    mass = np.abs(x) @ np.abs(values(np.abs(q), np.abs(scale), None if offset is None else np.abs(offset), group)).T
+    mass = np.abs(x) @ values(np.asarray(q, np.int64) + 16, np.abs(scale), None if offset is None else np.abs(offset), group).T
     return (y if bias is None else y + np.asarray(bias, np.float64)), mass
 
 
