@@ -198,35 +198,37 @@ __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_
   return __builtin_amdgcn_raw_buffer_load_b128(r, int(voff), int(soff), NT ? 2 : 0);
 }
 
-// Scales and offsets of a tile's rows: as they lie in memory, so that a load is
-// not waited for before its value is used.
+// Scales and offsets of the rows from row0 on (S32: fp32, else bf16), loaded as
+// they lie in memory: apart from their value, so that a load is not waited for
+// before it is used.
+template <bool S32>
 struct GroupRows {
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t step;  // bytes between groups
-  int shift;      // log2 of an element's bytes: 1 (bf16) or 2 (fp32)
+  static constexpr int kShift = S32 ? 2 : 1;
 
-  __device__ __forceinline__ GroupRows(const char* p, int64_t ld, int st, int64_t groups, int64_t rows, int64_t row0)
-      : shift(st == UW_F32 ? 2 : 1) {
-    step = __builtin_amdgcn_readfirstlane(uint32_t(ld << shift));
-    rsrc = buffer_over(p + (row0 << shift), ((groups - 1) * ld + rows - row0) << shift);
+  __device__ __forceinline__ GroupRows(const char* p, int64_t ld, int64_t groups, int64_t rows, int64_t row0) {
+    step = __builtin_amdgcn_readfirstlane(uint32_t(ld << kShift));
+    rsrc = buffer_over(p + (row0 << kShift), ((groups - 1) * ld + rows - row0) << kShift);
   }
-  // group g, row `row` (of the lane) + base
+  // group g (of the wave), row `row` (of the lane) + base (of the wave)
   __device__ __forceinline__ uint32_t load(uint32_t g, uint32_t row, uint32_t base = 0) const {
-    const int voff = int(row << shift), soff = int(__builtin_amdgcn_readfirstlane(g * step + (base << shift)));
-    if (shift == 2) return uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rsrc, voff, soff, 0));
+    const int voff = int(row << kShift), soff = int(__builtin_amdgcn_readfirstlane(g * step + (base << kShift)));
+    if (S32) return uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rsrc, voff, soff, 0));
     return uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rsrc, voff, soff, 0));
   }
-  __device__ __forceinline__ float value(uint32_t raw) const { return bits_f32(shift == 2 ? raw : raw << 16); }
+  __device__ __forceinline__ static float value(uint32_t raw) { return bits_f32(S32 ? raw : raw << 16); }
 };
 
 // Few tokens: bound by the weights' read.  A workgroup holds 16 WI weight rows
 // and 16 BJ activation rows, and its KW waves split k: wave w takes the blocks
 // of 128 columns w, w + KW, ...  A wave keeps D blocks in flight in registers
 // (weights, activations and scales), each refilled as soon as it is used, and
-// meets the others only to add the partial tiles at the end.  Lanes of tokens
-// that are not there load nothing.  NT: the weights are read by this
-// workgroup alone.
-template <int G, bool OFF, int WI, int BJ, int KW, int D, bool NT>
+// meets the others only to add the partial tiles at the end.
+// Loads of blocks that are not there are made all the same, from one address:
+// where a load hangs on a branch, the wait for an older one becomes a wait for
+// all.  A last block that is not whole comes at the end, by itself.
+template <int G, bool OFF, bool S32, int WI, int BJ, int KW, int D>
 __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tiles, int nb_tiles) {
   constexpr int GB = 128 / G;  // groups of a block
   // the batch tiles of one weight tile run back to back on one XCD
@@ -238,51 +240,48 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
   const int r = lane % 16, q = lane / 16;
   const uint32_t wlast = uint32_t(std::min<int64_t>(16 * WI, a.rows - row0)) - 1;  // rows past the last are that row again
   const auto wbuf = buffer_over(a.W + row0 * a.ldw, int64_t(wlast) * a.ldw + (a.cols + 31) / 32 * 16);
-  const int64_t groups = (a.cols + G - 1) / G;
-  const GroupRows scale(a.scale, a.lds, a.st, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, a.st, groups, a.rows, row0);
+  const uint32_t groups = uint32_t((a.cols + G - 1) / G);
+  const GroupRows<S32> scale(a.scale, a.lds, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, groups, a.rows, row0);
   uint32_t wr[WI], wvo[WI];
 #pragma unroll
   for (int i = 0; i < WI; ++i) {
     wr[i] = min(uint32_t(16 * i + r), wlast);
     wvo[i] = wr[i] * uint32_t(a.ldw) + 16 * q;
   }
-  const uint16_t* xr[BJ];
-  bool live[BJ];
+  // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
+  constexpr int kStep = G == 128 ? 8 : 32;
+  const char* xt = reinterpret_cast<const char*>(a.X + b0 * a.ldx);
+  uint32_t xvo[BJ];
 #pragma unroll
-  for (int j = 0; j < BJ; ++j) {
-    live[j] = b0 + 16 * j + r < a.batch;
-    // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
-    xr[j] = a.X + std::min<int64_t>(b0 + 16 * j + r, a.batch - 1) * a.ldx;
-  }
-  const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
+  for (int j = 0; j < BJ; ++j)  // tokens past the last are that token again, into results that are not written
+    xvo[j] = 2 * (uint32_t(std::min<int64_t>(16 * j + r, a.batch - b0 - 1)) * uint32_t(a.ldx) + uint32_t(G == 128 ? 32 * q : 8 * q));
+  const int nfull = int(a.cols / 128), n = (nfull - wave + KW - 1) / KW;  // this wave's whole blocks
   struct Block {
     u32x4 w[WI], x[BJ][4];
     uint32_t s[WI][GB], m[WI][GB];
   };
   Block ring[D];
-  auto load = [&](Block& b, int i) {
-    const int kb = wave + KW * i;
-    const int64_t k0 = int64_t(kb) * 128;
-    // past a row's last word comes the next row: whole numbers against activations of zero
+  auto load_weights = [&](Block& b, int kb) {
 #pragma unroll
-    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16<NT>(wbuf, wvo[t], uint32_t(kb) * 64);
+    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16<false>(wbuf, wvo[t], uint32_t(kb) * 64);
 #pragma unroll
     for (int g = 0; g < GB; ++g) {
-      const uint32_t gi = min(uint32_t(kb * GB + g), uint32_t(groups - 1));
+      const uint32_t gi = min(uint32_t(kb * GB + g), groups - 1);
 #pragma unroll
       for (int t = 0; t < WI; ++t) {
         b.s[t][g] = scale.load(gi, wr[t]);
         if (OFF) b.m[t][g] = offset.load(gi, wr[t]);
       }
     }
+  };
+  auto load = [&](Block& b, int i) {
+    const int kb = i < n ? wave + KW * i : 0;
+    const char* at = xt + int64_t(kb) * 256;
 #pragma unroll
     for (int j = 0; j < BJ; ++j)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int64_t k = k0 + (G == 128 ? 32 * q + 8 * s : 32 * s + 8 * q);
-        b.x[j][s] = u32x4{0u, 0u, 0u, 0u};
-        if (live[j]) b.x[j][s] = load_x8(xr[j], k, a.cols);
-      }
+      for (int s = 0; s < 4; ++s) b.x[j][s] = load16_any(at + (xvo[j] + 2 * kStep * s));
+    load_weights(b, kb);
   };
   const bf16x8 eights = minus_eights();
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
@@ -326,15 +325,30 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
       }
     }
   };
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (d < n) load(ring[d], d);
-  for (int i = 0; i < n; i += D) {
+  if (n > 0) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (i + d < n) multiply(ring[d]);
-      if (i + d + D < n) load(ring[d], i + d + D);
+      load(ring[d], d);
+      __builtin_amdgcn_sched_barrier(0);  // in this order, which the waits count on
     }
+    for (int i = 0; i < n; i += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (i + d < n) multiply(ring[d]);
+        load(ring[d], i + d + D);
+      }
+    }
+  }
+  if (nfull * 128 < a.cols && nfull % KW == wave) {
+    Block b;
+    load_weights(b, nfull);
+#pragma unroll
+    for (int j = 0; j < BJ; ++j) {
+      const uint16_t* row = a.X + std::min<int64_t>(b0 + 16 * j + r, a.batch - 1) * a.ldx;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) b.x[j][s] = load_x8(row, int64_t(nfull) * 128 + (G == 128 ? 32 * q : 8 * q) + kStep * s, a.cols);
+    }
+    multiply(b);
   }
   // partial tile (i, j) of wave w at (w WI BJ + i BJ + j) KB
 #pragma unroll
@@ -354,9 +368,323 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
 #pragma unroll
       for (int e = 0; e < 4; ++e) total[e] += v[e];
     }
-    const float bias = a.bias ? a.bias[nn] : 0.f;
+    if (a.bias) {
+      const float bias = a.bias[nn];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) store_y(a, b + e, nn, a.bias ? total[e] + bias : total[e]);
+      for (int e = 0; e < 4; ++e) total[e] += bias;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) store_y(a, b + e, nn, total[e]);
+  }
+}
+
+// Up to NB = 1 or 4 tokens.  As the slices, with WI tiles of 16 weight rows per
+// workgroup, but a block's activations are 256 bytes per token: one 4-byte load
+// of the wave (in the operand's layout it would be four of 16 bytes, most of
+// them for tokens that are not there), put in order by the wave's own corner of
+// LDS.
+template <int G, bool OFF, bool S32, int WI, int NB, int KW, int D>
+__global__ __launch_bounds__(64 * KW) void i4_token_kernel(I4Args a, int nw_tiles) {
+  constexpr int GB = 128 / G;       // groups of a block
+  constexpr uint32_t kRow = 272;    // a token's 256 bytes, 16 further into the banks than the one before
+  const int wt = int(blockIdx.x);
+  if (wt >= nw_tiles) return;
+  const int64_t row0 = int64_t(wt) * 16 * WI;
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int r = lane % 16, q = lane / 16, batch = int(a.batch);
+  const uint32_t wlast = uint32_t(std::min<int64_t>(16 * WI, a.rows - row0)) - 1;  // rows past the last are that row again
+  const auto wbuf = buffer_over(a.W + row0 * a.ldw, int64_t(wlast) * a.ldw + (a.cols + 31) / 32 * 16);
+  const uint32_t groups = uint32_t((a.cols + G - 1) / G);
+  const GroupRows<S32> scale(a.scale, a.lds, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, groups, a.rows, row0);
+  uint32_t wr[WI], wvo[WI];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) {
+    wr[i] = min(uint32_t(16 * i + r), wlast);
+    wvo[i] = wr[i] * uint32_t(a.ldw) + 16 * q;
+  }
+  const int nfull = int(a.cols / 128), n = (nfull - wave + KW - 1) / KW;  // this wave's whole blocks
+  struct Block {
+    u32x4 w[WI];
+    uint32_t x[NB], s[WI][GB], m[WI][GB];
+  };
+  Block ring[D];
+  auto load_weights = [&](Block& b, int kb) {
+#pragma unroll
+    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16<false>(wbuf, wvo[t], uint32_t(kb) * 64);
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      const uint32_t gi = min(uint32_t(kb * GB + g), groups - 1);
+#pragma unroll
+      for (int t = 0; t < WI; ++t) {
+        b.s[t][g] = scale.load(gi, wr[t]);
+        if (OFF) b.m[t][g] = offset.load(gi, wr[t]);
+      }
+    }
+  };
+  auto load = [&](Block& b, int i) {
+    const int kb = i < n ? wave + KW * i : 0;
+#pragma unroll
+    for (int t = 0; t < NB; ++t) {
+      const char* at = reinterpret_cast<const char*>(a.X + int64_t(min(t, batch - 1)) * a.ldx) + int64_t(kb) * 256;
+      __builtin_memcpy(&b.x[t], at + 4 * lane, 4);
+    }
+    load_weights(b, kb);
+  };
+  const uint32_t corner = uint32_t(wave) * (NB * kRow);
+  const uint32_t xat = corner + uint32_t(min(r, NB - 1)) * kRow + (G == 128 ? 64 * q : 16 * q);
+  constexpr uint32_t kStep = G == 128 ? 16 : 64;  // lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
+  const bf16x8 eights = minus_eights();
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[WI];
+#pragma unroll
+  for (int i = 0; i < WI; ++i) acc[i] = zero;
+  auto multiply = [&](Block& b) {
+    bf16x8 x[4];
+#pragma unroll
+    for (int t = 0; t < NB; ++t) st32(corner + uint32_t(t) * kRow + 4 * lane, b.x[t]);
+    wave_lds_fence();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) x[s] = __builtin_bit_cast(bf16x8, ld128(xat + kStep * s));
+    wave_lds_fence();
+    if (G != 128) {
+#pragma unroll
+      for (int i = 0; i < WI; ++i) transpose4(b.w[i]);
+    }
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      f32x4 part[WI], sum = zero;
+#pragma unroll
+      for (int s = 0; s < 4 / GB; ++s) sum = mfma_bf16(x[g * (4 / GB) + s], eights, sum);
+#pragma unroll
+      for (int s = 0; s < 4 / GB; ++s)
+#pragma unroll
+        for (int i = 0; i < WI; ++i) part[i] = mfma_bf16(x[g * (4 / GB) + s], decode_u8(b.w[i][g * (4 / GB) + s]), s ? part[i] : sum);
+#pragma unroll
+      for (int i = 0; i < WI; ++i) {
+        const float sc = scale.value(b.s[i][g]), m = OFF ? against_eights(offset.value(b.m[i][g])) : 0.f;
+#pragma unroll
+        for (int e = 0; e < NB; ++e) {  // of the lanes q = 0, the others' tokens are not there
+          acc[i][e] = fmaf(sc, part[i][e], acc[i][e]);
+          if (OFF) acc[i][e] = fmaf(m, sum[e], acc[i][e]);
+        }
+      }
+    }
+  };
+  if (n > 0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      load(ring[d], d);
+      __builtin_amdgcn_sched_barrier(0);  // in this order, which the waits count on
+    }
+    for (int i = 0; i < n; i += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (i + d < n) multiply(ring[d]);
+        if (i + D < n) load(ring[d], i + d + D);
+      }
+    }
+  }
+  if (nfull * 128 < a.cols && nfull % KW == wave) {
+    Block b;
+    load_weights(b, nfull);
+    const int64_t k = int64_t(nfull) * 128 + 2 * lane;
+#pragma unroll
+    for (int t = 0; t < NB; ++t) {
+      const uint16_t* row = a.X + int64_t(min(t, batch - 1)) * a.ldx;
+      b.x[t] = k < a.cols ? row[k] : 0u;
+      if (k + 1 < a.cols) b.x[t] |= uint32_t(row[k + 1]) << 16;
+    }
+    multiply(b);
+  }
+  // of tile i, wave w's sums at (w WI + i) 256 bytes
+  __syncthreads();  // the corners are done with
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+    if (q == 0) st128(uint32_t((wave * WI + i) * 256 + 16 * r), __builtin_bit_cast(uint4, acc[i]));
+  __syncthreads();
+  for (int t = wave; t < WI; t += KW) {
+    const int64_t nn = row0 + 16 * t + r;
+    if (q || nn >= a.rows) continue;
+    f32x4 total = zero;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const f32x4 v = __builtin_bit_cast(f32x4, ld128(uint32_t((w * WI + t) * 256 + 16 * r)));
+#pragma unroll
+      for (int e = 0; e < NB; ++e) total[e] += v[e];
+    }
+    if (a.bias) {
+      const float bias = a.bias[nn];
+#pragma unroll
+      for (int e = 0; e < NB; ++e) total[e] += bias;
+    }
+#pragma unroll
+    for (int e = 0; e < NB; ++e) store_y(a, e, nn, total[e]);
+  }
+}
+
+// The fewest tokens (at most 16, whose activations fit in LDS): bound by the
+// weights' read, which has to run on without a pause.  A workgroup stays on its
+// compute unit and takes the tiles of 16 weight rows blockIdx, blockIdx + grid,
+// ...  It puts the activations into LDS once.  Of every tile, wave w takes the
+// blocks of 128 columns w, w + KW, ..., with D of them in flight in registers,
+// those of the next tiles among them (and, as above, loads that are made
+// whether there is a block or not); at a tile's end the waves put their sums
+// into LDS, and one of them adds them up while the others go on.
+// An activation row starts 16 bytes further into the banks than the one before
+// it; lanes of tokens that are not there read the last one's again, into
+// results that are not written.
+// LDS: activations; the waves' sums of two tiles, of the tokens that are there.
+template <int G, bool OFF, bool S32, int KW, int D, int U>
+__global__ __launch_bounds__(64 * KW) void i4_stream_kernel(I4Args a, int n_tiles, uint32_t pitch) {
+  constexpr int GB = 128 / G;  // groups of a block
+  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  const int r = lane % 16, q = lane / 16, batch = int(a.batch);
+  const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks of a tile
+  const int grid = int(gridDim.x), tiles = (n_tiles - int(blockIdx.x) + grid - 1) / grid;
+  const uint32_t groups = uint32_t((a.cols + G - 1) / G);
+  const uint32_t parts = uint32_t(batch) * pitch;
+  const uint32_t part_bytes = uint32_t((batch + 3) / 4) * 256;  // of a wave
+  // the activations' whole chunks of 8 columns, U steps of the workgroup's threads at a time: step (row b, part c) by step
+  constexpr int T = 64 * KW;
+  const int full = int(a.cols / 8), per = (full + T - 1) / T;
+  int xb = 0, xc = 0, sb = 0, sc = 0;
+  u32x4 xv[U];
+  auto load_x = [&]() {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      xv[u] = load16_any(reinterpret_cast<const char*>(a.X + int64_t(xb) * a.ldx) + uint32_t(16 * min(xc * T + int(threadIdx.x), full - 1)));
+      const bool row = xc + 1 == per;
+      xc = row ? 0 : xc + 1;
+      xb = min(xb + (row ? 1 : 0), batch - 1);
+    }
+  };
+  auto store_x = [&]() {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = sc * T + int(threadIdx.x);
+      if (sb < batch && c < full) st128(uint32_t(sb) * pitch + uint32_t(c) * 16, __builtin_bit_cast(uint4, xv[u]));
+      const bool row = sc + 1 == per;
+      sc = row ? 0 : sc + 1;
+      sb += row ? 1 : 0;
+    }
+  };
+  if (full) load_x();
+  // rows past the last are that row again
+  const auto wbuf = buffer_over(a.W, (a.rows - 1) * a.ldw + (a.cols + 31) / 32 * 16);
+  const GroupRows<S32> scale(a.scale, a.lds, groups, a.rows, 0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, groups, a.rows, 0);
+  struct Block {
+    u32x4 w;
+    uint32_t s[GB], m[GB];
+  };
+  Block ring[D];
+  int lt = int(blockIdx.x), lb = 0, left = tiles * n;  // the next block to load: its tile and place; how many are left
+  const int last_row = int(a.rows) - 1;
+  auto load = [&](Block& b) {
+    const bool there = left > 0;
+    const uint32_t kb = there ? uint32_t(wave + KW * lb) : 0u, tile = there ? uint32_t(lt) : 0u;
+    const uint32_t row = there ? uint32_t(min(r, last_row - int(tile) * 16)) : 0u;
+    b.w = buffer_load16<false>(wbuf, row * uint32_t(a.ldw) + (there ? 16 * q : 0), tile * 16 * uint32_t(a.ldw) + kb * 64);
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      const uint32_t gi = min(kb * GB + g, groups - 1);
+      b.s[g] = scale.load(gi, row, tile * 16);
+      if (OFF) b.m[g] = offset.load(gi, row, tile * 16);
+    }
+    --left;
+    if (++lb == n) {
+      lb = 0;
+      lt += grid;
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    load(ring[d]);
+    __builtin_amdgcn_sched_barrier(0);  // in this order, which the waits count on
+  }
+  if (full) {
+    store_x();
+    while (sb < batch) {
+      load_x();
+      store_x();
+    }
+  }
+  // behind a row's last whole chunk: its last columns, then zeros
+  for (int b = wave; b < batch; b += KW) {
+    for (int c = full + lane; c < 16 * nkb; c += kWave)
+      st128(uint32_t(b) * pitch + uint32_t(c) * 16,
+            __builtin_bit_cast(uint4, 8 * int64_t(c) < a.cols ? load_x8(a.X + int64_t(b) * a.ldx, 8 * int64_t(c), a.cols) : u32x4{0u, 0u, 0u, 0u}));
+  }
+  lds_barrier();
+  const uint32_t xat = uint32_t(min(r, batch - 1)) * pitch;
+  // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
+  auto read_x = [&](int kb, int s) {
+    return __builtin_bit_cast(bf16x8, ld128(xat + uint32_t(kb) * 256 + uint32_t(G == 128 ? 4 * q + s : 4 * s + q) * 16));
+  };
+  const bf16x8 eights = minus_eights();
+  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = zero;
+  auto multiply = [&](Block& b, int kb) {
+    bf16x8 x[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) x[s] = read_x(kb, s);
+    if (G != 128) transpose4(b.w);
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      f32x4 sum = zero;
+#pragma unroll
+      for (int s = 0; s < 4 / GB; ++s) sum = mfma_bf16(x[g * (4 / GB) + s], eights, sum);
+      f32x4 part = sum;
+#pragma unroll
+      for (int s = 0; s < 4 / GB; ++s) part = mfma_bf16(x[g * (4 / GB) + s], decode_u8(b.w[g * (4 / GB) + s]), part);
+      const float sc = scale.value(b.s[g]), m = OFF ? against_eights(offset.value(b.m[g])) : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[e] = fmaf(sc, part[e], acc[e]);
+        if (OFF) acc[e] = fmaf(m, sum[e], acc[e]);
+      }
+    }
+  };
+  // the end of a tile: every wave's sums, added by one of them
+  auto finish_tile = [&](int t) {
+    const uint32_t at = parts + uint32_t(t & 1) * (KW * part_bytes);
+    if (4 * q < batch) st128(at + uint32_t(wave) * part_bytes + 16 * lane, __builtin_bit_cast(uint4, acc));
+    acc = zero;
+    lds_barrier();
+    const int64_t nn = (int64_t(blockIdx.x) + int64_t(t) * grid) * 16 + r;
+    if (wave != t % KW || 4 * q >= batch || nn >= a.rows) return;
+    f32x4 total = zero;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const f32x4 v = __builtin_bit_cast(f32x4, ld128(at + uint32_t(w) * part_bytes + 16 * lane));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) total[e] += v[e];
+    }
+    if (a.bias) {
+      const float bias = a.bias[nn];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) total[e] += bias;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) store_y(a, 4 * q + e, nn, total[e]);
+  };
+  if (n == 0) {
+    for (int t = 0; t < tiles; ++t) finish_tile(t);
+    return;
+  }
+  int t = 0, at = 0;  // the tile and the place of the block at hand
+  while (t < tiles) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (t < tiles) {
+        multiply(ring[d], wave + KW * at);
+        if (++at == n) {
+          finish_tile(t);
+          at = 0;
+          ++t;
+        }
+      }
+      load(ring[d]);
+    }
   }
 }
 
@@ -431,142 +759,6 @@ __device__ __forceinline__ void store_through_lds(const I4Args& a, int64_t n0, i
   }
 }
 
-// The fewest tokens (at most 16, whose activations fit in LDS): bound by the
-// weights' read, which has to run on without a pause.  A workgroup stays on its
-// compute unit and takes the tiles of 16 weight rows blockIdx, blockIdx + grid,
-// ...  It puts the activations into LDS once.  Of every tile, wave w takes the
-// blocks of 128 columns w, w + KW, ..., with D of them in flight in registers,
-// those of the next tiles among them; at a tile's end the waves put their sums
-// into LDS, and one of them adds them up while the others go on.
-// An activation row starts 16 bytes further into the banks than the one before
-// it; lanes of tokens that are not there read the last one's again, into
-// results that are not written.
-// LDS: activations; -8 times their sums, per group and token; the waves' sums
-// of two tiles, of the tokens that are there.
-template <int G, bool OFF, int KW, int D>
-__global__ __launch_bounds__(64 * KW) void i4_stream_kernel(I4Args a, int n_tiles, uint32_t pitch) {
-  constexpr int GB = 128 / G;  // groups of a block
-  const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
-  const int r = lane % 16, q = lane / 16, batch = int(a.batch);
-  const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks of a tile
-  const int grid = int(gridDim.x), tiles = (n_tiles - int(blockIdx.x) + grid - 1) / grid;
-  const uint32_t groups = uint32_t((a.cols + G - 1) / G);
-  const uint32_t sums = uint32_t(batch) * pitch, parts = sums + uint32_t(nkb) * (GB * 64);
-  const uint32_t part_bytes = uint32_t((batch + 3) / 4) * 256;  // of a wave
-  // past a row's last word comes the next row, past the last row nothing: zeros
-  const auto wbuf = buffer_over(a.W, (a.rows - 1) * a.ldw + (a.cols + 31) / 32 * 16);
-  const GroupRows scale(a.scale, a.lds, a.st, groups, a.rows, 0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, a.st, groups, a.rows, 0);
-  const uint32_t wvo = uint32_t(r) * uint32_t(a.ldw) + 16 * q;
-  struct Block {
-    u32x4 w;
-    uint32_t s[GB], m[GB];
-  };
-  Block ring[D];
-  int lt = int(blockIdx.x), lb = 0, left = tiles * n;  // the next block to load: its tile and place; how many are left
-  auto load = [&](Block& b) {
-    const int kb = wave + KW * lb;
-    b.w = buffer_load16<false>(wbuf, wvo, uint32_t(lt) * 16 * uint32_t(a.ldw) + uint32_t(kb) * 64);
-#pragma unroll
-    for (int g = 0; g < GB; ++g) {
-      const uint32_t gi = min(uint32_t(kb * GB + g), groups - 1);
-      b.s[g] = scale.load(gi, r, uint32_t(lt) * 16);
-      if (OFF) b.m[g] = offset.load(gi, r, uint32_t(lt) * 16);
-    }
-    --left;
-    if (++lb == n) {
-      lb = 0;
-      lt += grid;
-    }
-  };
-  // the activations: chunk c of 8 columns of row b at b pitch + 16 c, zeros past the last column
-  const int chunks = 16 * nkb;
-  u32x4 first{0u, 0u, 0u, 0u};
-  const int t0 = int(threadIdx.x);
-  if (t0 < batch * chunks) first = load_x8(a.X + int64_t(t0 / chunks) * a.ldx, 8 * int64_t(t0 % chunks), a.cols);
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (left > 0) load(ring[d]);
-  if (t0 < batch * chunks) st128(uint32_t(t0 / chunks) * pitch + uint32_t(t0 % chunks) * 16, __builtin_bit_cast(uint4, first));
-  for (int at = t0 + 64 * KW; at < batch * chunks; at += 64 * KW)
-    st128(uint32_t(at / chunks) * pitch + uint32_t(at % chunks) * 16,
-          __builtin_bit_cast(uint4, load_x8(a.X + int64_t(at / chunks) * a.ldx, 8 * int64_t(at % chunks), a.cols)));
-  lds_barrier();
-  const uint32_t xat = uint32_t(min(r, batch - 1)) * pitch;
-  // G = 128: lane (r, q) holds columns 32 q and on; else, transposed, 8 q and on of each 32
-  auto read_x = [&](int kb, int s) {
-    return __builtin_bit_cast(bf16x8, ld128(xat + uint32_t(kb) * 256 + uint32_t(G == 128 ? 4 * q + s : 4 * s + q) * 16));
-  };
-  const bf16x8 eights = minus_eights();
-  const f32x4 zero{0.f, 0.f, 0.f, 0.f};
-  for (int kb = wave; kb < nkb; kb += KW) {
-    f32x4 sum[GB];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) sum[s / (4 / GB)] = mfma_bf16(read_x(kb, s), eights, s % (4 / GB) ? sum[s / (4 / GB)] : zero);
-#pragma unroll
-    for (int g = 0; g < GB; ++g)
-      if (r == 0) st128(sums + uint32_t(kb * GB + g) * 64 + 16 * q, __builtin_bit_cast(uint4, sum[g]));
-  }
-  wave_lds_fence();
-  f32x4 acc = zero;
-  auto multiply = [&](Block& b, int kb) {
-    bf16x8 x[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) x[s] = read_x(kb, s);
-    if (G != 128) transpose4(b.w);
-#pragma unroll
-    for (int g = 0; g < GB; ++g) {
-      const f32x4 sum = __builtin_bit_cast(f32x4, ld128(sums + uint32_t(kb * GB + g) * 64 + 16 * q));
-      f32x4 part = sum;
-#pragma unroll
-      for (int s = 0; s < 4 / GB; ++s) part = mfma_bf16(x[g * (4 / GB) + s], decode_u8(b.w[g * (4 / GB) + s]), part);
-      const float sc = scale.value(b.s[g]), m = OFF ? against_eights(offset.value(b.m[g])) : 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[e] = fmaf(sc, part[e], acc[e]);
-        if (OFF) acc[e] = fmaf(m, sum[e], acc[e]);
-      }
-    }
-  };
-  // the end of a tile: every wave's sums, added by one of them
-  auto finish_tile = [&](int t) {
-    const uint32_t at = parts + uint32_t(t & 1) * (KW * part_bytes);
-    if (4 * q < batch) st128(at + uint32_t(wave) * part_bytes + 16 * lane, __builtin_bit_cast(uint4, acc));
-    acc = zero;
-    lds_barrier();
-    const int64_t nn = (int64_t(blockIdx.x) + int64_t(t) * grid) * 16 + r;
-    if (wave != t % KW || 4 * q >= batch || nn >= a.rows) return;
-    f32x4 total = zero;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      const f32x4 v = __builtin_bit_cast(f32x4, ld128(at + uint32_t(w) * part_bytes + 16 * lane));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) total[e] += v[e];
-    }
-    const float bias = a.bias ? a.bias[nn] : 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) store_y(a, 4 * q + e, nn, a.bias ? total[e] + bias : total[e]);
-  };
-  if (n == 0) {
-    for (int t = 0; t < tiles; ++t) finish_tile(t);
-    return;
-  }
-  int t = 0, at = 0;  // the tile and the place of the block at hand
-  while (t < tiles) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (t < tiles) {
-        multiply(ring[d], wave + KW * at);
-        if (left > 0) load(ring[d]);
-        if (++at == n) {
-          finish_tile(t);
-          at = 0;
-          ++t;
-        }
-      }
-    }
-  }
-}
-
 // A tile of an operand as a buffer: `rows` rows of `bytes` bytes (the end of
 // the last one rounded up to 4), ld bytes apart; rows past the last are that
 // row again.
@@ -603,7 +795,7 @@ __device__ __forceinline__ u32x4 tail_mask8(int left) {
 // time fall into different banks.  In the last block, lanes past the last
 // chunk of their row read that chunk again; what lies past `cols` is then
 // cleared in the activations.
-template <int G, bool OFF, int WGW, int WGB, int WI, int BJ, int KG>
+template <int G, bool OFF, bool S32, int WGW, int WGB, int WI, int BJ, int KG>
 __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a, int nw_tiles, int nb_tiles, int per_xcd) {
   constexpr int NW = WGW * WGB, GB = 128 / G;
   constexpr int BW = 16 * WI * WGW, BB = 16 * BJ * WGB;
@@ -664,7 +856,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     }
   };
   const int64_t groups = (a.cols + G - 1) / G;
-  const GroupRows scale(a.scale, a.lds, a.st, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, a.st, groups, a.rows, row0);
+  const GroupRows<S32> scale(a.scale, a.lds, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, groups, a.rows, row0);
   uint32_t sn[WI][GB], mn[WI][GB];  // the next block's scales and offsets
   auto scales = [&](int i) {
     const uint32_t g0 = uint32_t(i * KG + group) * GB;
@@ -995,29 +1187,40 @@ int run_direct(const I4Args& a, hipStream_t s) {
 
 // LDS of the stream kernel.
 uint32_t stream_pitch(int64_t cols) { return uint32_t((cols + 127) / 128 * 256 + 16); }
-int64_t stream_lds(const I4Args& a, int group, int kw) {
-  return a.batch * int64_t(stream_pitch(a.cols)) + (a.cols + 127) / 128 * (128 / group) * 64 + int64_t(2) * kw * (a.batch + 3) / 4 * 256;
+int64_t stream_lds(const I4Args& a, int kw) {
+  return a.batch * int64_t(stream_pitch(a.cols)) + int64_t(2) * kw * ((a.batch + 3) / 4) * 256;
 }
-bool stream_ok(const I4Args& a, int group, int kw) {
-  return a.batch <= 16 && a.cols <= 65536 && (a.rows + 16) * a.ldw < (int64_t(1) << 31) && stream_lds(a, group, kw) <= kLdsLimit;
+bool stream_ok(const I4Args& a, int kw) {
+  return a.batch <= 16 && a.cols <= 65536 && (a.rows + 16) * a.ldw < (int64_t(1) << 31) && stream_lds(a, kw) <= kLdsLimit;
 }
 
-template <int G, bool OFF, int KW, int D>
+template <int G, bool OFF, bool S32, int KW, int D>
 int run_stream(const I4Args& a, hipStream_t s) {
-  const int64_t tiles = (a.rows + 15) / 16, lds = stream_lds(a, G, KW);
+  const int64_t tiles = (a.rows + 15) / 16, lds = stream_lds(a, KW);
   const int64_t grid = std::min<int64_t>(tiles, kCus * std::max<int64_t>(1, std::min<int64_t>(16 / KW, kLdsLimit / lds)));
-  auto kern = i4_stream_kernel<G, OFF, KW, D>;
+  const bool small = a.batch * ((a.cols / 8 + 64 * KW - 1) / (64 * KW)) <= 2;  // steps of the activations' way into LDS
+  auto kern = small ? i4_stream_kernel<G, OFF, S32, KW, D, 2> : i4_stream_kernel<G, OFF, S32, KW, D, 8>;
   allow_full_lds(kern);
   hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(KW * kWave), size_t(lds), s, a, int(tiles), stream_pitch(a.cols));
   return hip_check(hipGetLastError(), "i4_stream_kernel launch");
 }
 
-template <int G, bool OFF, int WI, int BJ, int KW, int D>
+template <int G, bool OFF, bool S32, int WI, int KW, int D>
+int run_token(const I4Args& a, hipStream_t s) {
+  const int64_t nw = (a.rows + 16 * WI - 1) / (16 * WI);
+  if (int rc = check_launch(nw, 1, KW * kWave)) return rc;
+  auto kern = a.batch == 1 ? i4_token_kernel<G, OFF, S32, WI, 1, KW, D> : i4_token_kernel<G, OFF, S32, WI, 4, KW, D>;
+  const size_t lds = size_t(KW) * std::max(256 * WI, 272 * (a.batch == 1 ? 1 : 4));
+  hipLaunchKernelGGL(kern, dim3(unsigned(nw)), dim3(KW * kWave), lds, s, a, int(nw));
+  return hip_check(hipGetLastError(), "i4_token_kernel launch");
+}
+
+template <int G, bool OFF, bool S32, int WI, int BJ, int KW, int D>
 int run_slice(const I4Args& a, hipStream_t s) {
   const int64_t nw = (a.rows + 16 * WI - 1) / (16 * WI), nb = (a.batch + 16 * BJ - 1) / (16 * BJ);
   if (int rc = check_launch((nw + kXcds - 1) / kXcds * kXcds, nb, KW * kWave)) return rc;
   const int64_t grid = (nw + kXcds - 1) / kXcds * kXcds * nb;
-  auto kern = nb == 1 ? i4_slice_kernel<G, OFF, WI, BJ, KW, D, true> : i4_slice_kernel<G, OFF, WI, BJ, KW, D, false>;
+  auto kern = i4_slice_kernel<G, OFF, S32, WI, BJ, KW, D>;
   constexpr size_t kLds = size_t(KW) * WI * BJ * 1024;
   static_assert(kLds <= kLdsLimit, "LDS");
   allow_full_lds(kern);
@@ -1025,13 +1228,13 @@ int run_slice(const I4Args& a, hipStream_t s) {
   return hip_check(hipGetLastError(), "i4_slice_kernel launch");
 }
 
-template <int G, bool OFF, int WGW, int WGB, int WI, int BJ, int KG>
+template <int G, bool OFF, bool S32, int WGW, int WGB, int WI, int BJ, int KG>
 int run_stage(const I4Args& a, hipStream_t s) {
   constexpr int BW = 16 * WI * WGW, BB = 16 * BJ * WGB, kThreads = 64 * WGW * WGB * KG;
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
   if (int rc = check_launch(nw, nb, kThreads)) return rc;
   const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
-  auto kern = i4_stage_kernel<G, OFF, WGW, WGB, WI, BJ, KG>;
+  auto kern = i4_stage_kernel<G, OFF, S32, WGW, WGB, WI, BJ, KG>;
   constexpr size_t kLds = size_t(KG) * 2 * (BW * 64 + BB * 256);
   static_assert(kLds <= kLdsLimit, "LDS");
   allow_full_lds(kern);
@@ -1048,45 +1251,56 @@ bool offsets_ok(const I4Args& a, int group) {
 // 16-byte chunks of the activations.
 bool aligned_ok(const I4Args& a) { return reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 8 == 0; }
 
-constexpr int kShapes = 15;
-enum Kind { kDirect, kStream, kSlice, kStage };
+constexpr int kShapes = 19;
+enum Kind { kDirect, kToken, kStream, kSlice, kStage };
 constexpr Kind kKinds[kShapes] = {kDirect, kDirect, kStream, kStream, kStream, kSlice, kSlice, kSlice, kSlice,
-                                  kStage, kStage, kStage, kStage, kStage, kStage};
+                                  kStage, kStage, kStage, kStage, kStage, kStage, kToken, kToken, kToken, kToken};
 
 bool shape_ok(const I4Args& a, int group, int shape) {
   if (kKinds[shape] == kDirect) return true;
   if (!offsets_ok(a, group)) return false;
-  return kKinds[shape] == kStream ? stream_ok(a, group, shape == 2 ? 16 : 8) : kKinds[shape] == kStage ? aligned_ok(a) : true;
+  return kKinds[shape] == kToken ? a.batch <= 4 : kKinds[shape] == kStream ? stream_ok(a, shape == 2 ? 16 : 8) : kKinds[shape] == kStage ? aligned_ok(a) : true;
 }
 
 int pick_shape(const I4Args& a, int group) {
   if (!offsets_ok(a, group)) return 1;
-  if (shape_ok(a, group, 2)) return 2;
+  if (a.batch <= 4) return 15;
+  if (shape_ok(a, group, 4)) return 4;
   if (a.batch <= 16) return a.rows >= 8192 ? 5 : 6;
   if (a.batch <= 32) return 7;
   if (!aligned_ok(a)) return 8;
   return a.batch <= 64 ? 9 : a.batch <= 1024 ? 12 : 14;
 }
 
-template <int G, bool OFF>
+template <int G, bool OFF, bool S32>
 int run_gemm(const I4Args& a, int shape, hipStream_t s) {
   if (shape <= 0) shape = pick_shape(a, G);
   switch (shape) {
     case 1: return run_direct<G, OFF>(a, s);
-    case 2: return run_stream<G, OFF, 16, 4>(a, s);
-    case 3: return run_stream<G, OFF, 8, 8>(a, s);
-    case 4: return run_stream<G, OFF, 8, 4>(a, s);
-    case 5: return run_slice<G, OFF, G == 32 ? 2 : 4, 1, 8, 2>(a, s);
-    case 6: return run_slice<G, OFF, 1, 1, 16, 2>(a, s);
-    case 7: return run_slice<G, OFF, 2, 2, 8, 1>(a, s);
-    case 8: return run_slice<G, OFF, G == 32 ? 1 : 2, 4, 8, 1>(a, s);
-    case 9: return run_stage<G, OFF, 2, 2, 2, 2, 1>(a, s);    // 64 x 64
-    case 10: return run_stage<G, OFF, 4, 1, 2, 4, 2>(a, s);   // 128 x 64, 2 groups
-    case 11: return run_stage<G, OFF, 2, 2, 4, 4, 2>(a, s);   // 128 x 128, 2 groups
-    case 12: return run_stage<G, OFF, 2, 2, 4, 4, 1>(a, s);   // 128 x 128
-    case 13: return run_stage<G, OFF, 4, 2, 4, 6, 1>(a, s);   // 256 x 192
-    default: return run_stage<G, OFF, 4, 2, 3, 8, 1>(a, s);   // 192 x 256
+    case 2: return run_stream<G, OFF, S32, 16, 2>(a, s);
+    case 3: return run_stream<G, OFF, S32, 8, 8>(a, s);
+    case 4: return run_stream<G, OFF, S32, 8, 4>(a, s);
+    case 5: return run_slice<G, OFF, S32, G == 32 ? 2 : 4, 1, 8, 2>(a, s);
+    case 6: return run_slice<G, OFF, S32, 1, 1, 16, 2>(a, s);
+    case 7: return run_slice<G, OFF, S32, 2, 2, 8, 1>(a, s);
+    case 8: return run_slice<G, OFF, S32, G == 32 ? 1 : 2, 4, 8, 1>(a, s);
+    case 9: return run_stage<G, OFF, S32, 2, 2, 2, 2, 1>(a, s);    // 64 x 64
+    case 10: return run_stage<G, OFF, S32, 4, 1, 2, 4, 2>(a, s);   // 128 x 64, 2 groups
+    case 11: return run_stage<G, OFF, S32, 2, 2, 4, 4, 2>(a, s);   // 128 x 128, 2 groups
+    case 12: return run_stage<G, OFF, S32, 2, 2, 4, 4, 1>(a, s);   // 128 x 128
+    case 13: return run_stage<G, OFF, S32, 4, 2, 4, 6, 1>(a, s);   // 256 x 192
+    case 15: return run_token<G, OFF, S32, 1, 16, 2>(a, s);
+    case 16: return run_token<G, OFF, S32, 1, 8, 4>(a, s);
+    case 17: return run_token<G, OFF, S32, 2, 16, 2>(a, s);
+    case 18: return run_token<G, OFF, S32, 2, 8, 2>(a, s);
+    default: return run_stage<G, OFF, S32, 4, 2, 3, 8, 1>(a, s);   // 192 x 256
   }
+}
+
+template <int G>
+int run_form(const I4Args& a, int shape, hipStream_t s) {
+  if (a.st == UW_F32) return a.offset ? run_gemm<G, true, true>(a, shape, s) : run_gemm<G, false, true>(a, shape, s);
+  return a.offset ? run_gemm<G, true, false>(a, shape, s) : run_gemm<G, false, false>(a, shape, s);
 }
 
 template <bool F32, int G, bool OFF>
@@ -1147,9 +1361,7 @@ int launch_i4_gemm(const uint8_t* W, int64_t rows, int64_t cols, int64_t ldw, in
   const I4Args a{W, static_cast<const char*>(scale), static_cast<const char*>(offset), X, bias, static_cast<char*>(Y), rows, cols,
                  rows > 1 ? ldw : 0, one ? 0 : lds, one || !offset ? 0 : ldo, batch, batch > 1 ? ldx : 0, ldy, st, yt};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (group == 32) return offset ? run_gemm<32, true>(a, shape, s) : run_gemm<32, false>(a, shape, s);
-  if (group == 64) return offset ? run_gemm<64, true>(a, shape, s) : run_gemm<64, false>(a, shape, s);
-  return offset ? run_gemm<128, true>(a, shape, s) : run_gemm<128, false>(a, shape, s);
+  return group == 32 ? run_form<32>(a, shape, s) : group == 64 ? run_form<64>(a, shape, s) : run_form<128>(a, shape, s);
 }
 
 int launch_i4_quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, int xt, int group, uint8_t* Q, int64_t ldq,

@@ -110,7 +110,7 @@ def run_gemm(b, rows, cols, group, affine, st, out, bias=False, shape=0, whole=F
         except uw.UwError as e:
             assert e.status == uw.UW_ERR_UNSUPPORTED
             if not (X.data_ptr() % 16 or (b > 1 and X.stride(0) % 8)):
-                assert b > 16 or b * cols > 60000  # a shape for few tokens and short rows
+                assert b > 4  # a shape for few tokens
                 return
             # a shape for rows on 16-byte boundaries
             return run_gemm(b, rows, cols, group, affine, st, out, bias, shape, whole, pad + -(cols + pad) % 8, 8 * (shift > 0), seed)
@@ -139,7 +139,7 @@ def takes(w, X, Y, shape):
     try:
         w.run(X, Y, shape)
     except uw.UwError as e:
-        assert e.status == uw.UW_ERR_UNSUPPORTED and X.shape[0] > 16
+        assert e.status == uw.UW_ERR_UNSUPPORTED and X.shape[0] > 4
         return False
     return True
 
@@ -201,17 +201,17 @@ def test_gemm_drawn_sizes():
 
 def test_gemm_infinities_stay_in_their_token():
     for shape in SHAPES:  # 520 columns: rows on 16-byte boundaries
-        for affine, b in itertools.product((False, True), (16, 40)):
+        for affine, b in itertools.product((False, True), (4, 16, 40)):
             w = Weights(48, 520, 64, affine, "bf16", 3)
             X = tokens(b, 520, 4)
             Y = torch.empty(b, 48, device=DEV)
             if not takes(w, X, Y, shape):
                 continue
             clean = Y.clone()
-            X[7, 13], X[11, 519], X[b - 1, 200] = float("nan"), float("inf"), float("-inf")
+            X[1, 13], X[2, 519], X[b - 1, 200] = float("nan"), float("inf"), float("-inf")
             w.run(X, Y, shape)
             bad = torch.zeros(b, dtype=torch.bool, device=DEV)
-            bad[[7, 11, b - 1]] = True
+            bad[[1, 2, b - 1]] = True
             assert torch.equal(Y[~bad], clean[~bad]) and not torch.isfinite(Y[bad]).any(), f"shape {shape} affine {affine}"
 
 
@@ -228,7 +228,7 @@ def test_gemm_nan_scales_show_in_their_row_alone():
 
 def test_gemm_repeats_to_the_bit_and_rows_do_not_see_each_other():
     w = Weights(333, 1304, 32, True, "f32", 8)
-    for shape, b in itertools.product(SHAPES, (11, 37)):
+    for shape, b in itertools.product(SHAPES, (3, 11, 37)):
         X = tokens(b, 1304, 9)
         Y, Z = torch.empty(b, 333, device=DEV), torch.empty(b, 333, device=DEV)
         if not takes(w, X, Y, shape):
