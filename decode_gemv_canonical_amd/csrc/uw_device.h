@@ -145,6 +145,29 @@ __device__ __forceinline__ void stage_load(__amdgpu_buffer_rsrc_t r, uint32_t vo
   }
 }
 
+// The same with 4 bytes per lane, at m0 + 4 * lane.
+__device__ __forceinline__ void stage_load4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t m0) {
+  asm volatile(
+      "s_nop 4\n"
+      "s_mov_b32 m0, %[m]\n"
+      "s_nop 0\n"
+      "buffer_load_dword %[v], %[r], %[s] offen lds"
+      :
+      : [m] "s"(__builtin_amdgcn_readfirstlane(m0)), [v] "v"(voff), [r] "s"(r), [s] "s"(__builtin_amdgcn_readfirstlane(soff))
+      : "memory");
+}
+
+// s_waitcnt vmcnt for a ring: at most `young` groups of L loads may stay
+// outstanding, young <= MAX.
+template <int L, int MAX>
+__device__ __forceinline__ void wait_ring(int young) {
+  if (young >= MAX) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MAX * L) : "memory");
+  } else if constexpr (MAX > 0) {
+    wait_ring<L, MAX - 1>(young);
+  }
+}
+
 // Words read by the whole wave go through the constant address space so they
 // become scalar loads.
 typedef __attribute__((address_space(4))) const uint32_t const_word;

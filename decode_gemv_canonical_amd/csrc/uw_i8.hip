@@ -295,17 +295,6 @@ __device__ __forceinline__ u32x4 tail_mask(int left) {
   return m;
 }
 
-// s_waitcnt vmcnt for a ring: at most `young` groups of L loads may stay
-// outstanding, young <= MAX.
-template <int L, int MAX>
-__device__ __forceinline__ void wait_ring(int young) {
-  if (young >= MAX) {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MAX * L) : "memory");
-  } else if constexpr (MAX > 0) {
-    wait_ring<L, MAX - 1>(young);
-  }
-}
-
 // Small batches: a workgroup holds BW weight rows and BB activation rows, and
 // its KW waves split k: wave w takes the 128-byte blocks w, w + KW, ... for the
 // whole tile.  A wave stages its blocks into its own ring of ST slots in LDS
