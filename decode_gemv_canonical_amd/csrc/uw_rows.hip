@@ -184,6 +184,20 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
   }
 }
 
+// The sum alone.
+template <int NT, int SLOT = 0>
+__device__ __forceinline__ float row_sum(float sum) {
+  sum = wave_sum(sum);
+  if (NT == kWave) return sum;
+  __shared__ float s_sum[16];
+  if (threadIdx.x % kWave == 0) s_sum[int(threadIdx.x) / kWave] = sum;
+  lds_barrier();
+  sum = s_sum[0];
+#pragma unroll
+  for (int i = 1; i < NT / kWave; ++i) sum += s_sum[i];
+  return sum;
+}
+
 // 112 bytes: with 120 every launch took 0.4 us longer.
 struct RowArgs {
   const char* x;
@@ -517,26 +531,32 @@ struct BlockArgs {  // 112 bytes, as RowArgs
 static_assert(sizeof(BlockArgs) == 112, "kernel arguments");
 enum BlockFlags { kPostNorm = 1, kYF32 = 2, kStreamPastCaches = 4 };
 
-__device__ __forceinline__ void load_as(const char* row, int type, int64_t i, int64_t n, float (&f)[8]) {
-  if (type == UW_F32) unpack8<kF32>(load8<kF32>(row, i, n), f);
-  else unpack8<kBf16>(load8<kBf16>(row, i, n), f);
+// Values of a gain or gate as they lie in memory; a null row reads as zeros.
+__device__ __forceinline__ Raw8 load_raw(const char* row, int type, int64_t i, int64_t n) {
+  if (type == UW_F32) return load8<kF32>(row, i, row ? n : 0);
+  return load8<kBf16>(row, i, row ? n : 0);
+}
+__device__ __forceinline__ void unpack_as(const Raw8& v, int type, float (&f)[8]) {
+  if (type == UW_F32) unpack8<kF32>(v, f);
+  else unpack8<kBf16>(v, f);
 }
 
-// h of one chunk from x (in p) and r; p receives h as it is kept.
+// h of one chunk from x (in p), r, and the chunk's gain and gate; p receives h
+// as it is kept.
 template <int RT>
-__device__ __forceinline__ void join8(const BlockArgs& a, float rstd, const char* gate, int64_t i, const Raw8& rr, float (&p)[8]) {
+__device__ __forceinline__ void join8(const BlockArgs& a, float rstd, const Raw8& rr, const Raw8& post, const Raw8& gate, float (&p)[8]) {
   float v[8];
   if (a.flags & kPostNorm) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] *= rstd;
     if (a.post) {
-      load_as(a.post, a.pt, i, a.cols, v);
+      unpack_as(post, a.pt, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) p[e] *= v[e];
     }
   }
-  if (gate) {
-    load_as(gate, a.gt, i, a.cols, v);
+  if (a.gate) {
+    unpack_as(gate, a.gt, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] *= a.branch * v[e];
   } else {
@@ -556,6 +576,9 @@ template <int XT, int RT, bool I8, int NT, int VPT>
 __global__ __launch_bounds__(NT == kWave ? 256 : NT) void block_kernel(BlockArgs a) {
   constexpr int kRowsPer = NT == kWave ? 4 : 1;
   constexpr int kXs = XT == kF32 ? 4 : 2, kRs = RT == kF32 ? 4 : 2;
+  // one chunk a thread: gains and gates are loaded with x and r, before the first sum.  With more chunks the registers
+  // that they take cost more waves than the latency behind the sum (2048 x 8192, bf16: 30.5 us late, 33.5 early)
+  constexpr bool kEarly = VPT == 1;
   const int t = int(threadIdx.x) % NT;
   const int64_t row = int64_t(blockIdx.x) * kRowsPer + (NT == kWave ? int(threadIdx.x) / kWave : 0);
   if (row >= a.rows) return;  // whole waves, and no barrier follows where a workgroup holds several rows
@@ -563,12 +586,17 @@ __global__ __launch_bounds__(NT == kWave ? 256 : NT) void block_kernel(BlockArgs
   const char* r = a.r + row * a.ldr * kRs;
   const char* gate = a.gate ? a.gate + row * a.ldg * (a.gt == UW_F32 ? 4 : 2) : nullptr;
   char* h = a.h ? a.h + row * a.ldh * kRs : nullptr;
-  Raw8 xr[VPT], rr[VPT];
+  Raw8 xr[VPT], rr[VPT], pr[kEarly ? VPT : 1], tr[kEarly ? VPT : 1], gr[kEarly ? VPT : 1];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int64_t i = 8 * (t + int64_t(j) * NT);
     xr[j] = load8<XT>(x, i, a.cols);
     rr[j] = load8<RT>(r, i, a.cols);
+    if (kEarly) {
+      tr[j] = load_raw(gate, a.gt, i, a.cols);
+      pr[j] = load_raw(a.post, a.pt, i, a.cols);
+      gr[j] = load_raw(a.gain, a.nt, i, a.cols);
+    }
   }
   float p[VPT][8];
   float sum = 0.f, rstd = 1.f;
@@ -582,15 +610,13 @@ __global__ __launch_bounds__(NT == kWave ? 256 : NT) void block_kernel(BlockArgs
     sum += part;
   }
   const float n = float(a.cols);
-  if (a.flags & kPostNorm) {
-    row_reduce<NT, 0>(sum, top);
-    rstd = 1.f / sqrtf(fmaf(sum, 1.f / n, a.post_eps));
-  }
+  if (a.flags & kPostNorm) rstd = 1.f / sqrtf(fmaf(row_sum<NT>(sum), 1.f / n, a.post_eps));
   sum = 0.f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int64_t i = 8 * (t + int64_t(j) * NT);
-    join8<RT>(a, rstd, gate, i, rr[j], p[j]);
+    if (kEarly) join8<RT>(a, rstd, rr[j], pr[j], tr[j], p[j]);
+    else join8<RT>(a, rstd, rr[j], load_raw(a.post, a.pt, i, a.cols), load_raw(gate, a.gt, i, a.cols), p[j]);
     if (h) store8(h, RT, i, a.cols, p[j], a.flags & kStreamPastCaches);
   }
   if (!a.y) return;
@@ -607,7 +633,8 @@ __global__ __launch_bounds__(NT == kWave ? 256 : NT) void block_kernel(BlockArgs
     sum += part;
     if (a.gain) {
       float g[8];
-      load_as(a.gain, a.nt, i, a.cols, g);
+      if (kEarly) unpack_as(gr[j], a.nt, g);
+      else unpack_as(load_raw(a.gain, a.nt, i, a.cols), a.nt, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) p[j][e] *= g[e];
     }
@@ -616,7 +643,8 @@ __global__ __launch_bounds__(NT == kWave ? 256 : NT) void block_kernel(BlockArgs
       for (int e = 0; e < 8; ++e) top = max(top, f32_bits(p[j][e]) & 0x7FFFFFFFu);
     }
   }
-  row_reduce<NT, 1>(sum, top);
+  if (I8) row_reduce<NT, 1>(sum, top);
+  else sum = row_sum<NT, 1>(sum);
   rstd = 1.f / sqrtf(fmaf(sum, 1.f / n, a.eps));
   if (I8) {
     float s, inv;
@@ -662,9 +690,7 @@ __global__ __launch_bounds__(1024) void long_block_kernel(BlockArgs a) {
       for (int e = 0; e < 8; ++e) part = fmaf(p[e], p[e], part);
       squares += double(part);
     }
-    sum = float(squares);
-    row_reduce<NT, 0>(sum, top);
-    rstd = 1.f / sqrtf(fmaf(sum, 1.f / n, a.post_eps));
+    rstd = 1.f / sqrtf(fmaf(row_sum<NT>(float(squares)), 1.f / n, a.post_eps));
   }
   // h of a chunk, times the gain; its squares
   auto chunk = [&](int64_t i, bool kept, float& part) {
@@ -672,7 +698,7 @@ __global__ __launch_bounds__(1024) void long_block_kernel(BlockArgs a) {
       unpack8<RT>(load8<RT>(h, i, cols), p);
     } else {
       unpack8<XT>(load8<XT>(x, i, cols), p);
-      join8<RT>(a, rstd, gate, i, load8<RT>(r, i, cols), p);
+      join8<RT>(a, rstd, load8<RT>(r, i, cols), load_raw(a.post, a.pt, i, cols), load_raw(gate, a.gt, i, cols), p);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -683,7 +709,7 @@ __global__ __launch_bounds__(1024) void long_block_kernel(BlockArgs a) {
   auto times_gain = [&](int64_t i) {
     if (!a.gain) return;
     float g[8];
-    load_as(a.gain, a.nt, i, cols, g);
+    unpack_as(load_raw(a.gain, a.nt, i, cols), a.nt, g);
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] *= g[e];
   };
@@ -745,11 +771,11 @@ int run_block(const BlockRows& b, hipStream_t s) {
     }
     return int(UW_OK);
   };
-  // the norm's threads and chunks (run_rows)
+  // the norm's threads and chunks (run_rows), but one chunk a thread up to 4096 columns whatever the rows: two chunks
+  // take 2048 x 4096 in 15.9 us, one in 15.2
   if (chunks <= 64) return go(block_kernel<XT, RT, I8, 64, 1>, 256, 4);
   if (chunks <= 128) return go(block_kernel<XT, RT, I8, 64, 2>, 256, 4);
   if (chunks <= 256) return go(block_kernel<XT, RT, I8, 256, 1>, 256, 1);
-  if (chunks <= 512 && b.rows > 1024) return go(block_kernel<XT, RT, I8, 256, 2>, 256, 1);
   if (chunks <= 512) return go(block_kernel<XT, RT, I8, 512, 1>, 512, 1);
   if (chunks <= 1024) return go(block_kernel<XT, RT, I8, 1024, 1>, 1024, 1);
   if (chunks <= 2048) return go(block_kernel<XT, RT, I8, 1024, 2>, 1024, 1);
