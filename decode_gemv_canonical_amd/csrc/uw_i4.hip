@@ -28,30 +28,41 @@ __device__ __forceinline__ u32x4 load16_any(const void* p) {
 
 // -- rows in 4 bits and back ----------------------------------------------------
 
-// Values [i, i + 8) of a row of n as fp32; those past the end read as `pad`.
+// Eight values as they lie in memory.
+struct Raw8 {
+  u32x4 a, b;  // b: of fp32
+};
+// The first `left` (1 .. 7) of them, the others zero.
 template <bool F32>
-__device__ __forceinline__ void load_f8(const char* row, int64_t i, int64_t n, float pad, float (&f)[8]) {
-  if (i + 8 <= n) {
+__device__ __forceinline__ Raw8 load_part(const char* p, int left) {
+  Raw8 v{u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
+#pragma unroll
+  for (int e = 0; e < 7; ++e) {
+    if (e >= left) continue;
     if (F32) {
-      const u32x4 a = load16_any(row + 4 * i), b = load16_any(row + 4 * i + 16);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = bits_f32(e < 4 ? a[e] : b[e - 4]);
+      const uint32_t w = reinterpret_cast<const uint32_t*>(p)[e];
+      if (e < 4) v.a[e] = w;
+      else v.b[e - 4] = w;
     } else {
-      const u32x4 a = load16_any(row + 2 * i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = bits_f32((e & 1) ? (a[e / 2] & 0xFFFF0000u) : (a[e / 2] << 16));
+      v.a[e / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[e]) << (16 * (e & 1));
     }
-    return;
   }
+  return v;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw8& v, float (&f)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    f[e] = pad;
-    if (i + e < n) {
-      if (F32) f[e] = reinterpret_cast<const float*>(row)[i + e];
-      else f[e] = bits_f32(uint32_t(reinterpret_cast<const uint16_t*>(row)[i + e]) << 16);
-    }
+    if (F32) f[e] = bits_f32(e < 4 ? v.a[e] : v.b[e - 4]);
+    else f[e] = bits_f32((e & 1) ? (v.a[e / 2] & 0xFFFF0000u) : (v.a[e / 2] << 16));
   }
 }
+
+// A workgroup of 256 threads takes kTileRows rows by kTileCols columns, a wave
+// a row at a time, so that the scales of a group go out (and come in) for 32
+// rows side by side: one at a time they cost as much as the matrix (groups of
+// 32: 55 us for 14336 x 4096).
+constexpr int kTileCols = 512;
 
 struct Q4Args {
   const char* X;
@@ -60,8 +71,18 @@ struct Q4Args {
   char* offset;
   int64_t rows, cols, ldx, ldq, lds, ldo;
   int32_t st;
-  uint32_t per_row;  // workgroups of a row
+  uint32_t across;  // tiles of a row
 };
+
+// Over the 4, 8 or 16 lanes of a group: DPP within rows of 16 lanes.
+template <int N, class F>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, F f) {
+  v = f(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false)));   // quad_perm 1,0,3,2
+  v = f(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, false)));   // quad_perm 2,3,0,1
+  if (N > 4) v = f(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, false)));  // row_half_mirror
+  if (N > 8) v = f(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x140, 0xF, 0xF, false)));  // row_mirror
+  return v;
+}
 
 __device__ __forceinline__ void store_scale(char* p, int64_t i, int st, float v) {
   if (st == UW_F32) reinterpret_cast<float*>(p)[i] = v;
@@ -72,80 +93,118 @@ __device__ __forceinline__ float as_kept(float v, int st) {
   return st == UW_F32 ? v : static_cast<float>(static_cast<__bf16>(v));
 }
 
-// The integer nearest to the fp32 quotient t / s (ties to even), held to -8 ..
-// 7, plus 8.  inv is 1 / s rounded: the quotient is corrected by its residual,
-// which gives the rounded quotient, and where t itself is infinite (p - m past
-// the fp32 range) stays as it is.  Adding 1.5 * 2^23 + 8 rounds to the nearest
-// integer and leaves it in the low bits.
+// The bits of 1.5 * 2^23 + 8 plus the integer nearest to the fp32 quotient t / s
+// (ties to even), held to -8 .. 7: the sum rounds, and leaves the integer in the
+// low bits.  inv is 1 / s rounded.  The product with it is corrected by its
+// residual, which gives the rounded quotient; held to +-16 before, an infinite t
+// (p - m past the fp32 range) comes out infinite rather than NaN.
+constexpr uint32_t kNibbleBase = 0x4B400000u;
 __device__ __forceinline__ uint32_t nibble(float t, float s, float inv) {
 #pragma clang fp contract(off)
-  const float q0 = t * inv, q1 = fmaf(fmaf(-q0, s, t), inv, q0);
-  const float q = fminf(fmaxf(fabsf(q0) < 64.f ? q1 : q0, -8.f), 7.f);
-  return f32_bits(q + 12582920.f) & 15u;
+  const float q0 = __builtin_amdgcn_fmed3f(t * inv, -16.f, 16.f), q1 = fmaf(fmaf(-q0, s, t), inv, q0);
+  return f32_bits(__builtin_amdgcn_fmed3f(q1, -8.f, 7.f) + 12582920.f);
 }
 
-// One thread holds 8 columns, G / 8 neighbouring lanes a group.
-template <bool F32, int G, bool OFF>
+// A lane holds 8 columns, G / 8 neighbouring lanes a group, a wave STEPS rows.
+template <bool F32, int G, bool OFF, int STEPS>
 __global__ __launch_bounds__(256) void quantize4_kernel(Q4Args a) {
-  const int64_t row = blockIdx.x / a.per_row;
-  const int64_t i = 8 * (int64_t(blockIdx.x % a.per_row) * 256 + threadIdx.x);
-  const char* x = a.X + row * a.ldx * (F32 ? 4 : 2);
-  float f[8];
-  load_f8<F32>(x, i, a.cols, 0.f, f);
-  uint32_t top = 0u;
-  float most = -INFINITY, least = INFINITY;
+  constexpr int kGroups = kTileCols / G, kRows = 4 * STEPS;
+  __shared__ float s_scale[kGroups][kRows + 1], s_offset[OFF ? kGroups : 1][kRows + 1];
+  const int64_t row0 = int64_t(blockIdx.x / a.across) * kRows, col0 = int64_t(blockIdx.x % a.across) * kTileCols;
+  const int lane = int(threadIdx.x) % kWave, wave = int(threadIdx.x) / kWave;
+  const int64_t i = col0 + 8 * lane;
+  const int left = int(std::min<int64_t>(a.cols - i, 8));  // of the lane's columns
+  // rows past the last read it again
+  const char* x[STEPS];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    top = max(top, f32_bits(f[e]) & 0x7FFFFFFFu);
-    if (OFF && i + e < a.cols) {
-      most = fmaxf(most, f[e]);
-      least = fminf(least, f[e]);
+  for (int u = 0; u < STEPS; ++u)
+    x[u] = a.X + (std::min<int64_t>(row0 + 4 * u + wave, a.rows - 1) * a.ldx + i) * (F32 ? 4 : 2);
+  Raw8 raw[STEPS] = {};
+  if (left == 8) {
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      raw[u].a = load16_any(x[u]);
+      if (F32) raw[u].b = load16_any(x[u] + 16);
     }
+  } else if (left > 0) {
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) raw[u] = load_part<F32>(x[u], left);
   }
 #pragma unroll
-  for (int d = 1; d < G / 8; d *= 2) {
-    top = max(top, uint32_t(__shfl_xor(int(top), d, kWave)));
-    if (OFF) {
-      most = fmaxf(most, __shfl_xor(most, d, kWave));
-      least = fminf(least, __shfl_xor(least, d, kWave));
-    }
-  }
-  if (i >= a.cols) return;
-  const bool fine = top < 0x7F800000u;
-  float s, m = 0.f;
-  {
-#pragma clang fp contract(off)
-    if (OFF) {
-      s = as_kept(fmaxf(most / 15.f - least / 15.f, kTiny), a.st);
-      m = as_kept((least * 0.5f + most * 0.5f) + s * 0.5f, a.st);
+  for (int u = 0; u < STEPS; ++u) {
+    const int64_t row = row0 + 4 * u + wave;
+    float f[8];
+    unpack8<F32>(raw[u], f);
+    uint32_t top;
+    if (F32) {
+      const u32x4 v = raw[u].a & 0x7FFFFFFFu, w = raw[u].b & 0x7FFFFFFFu;
+      top = max(max(max(v[0], v[1]), max(v[2], v[3])), max(max(w[0], w[1]), max(w[2], w[3])));
     } else {
-      s = as_kept(fmaxf(bits_f32(top) / 7.f, kTiny), a.st);
+      using u16x8 = uint16_t __attribute__((ext_vector_type(8)));
+      const u32x4 v = raw[u].a & 0x7FFF7FFFu;
+      const u16x8 h = __builtin_bit_cast(u16x8, v);
+      const auto m = __builtin_elementwise_max(__builtin_elementwise_max(h.s01, h.s23), __builtin_elementwise_max(h.s45, h.s67));
+      top = max(uint32_t(m[0]), uint32_t(m[1])) << 16;
+    }
+    top = group_reduce<G / 8>(top, [](uint32_t p, uint32_t q) { return max(p, q); });
+    float most = -INFINITY, least = INFINITY;
+    if (OFF) {
+      if (left < 8) {
+#pragma unroll
+        for (int e = 1; e < 8; ++e) f[e] = e < left ? f[e] : f[0];
+      }
+      if (left > 0) {
+        most = least = f[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) {
+          most = fmaxf(most, f[e]);
+          least = fminf(least, f[e]);
+        }
+      }
+      most = bits_f32(group_reduce<G / 8>(f32_bits(most), [](uint32_t p, uint32_t q) { return f32_bits(fmaxf(bits_f32(p), bits_f32(q))); }));
+      least = bits_f32(group_reduce<G / 8>(f32_bits(least), [](uint32_t p, uint32_t q) { return f32_bits(fminf(bits_f32(p), bits_f32(q))); }));
+    }
+    if (left <= 0 || row >= a.rows) continue;
+    const bool fine = top < 0x7F800000u;
+    float s, m = 0.f;
+    {
+#pragma clang fp contract(off)
+      if (OFF) {
+        s = as_kept(fmaxf(most / 15.f - least / 15.f, kTiny), a.st);
+        m = as_kept((least * 0.5f + most * 0.5f) + s * 0.5f, a.st);
+      } else {
+        s = as_kept(fmaxf(bits_f32(top) / 7.f, kTiny), a.st);
+      }
+    }
+    // where s nears the denormal range the residual would leave it: both are scaled up (t is at most 8 s)
+    const float up = s < 0x1p-60f ? 0x1p64f : 1.f;
+    const float su = s * up, inv = 1.f / su;
+    uint32_t w = 0u - kNibbleBase * 0x11111111u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w += nibble((OFF ? f[e] - m : f[e]) * up, su, inv) << (4 * e);
+    if (!fine) w = 0x88888888u;
+    uint8_t* q = a.Q + row * a.ldq + i / 2;
+    if (left == 8) {
+      *reinterpret_cast<uint32_t*>(q) = w;
+    } else {
+      if (left & 1) w = (w & ~(15u << (4 * left))) | 8u << (4 * left);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (2 * e < left) q[e] = uint8_t(w >> (8 * e));
+    }
+    if (lane % (G / 8) == 0) {
+      const float nan = bits_f32(0x7FC00000u);
+      s_scale[lane / (G / 8)][4 * u + wave] = fine ? s : nan;
+      if (OFF) s_offset[lane / (G / 8)][4 * u + wave] = fine ? m : nan;
     }
   }
-  // where s nears the denormal range the residual would leave it: both are scaled up (t is at most 8 s)
-  const float up = s < 0x1p-60f ? 0x1p64f : 1.f;
-  const float su = s * up, inv = 1.f / su;
-  uint32_t w = 0u;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float t = (OFF ? f[e] - m : f[e]) * up;
-    w |= (fine ? nibble(t, su, inv) : 8u) << (4 * e);
-  }
-  uint8_t* q = a.Q + row * a.ldq + i / 2;
-  if (i + 8 <= a.cols) {
-    *reinterpret_cast<uint32_t*>(q) = w;
-  } else {
-    const int left = int(a.cols - i);
-    if (left & 1) w = (w & ~(15u << (4 * left))) | 8u << (4 * left);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (2 * e < left) q[e] = uint8_t(w >> (8 * e));
-  }
-  if (i % G == 0) {
-    const int64_t g = i / G;
-    const float nan = bits_f32(0x7FC00000u);
-    store_scale(a.scale, g * a.lds + row, a.st, fine ? s : nan);
-    if (OFF) store_scale(a.offset, g * a.ldo + row, a.st, fine ? m : nan);
+  __syncthreads();
+  for (int at = int(threadIdx.x); at < kGroups * kRows; at += 256) {
+    const int g = at / kRows, r = at % kRows;
+    if (col0 + int64_t(g) * G >= a.cols || row0 + r >= a.rows) continue;
+    const int64_t to = col0 / G + g;
+    store_scale(a.scale, to * a.lds + row0 + r, a.st, s_scale[g][r]);
+    if (OFF) store_scale(a.offset, to * a.ldo + row0 + r, a.st, s_offset[g][r]);
   }
 }
 
@@ -155,70 +214,104 @@ struct D4Args {
   const char* offset;
   char* Y;
   int64_t rows, cols, ldq, lds, ldo, ldy;
-  int32_t st, yt, log_group;
-  uint32_t per_row;
+  int32_t st, log_group;
+  uint32_t across;
 };
 
-// One thread, 8 columns: s q rounded to fp32, the offset added in a rounding
-// of its own, then rounded to Y's type.
+// The same tile; s q rounded to fp32, the offset added in a rounding of its
+// own, then rounded to Y's type.
+template <bool OFF, bool YF32, int STEPS>
 __global__ __launch_bounds__(256) void dequantize4_kernel(D4Args a) {
 #pragma clang fp contract(off)
-  const int64_t row = blockIdx.x / a.per_row;
-  const int64_t i = 8 * (int64_t(blockIdx.x % a.per_row) * 256 + threadIdx.x);
-  if (i >= a.cols) return;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(a.Q + row * a.ldq + i / 2) ^ 0x88888888u;
-  const int64_t g = i >> a.log_group;
-  const float s = load_scale(a.scale, g * a.lds + row, a.st);
-  const float m = a.offset ? load_scale(a.offset, g * a.ldo + row, a.st) : 0.f;
-  float f[8];
+  constexpr int kRows = 4 * STEPS;
+  __shared__ float s_scale[kTileCols / 32][kRows + 1], s_offset[OFF ? kTileCols / 32 : 1][kRows + 1];
+  const int64_t row0 = int64_t(blockIdx.x / a.across) * kRows, col0 = int64_t(blockIdx.x % a.across) * kTileCols;
+  const int lane = int(threadIdx.x) % kWave, wave = int(threadIdx.x) / kWave;
+  const int64_t i = col0 + 8 * lane;
+  uint32_t words[STEPS];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    f[e] = float(int32_t(w << (28 - 4 * e)) >> 28) * s;
-    if (a.offset) f[e] = f[e] + m;
+  for (int u = 0; u < STEPS; ++u) {
+    const int64_t row = std::min<int64_t>(row0 + 4 * u + wave, a.rows - 1);
+    words[u] = *reinterpret_cast<const uint32_t*>(a.Q + row * a.ldq + std::min<int64_t>(i, a.cols - 1) / 8 * 4);
   }
-  if (a.yt == UW_F32) {
-    float* y = reinterpret_cast<float*>(a.Y) + row * a.ldy + i;
+  const int64_t groups = ((a.cols - 1) >> a.log_group) + 1, first = col0 >> a.log_group;
+  for (int at = int(threadIdx.x); at < (kTileCols >> a.log_group) * kRows; at += 256) {
+    const int g = at / kRows, r = at % kRows;
+    const int64_t from = std::min(first + g, groups - 1), row = std::min<int64_t>(row0 + r, a.rows - 1);
+    s_scale[g][r] = load_scale(a.scale, from * a.lds + row, a.st);
+    if (OFF) s_offset[g][r] = load_scale(a.offset, from * a.ldo + row, a.st);
+  }
+  __syncthreads();
+  if (i >= a.cols) return;
+  const int g = (8 * lane) >> a.log_group;
+#pragma unroll
+  for (int u = 0; u < STEPS; ++u) {
+    const int r = 4 * u + wave;
+    if (row0 + r >= a.rows) break;
+    const uint32_t w = words[u] ^ 0x88888888u;
+    const float s = s_scale[g][r], m = OFF ? s_offset[g][r] : 0.f;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = float(int32_t(w << (28 - 4 * e)) >> 28) * s;
+      if (OFF) f[e] = f[e] + m;
+    }
+    if (YF32) {
+      float* y = reinterpret_cast<float*>(a.Y) + (row0 + r) * a.ldy + i;
+      if (i + 8 <= a.cols) {
+        __builtin_memcpy(y, f, 32);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+          if (i + e < a.cols) y[e] = f[e];
+      }
+      continue;
+    }
+    uint16_t* y = reinterpret_cast<uint16_t*>(a.Y) + (row0 + r) * a.ldy + i;
+    const uint32_t v[4] = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
     if (i + 8 <= a.cols) {
-      __builtin_memcpy(y, f, 32);
+      __builtin_memcpy(y, v, 16);
     } else {
 #pragma unroll
       for (int e = 0; e < 7; ++e)
-        if (i + e < a.cols) y[e] = f[e];
+        if (i + e < a.cols) y[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
     }
-    return;
-  }
-  uint16_t* y = reinterpret_cast<uint16_t*>(a.Y) + row * a.ldy + i;
-  const uint32_t v[4] = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
-  if (i + 8 <= a.cols) {
-    __builtin_memcpy(y, v, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (i + e < a.cols) y[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
   }
 }
 
-// Rows that a launch takes where each is spread over per_row workgroups of
-// 256: a launch holds fewer than 2^32 threads.
-int64_t band_rows(int64_t per_row) { return ((int64_t(1) << 24) - 1) / per_row; }
+// Rows that a launch takes where `across` tiles cover a row: it holds fewer
+// than 2^32 threads.  0: not even one tile high.
+int64_t band_rows(int64_t across, int steps) { return ((int64_t(1) << 24) - 1) / across * (4 * steps); }
+int64_t tiles_across(int64_t cols) { return (cols + kTileCols - 1) / kTileCols; }
+unsigned tiles_of(int64_t rows, int64_t across, int steps) {
+  return unsigned((rows + 4 * steps - 1) / (4 * steps) * across);
+}
 
-template <bool F32, int G, bool OFF>
-int run_quantize(const Q4Args& a, hipStream_t s) {
-  const int64_t per_row = (a.cols + 2047) / 2048, band = band_rows(per_row);
+// Tiles of 32 rows where they fill the compute units four times over, else of 8.
+bool tall_tiles(int64_t rows, int64_t cols) { return (rows + 31) / 32 >= (4 * kCus + tiles_across(cols) - 1) / tiles_across(cols); }
+
+template <bool F32, int G, bool OFF, int STEPS>
+int run_quantize_steps(const Q4Args& a, hipStream_t s) {
+  const int64_t across = tiles_across(a.cols), band = band_rows(across, STEPS);
   if (band == 0) return fail(UW_ERR_UNSUPPORTED, "uw_i4_quantize: a row wider than a launch holds");
   for (int64_t row0 = 0; row0 < a.rows; row0 += band) {
     Q4Args b = a;
     const int64_t es = a.st == UW_F32 ? 4 : 2;
     b.rows = std::min(band, a.rows - row0);
-    b.per_row = uint32_t(per_row);
+    b.across = uint32_t(across);
     b.X += row0 * a.ldx * (F32 ? 4 : 2);
     b.Q += row0 * a.ldq;
     b.scale += row0 * es;
     if (OFF) b.offset += row0 * es;
-    hipLaunchKernelGGL((quantize4_kernel<F32, G, OFF>), dim3(unsigned(b.rows * per_row)), dim3(256), 0, s, b);
+    hipLaunchKernelGGL((quantize4_kernel<F32, G, OFF, STEPS>), dim3(tiles_of(b.rows, across, STEPS)), dim3(256), 0, s, b);
     if (int rc = hip_check(hipGetLastError(), "quantize4_kernel launch")) return rc;
   }
   return UW_OK;
+}
+
+template <bool F32, int G, bool OFF>
+int run_quantize(const Q4Args& a, hipStream_t s) {
+  return tall_tiles(a.rows, a.cols) ? run_quantize_steps<F32, G, OFF, 8>(a, s) : run_quantize_steps<F32, G, OFF, 2>(a, s);
 }
 
 template <bool F32, int G>
@@ -369,20 +462,35 @@ int launch_i4_quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, i
   return xt == UW_F32 ? run_quantize_group<true>(a, group, s) : run_quantize_group<false>(a, group, s);
 }
 
-int launch_i4_dequantize(const uint8_t* Q, int64_t rows, int64_t cols, int64_t ldq, int group, const void* scale, int64_t lds,
-                         const void* offset, int64_t ldo, int st, void* Y, int64_t ldy, int yt, void* stream) {
-  const int64_t per_row = (cols + 2047) / 2048, band = band_rows(per_row);
+template <bool OFF, bool YF32, int STEPS>
+int run_dequantize(const D4Args& a, hipStream_t s) {
+  const int64_t across = tiles_across(a.cols), band = band_rows(across, STEPS), es = a.st == UW_F32 ? 4 : 2;
   if (band == 0) return fail(UW_ERR_UNSUPPORTED, "uw_i4_dequantize: a row wider than a launch holds");
-  const int64_t es = st == UW_F32 ? 4 : 2;
-  for (int64_t row0 = 0; row0 < rows; row0 += band) {
-    const D4Args a{Q + row0 * ldq, static_cast<const char*>(scale) + row0 * es,
-                   offset ? static_cast<const char*>(offset) + row0 * es : nullptr,
-                   static_cast<char*>(Y) + row0 * ldy * int64_t(elem_size(yt)), std::min(band, rows - row0), cols, ldq, lds, ldo,
-                   ldy, st, yt, group == 32 ? 5 : group == 64 ? 6 : 7, uint32_t(per_row)};
-    hipLaunchKernelGGL(dequantize4_kernel, dim3(unsigned(a.rows * per_row)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  for (int64_t row0 = 0; row0 < a.rows; row0 += band) {
+    D4Args b = a;
+    b.rows = std::min(band, a.rows - row0);
+    b.across = uint32_t(across);
+    b.Q += row0 * a.ldq;
+    b.scale += row0 * es;
+    if (OFF) b.offset += row0 * es;
+    b.Y += row0 * a.ldy * (YF32 ? 4 : 2);
+    hipLaunchKernelGGL((dequantize4_kernel<OFF, YF32, STEPS>), dim3(tiles_of(b.rows, across, STEPS)), dim3(256), 0, s, b);
     if (int rc = hip_check(hipGetLastError(), "dequantize4_kernel launch")) return rc;
   }
   return UW_OK;
+}
+template <bool OFF, bool YF32>
+int run_dequantize_tiles(const D4Args& a, hipStream_t s) {
+  return tall_tiles(a.rows, a.cols) ? run_dequantize<OFF, YF32, 8>(a, s) : run_dequantize<OFF, YF32, 2>(a, s);
+}
+
+int launch_i4_dequantize(const uint8_t* Q, int64_t rows, int64_t cols, int64_t ldq, int group, const void* scale, int64_t lds,
+                         const void* offset, int64_t ldo, int st, void* Y, int64_t ldy, int yt, void* stream) {
+  const D4Args a{Q, static_cast<const char*>(scale), static_cast<const char*>(offset), static_cast<char*>(Y), rows, cols, ldq,
+                 lds, ldo, ldy, st, group == 32 ? 5 : group == 64 ? 6 : 7, 0};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (offset) return yt == UW_F32 ? run_dequantize_tiles<true, true>(a, s) : run_dequantize_tiles<true, false>(a, s);
+  return yt == UW_F32 ? run_dequantize_tiles<false, true>(a, s) : run_dequantize_tiles<false, false>(a, s);
 }
 
 }  // namespace uw
