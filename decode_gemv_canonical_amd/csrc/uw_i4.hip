@@ -58,10 +58,14 @@ __device__ __forceinline__ void unpack8(const Raw8& v, float (&f)[8]) {
   }
 }
 
-// A workgroup of 256 threads takes kTileRows rows by kTileCols columns, a wave
-// a row at a time, so that the scales of a group go out (and come in) for 32
-// rows side by side: one at a time they cost as much as the matrix (groups of
-// 32: 55 us for 14336 x 4096).
+// A workgroup of 256 threads takes 16 rows (8 where those are few) by kTileCols
+// columns, a wave a row at a time with all its loads issued first, so that the
+// scales of a group go out (and come in) for 16 rows side by side: a row at a
+// time they cost as much as the matrix (14336 x 4096, groups of 32 with offsets:
+// 55 us, with these tiles 43; back 53, 34).  Bytes bound the plain forms (groups
+// of 128: 34.4 us from bf16, 4.3 TB/s; 50 from fp32, 5.3; back 29.8, 4.9), the
+// vector ALU the quantisation with offsets (three divisions, and the smallest and
+// largest value, for every 8 values).
 constexpr int kTileCols = 512;
 
 struct Q4Args {
@@ -287,8 +291,9 @@ unsigned tiles_of(int64_t rows, int64_t across, int steps) {
   return unsigned((rows + 4 * steps - 1) / (4 * steps) * across);
 }
 
-// Tiles of 32 rows where they fill the compute units four times over, else of 8.
-bool tall_tiles(int64_t rows, int64_t cols) { return (rows + 31) / 32 >= (4 * kCus + tiles_across(cols) - 1) / tiles_across(cols); }
+// Tiles of 16 rows where they fill the compute units four times over, else of 8
+// (37 x 1001 takes 3.5 us then, with 32 10.5).
+bool tall_tiles(int64_t rows, int64_t cols) { return (rows + 15) / 16 >= (4 * kCus + tiles_across(cols) - 1) / tiles_across(cols); }
 
 template <bool F32, int G, bool OFF, int STEPS>
 int run_quantize_steps(const Q4Args& a, hipStream_t s) {
@@ -311,7 +316,7 @@ int run_quantize_steps(const Q4Args& a, hipStream_t s) {
 
 template <bool F32, int G, bool OFF>
 int run_quantize(const Q4Args& a, hipStream_t s) {
-  return tall_tiles(a.rows, a.cols) ? run_quantize_steps<F32, G, OFF, 8>(a, s) : run_quantize_steps<F32, G, OFF, 2>(a, s);
+  return tall_tiles(a.rows, a.cols) ? run_quantize_steps<F32, G, OFF, 4>(a, s) : run_quantize_steps<F32, G, OFF, 2>(a, s);
 }
 
 template <bool F32, int G>
@@ -326,8 +331,10 @@ int run_quantize_group(const Q4Args& a, int group, hipStream_t s) {
                        : run_quantize_form<F32, 128>(a, s);
 }
 
-// 32-bit offsets inside a tile of 256 rows, and over the scales.
+// 32-bit offsets inside a tile of 256 rows, and over the scales.  (Where there is
+// one row the stride says nothing of its length.)
 bool offsets_ok(const I4Args& a, int group) {
+  if (a.cols >= int64_t(1) << 21) return false;
   const int64_t span = (a.cols + group - 1) / group * (a.st == UW_F32 ? 4 : 2), most = int64_t(1) << 31;
   return a.ldx < (int64_t(1) << 21) && a.ldw < (int64_t(1) << 22) && span * a.lds < most && span * a.ldo < most &&
          a.rows * 4 < most;
@@ -481,7 +488,7 @@ int run_dequantize(const D4Args& a, hipStream_t s) {
 }
 template <bool OFF, bool YF32>
 int run_dequantize_tiles(const D4Args& a, hipStream_t s) {
-  return tall_tiles(a.rows, a.cols) ? run_dequantize<OFF, YF32, 8>(a, s) : run_dequantize<OFF, YF32, 2>(a, s);
+  return tall_tiles(a.rows, a.cols) ? run_dequantize<OFF, YF32, 4>(a, s) : run_dequantize<OFF, YF32, 2>(a, s);
 }
 
 int launch_i4_dequantize(const uint8_t* Q, int64_t rows, int64_t cols, int64_t ldq, int group, const void* scale, int64_t lds,

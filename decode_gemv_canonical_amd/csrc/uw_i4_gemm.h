@@ -816,6 +816,21 @@ struct StagedGroups {
   }
 };
 
+// Where the 16-byte chunks of a staged block lie in LDS.  A 16-byte read serves
+// 16 lanes at a time in 64 banks: lanes 0 .. 3, 12 .. 15, 20 .. 27 first, then
+// the other 16 of the half.  The products' lane (r, q) reads activation chunk
+// 4 q + s (groups of 128) or 4 s + q of row r, weight chunk q of row r: with
+// activations' chunks in the order of 4 s + q, against the row's low bits, and
+// weights' against minus the row's quarter, every 16 lanes fall on all 64 banks
+// (plain c ^ (r % 16) and c ^ (r / 4): two on each, twice the time).
+template <int G>
+__device__ __forceinline__ int x_order(int c) { return G == 128 ? c % 4 * 4 + c / 4 : c; }  // its own inverse
+template <int G>
+__device__ __forceinline__ int x_slot(int chunk, int row) { return x_order<G>(chunk) ^ (row % 16); }
+template <int G>
+__device__ __forceinline__ int x_chunk(int slot, int row) { return x_order<G>(slot ^ (row % 16)); }
+__device__ __forceinline__ int w_slot(int chunk, int row) { return chunk ^ (-(row / 4) & 3); }  // its own inverse
+
 // Few tokens, long rows: as the slices, with everything staged by direct loads
 // into the wave's own ring of D blocks in LDS, so that many blocks are in
 // flight without registers and nothing but the wave's own loads is waited for.
@@ -840,7 +855,7 @@ __global__ __launch_bounds__(64 * KW) void i4_deep_kernel(I4Args a, int nw_tiles
   const Groups scale(a.scale, a.lds, groups, a.rows, row0), offset(OFF ? a.offset : a.scale, OFF ? a.ldo : a.lds, groups, a.rows, row0);
   const int nkb = int((a.cols + 127) / 128), n = (nkb - wave + KW - 1) / KW;  // this wave's blocks
   const int wlast = int((a.cols - 1) / 32) % 4, xlast = int((a.cols - 1) / 8) % 16;  // the last block's last chunks
-  const int wchunk = (lane % 4) ^ (lane / 16);
+  const int wchunk = w_slot(lane % 4, lane / 4);
   uint32_t wvo[WI], xvo[4 * BJ];
 #pragma unroll
   for (int u = 0; u < WI; ++u) wvo[u] = uint32_t(min(16 * u + lane / 4, tw.last)) * uint32_t(a.ldw);
@@ -853,7 +868,7 @@ __global__ __launch_bounds__(64 * KW) void i4_deep_kernel(I4Args a, int nw_tiles
     const int wmost = kb == nkb - 1 ? wlast : 3, xmost = kb == nkb - 1 ? xlast : 15;
 #pragma unroll
     for (int u = 0; u < 4 * BJ; ++u)
-      stage_load<false>(tx.rsrc, xvo[u] + 16 * min(r ^ (4 * (u % 4) + q), xmost), uint32_t(kb) * 256, base + u * 1024);
+      stage_load<false>(tx.rsrc, xvo[u] + 16 * min(x_chunk<G>(r, 4 * (u % 4) + q), xmost), uint32_t(kb) * 256, base + u * 1024);
 #pragma unroll
     for (int u = 0; u < WI; ++u) stage_load<false>(tw.rsrc, wvo[u] + 16 * min(wchunk, wmost), uint32_t(kb) * 64, base + kX + u * 1024);
     scale.issue(kb, lane, base + kX + kW);
@@ -878,12 +893,12 @@ __global__ __launch_bounds__(64 * KW) void i4_deep_kernel(I4Args a, int nw_tiles
     u32x4 w[WI], x[BJ][4];
     float sc[WI][GB], mc[WI][GB];
 #pragma unroll
-    for (int t = 0; t < WI; ++t) w[t] = __builtin_bit_cast(u32x4, ld128(base + kX + uint32_t(16 * t + r) * 64 + uint32_t(q ^ (r / 4)) * 16));
+    for (int t = 0; t < WI; ++t) w[t] = __builtin_bit_cast(u32x4, ld128(base + kX + uint32_t(16 * t + r) * 64 + uint32_t(w_slot(q, r)) * 16));
 #pragma unroll
     for (int j = 0; j < BJ; ++j)
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        x[j][s] = __builtin_bit_cast(u32x4, ld128(base + uint32_t(16 * j + r) * 256 + uint32_t((G == 128 ? 4 * q + s : 4 * s + q) ^ r) * 16));
+        x[j][s] = __builtin_bit_cast(u32x4, ld128(base + uint32_t(16 * j + r) * 256 + uint32_t((4 * s + q) ^ r) * 16));
 #pragma unroll
     for (int t = 0; t < WI; ++t)
 #pragma unroll
@@ -975,9 +990,7 @@ __global__ __launch_bounds__(64 * KW) void i4_deep_kernel(I4Args a, int nw_tiles
 // with its own two stages, take every KG-th block and add their sums in LDS at
 // the end.
 //
-// In LDS the 16-byte chunk c of an activation row r lies at chunk c ^ (r % 16),
-// that of a weight row at c ^ (r / 4 % 4): the 8 lanes that a read serves at a
-// time fall into different banks.  In the last block, lanes past the last
+// In the last block, lanes past the last
 // chunk of their row read that chunk again; what lies past `cols` is then
 // cleared in the activations.
 // LOOSE: activation rows that start at any element go through registers into
@@ -1010,7 +1023,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
   // a lane's rows and chunks of each load; chunks are the same for all of them
   static_assert(NW % 4 == 0, "rows of a load");
   constexpr int LWN = (LW + NW - 1) / NW, LBN = (LB + NW - 1) / NW;
-  const int wchunk = (lane % 4) ^ (lane / 16), xchunk = r ^ (4 * (wave % 4) + q);
+  const int wchunk = w_slot(lane % 4, lane / 4), xchunk = x_chunk<G>(r, 4 * (wave % 4) + q);
   uint32_t wvo[LWN], xvo[LBN];
 #pragma unroll
   for (int u = 0; u < LWN; ++u) wvo[u] = uint32_t(min(16 * (u * NW + wave) + lane / 4, tw.last)) * uint32_t(a.ldw) + 16 * wchunk;
@@ -1067,7 +1080,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     for (int at = wave * kWave + lane; at < BB * 16; at += NW * kWave) {
       const int row = at / 16, chunk = at % 16;
       if (8 * chunk + 8 <= left) continue;
-      const uint32_t p = ring + uint32_t(i & 1) * kStage + kWBytes + uint32_t(row) * 256 + uint32_t(chunk ^ (row % 16)) * 16;
+      const uint32_t p = ring + uint32_t(i & 1) * kStage + kWBytes + uint32_t(row) * 256 + uint32_t(x_slot<G>(chunk, row)) * 16;
       st128(p, __builtin_bit_cast(uint4, __builtin_bit_cast(u32x4, ld128(p)) & tail_mask8(left - 8 * chunk)));
     }
   };
@@ -1095,7 +1108,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
   for (int i = 0; i < WI; ++i)
 #pragma unroll
     for (int j = 0; j < BJ; ++j) acc[i][j] = zero;
-  const uint32_t wat = uint32_t(ww * WI * 16 + r) * 64 + uint32_t(q ^ (r / 4)) * 16;
+  const uint32_t wat = uint32_t(ww * WI * 16 + r) * 64 + uint32_t(w_slot(q, r)) * 16;
   const uint32_t xat = kWBytes + uint32_t(wb * BJ * 16 + r) * 256;
   auto multiply = [&](int i, const float (&sc)[WI][GB], const float (&mc)[WI][GB]) {
     const uint32_t base = ring + uint32_t(i & 1) * kStage;
@@ -1111,12 +1124,16 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     // products run; the barriers keep the compiler from holding more tiles than that in registers
     bf16x8 x[2][4];
     f32x4 part[2][WI], sum[2];
+    // kept apart, so that a read's address is one of these and a constant
+    uint32_t xs[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      xs[s] = base + xat + uint32_t((4 * s + q) ^ r) * 16;
+      asm("" : "+v"(xs[s]));
+    }
     auto read = [&](int j, bf16x8 (&to)[4]) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int chunk = G == 128 ? 4 * q + s : 4 * s + q;
-        to[s] = __builtin_bit_cast(bf16x8, ld128(base + xat + uint32_t(j) * 4096 + uint32_t(chunk ^ r) * 16));
-      }
+      for (int s = 0; s < 4; ++s) to[s] = __builtin_bit_cast(bf16x8, ld128(xs[s] + uint32_t(j) * 4096));
     };
     auto fold = [&](int j, int g, const f32x4 (&pt)[WI], const f32x4& sm) {
 #pragma unroll
