@@ -980,29 +980,42 @@ __global__ __launch_bounds__(64 * KW) void i4_deep_kernel(I4Args a, int nw_tiles
   }
 }
 
-// Many tokens.  The packed weights and the activations of a block of 128
-// columns are staged in LDS for the whole workgroup, one block ahead of the
-// products: BW = 16 WI WGW weight rows (64 bytes each) and BB = 16 BJ WGB
-// activation rows (256 bytes each), whose WGW x WGB waves each hold WI x BJ
-// tiles of 16 x 16.  A wave decodes its WI x 128 weights of a block into
-// registers once and runs them against one tile of tokens after another, so
-// that a group's sums live for one tile only.  KG groups of such waves, each
-// with its own two stages, take every KG-th block and add their sums in LDS at
-// the end.
+// Many tokens.  The activations of a block of 128 columns are staged in LDS for
+// the whole workgroup, one block ahead of the products: NW waves hold BB = 16 BJ
+// activation rows (256 bytes each) by 16 WI weight rows each, as WI x BJ tiles
+// of 16 x 16.  A wave decodes its WI x 128 weights of a block into registers
+// once and runs them against one tile of tokens after another, so that a group's
+// sums live for one tile only.  KG groups of such waves, each with its own two
+// stages, take every KG-th block and add their sums in LDS at the end.
 //
-// In the last block, lanes past the last
-// chunk of their row read that chunk again; what lies past `cols` is then
-// cleared in the activations.
+// A compute unit's matrix cores take 16 cycles a product and let 8 cycles of
+// the vector ALU's through beside it, about 4.3 an operation: two operations a
+// product go unseen, the third does not.  Decoding takes 15 per 8 weights, which
+// BJ tiles share, scaling one per product, so a tall tile of 256 tokens has
+// about two; and the decoding is kept beside other waves' products: with up to
+// 3 groups a wave reads its packed rows straight into registers, and half of
+// the waves decode the next block behind their products, under the barrier that
+// the others decode after (14336 x 4096, 4096 tokens: 422 us, 1.14 PF/s; all of
+// them after it 437; every wave at one priority 468).  Four groups are four
+// waves to a SIMD, which cover each other without that, and their packed rows
+// come faster through LDS, by direct loads (64 x 64 tiles: 867 us against 987).
+//
+// In the last block, lanes past the last chunk of their row read that chunk
+// again; what lies past `cols` is then cleared in the activations.
+// The smallest tile, with groups of 128 without offsets, fits twice into a compute unit's
+// registers (64 rows of 14336 x 4096 x 16 tokens: 11.5 us against 12.5).
 // LOOSE: activation rows that start at any element go through registers into
 // LDS, loaded before a block's products and stored behind them.
-template <int G, bool OFF, bool S32, int WGW, int WGB, int WI, int BJ, int KG, bool LOOSE>
-__global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a, int nw_tiles, int nb_tiles, int per_xcd) {
-  constexpr int NW = WGW * WGB, GB = 128 / G;
-  constexpr int BW = 16 * WI * WGW, BB = 16 * BJ * WGB;
-  constexpr int LW = BW / 16, LB = BB / 4;  // 1 KB loads of a stage
-  constexpr uint32_t kWBytes = BW * 64, kStage = BW * 64 + BB * 256;
+constexpr bool stage_own(int groups) { return groups < 4; }
+template <int G, bool OFF, bool S32, int NW, int WI, int BJ, int KG, bool LOOSE>
+__global__ __launch_bounds__(64 * NW * KG, G == 128 && !OFF && KG == 4 && BJ == 1 ? 8 : 1) void i4_stage_kernel(I4Args a, int nw_tiles, int nb_tiles, int per_xcd) {
+  constexpr int GB = 128 / G;
+  constexpr int BW = 16 * WI * NW, BB = 16 * BJ;
+  constexpr int LB = BB / 4;  // 1 KB loads of a stage's activations
+  constexpr int LW = BW / 16;
+  constexpr bool kOwn = stage_own(KG);
+  constexpr uint32_t kX = BB * 256, kStage = kX + (kOwn ? 0 : BW * 64);
   constexpr int kPartial = NW * WI * BJ * 1024;  // a group's sums
-  static_assert((KG - 1) * kPartial + NW * epilogue_bytes<WI> <= KG * 2 * int(kStage), "LDS");
   // workgroups are dealt to the XCDs round-robin: each XCD takes a run of
   // tiles, 4 activation tiles deep, so that its L2 serves the rereads
   const int id = int(blockIdx.x % kXcds) * per_xcd + int(blockIdx.x / kXcds);
@@ -1015,18 +1028,23 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
   const int lane = int(threadIdx.x) % kWave, w_all = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int group = w_all / NW, wave = w_all % NW;
   const int r = lane % 16, q = lane / 16;
-  const int ww = wave / WGB, wb = wave % WGB;
   const Staged4 tw(a.W + row0 * a.ldw, a.rows - row0, (a.cols + 31) / 32 * 16, a.ldw, BW);
   const Staged4 tx(a.X + b0 * a.ldx, a.batch - b0, 2 * a.cols, 2 * a.ldx, BB);
   const int nkb = int((a.cols + 127) / 128), n = (nkb - group + KG - 1) / KG;
   const uint32_t ring = uint32_t(group) * (2 * kStage);
   // a lane's rows and chunks of each load; chunks are the same for all of them
   static_assert(NW % 4 == 0, "rows of a load");
-  constexpr int LWN = (LW + NW - 1) / NW, LBN = (LB + NW - 1) / NW;
-  const int wchunk = w_slot(lane % 4, lane / 4), xchunk = x_chunk<G>(r, 4 * (wave % 4) + q);
+  constexpr int LBN = (LB + NW - 1) / NW;
+  const int xchunk = x_chunk<G>(r, 4 * (wave % 4) + q);
+  // own weights: rows r of the wave's tiles and chunk q; else the rows and chunks of its 1 KB loads
+  constexpr int LWN = kOwn ? WI : (LW + NW - 1) / NW;
+  const int wchunk = kOwn ? q : w_slot(lane % 4, lane / 4);
   uint32_t wvo[LWN], xvo[LBN];
 #pragma unroll
-  for (int u = 0; u < LWN; ++u) wvo[u] = uint32_t(min(16 * (u * NW + wave) + lane / 4, tw.last)) * uint32_t(a.ldw) + 16 * wchunk;
+  for (int u = 0; u < LWN; ++u) {
+    const int row = kOwn ? 16 * (wave * WI + u) + r : 16 * (u * NW + wave) + lane / 4;
+    wvo[u] = uint32_t(min(row, tw.last)) * uint32_t(a.ldw) + 16 * wchunk;
+  }
 #pragma unroll
   for (int u = 0; u < LBN; ++u) xvo[u] = uint32_t(min(4 * (u * NW + wave) + q, tx.last)) * uint32_t(2 * a.ldx) + 16 * xchunk;
   // in the last block, how far a lane's chunk lies past the row's last one
@@ -1055,7 +1073,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     }
   };
   auto store_tokens = [&](int i) {
-    const uint32_t base = ring + uint32_t(i & 1) * kStage + kWBytes + 16 * lane;
+    const uint32_t base = ring + uint32_t(i & 1) * kStage + 16 * lane;
 #pragma unroll
     for (int u = 0; u < LBN; ++u)
       if (LB % NW == 0 || u * NW + wave < LB) st128(base + uint32_t(u * NW + wave) * 1024, __builtin_bit_cast(uint4, xr[u]));
@@ -1066,13 +1084,9 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     const bool end = kb == nkb - 1;
     if (LOOSE && i > 0) load_tokens(i);
 #pragma unroll
-    for (int u = 0; u < LWN; ++u)
-      if (LW % NW == 0 || u * NW + wave < LW)
-        stage_load<false>(tw.rsrc, wvo[u] - (end ? wover : 0u), uint32_t(kb) * 64, base + uint32_t(u * NW + wave) * 1024);
-#pragma unroll
     for (int u = 0; u < LBN; ++u)
       if (!LOOSE && (LB % NW == 0 || u * NW + wave < LB))
-        stage_load<false>(tx.rsrc, xvo[u] - (end ? xover : 0u), uint32_t(kb) * 256, base + kWBytes + uint32_t(u * NW + wave) * 1024);
+        stage_load<false>(tx.rsrc, xvo[u] - (end ? xover : 0u), uint32_t(kb) * 256, base + uint32_t(u * NW + wave) * 1024);
   };
   // what the last block holds past `cols` is cleared by the group's threads
   auto clear_tail = [&](int i) {
@@ -1080,7 +1094,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
     for (int at = wave * kWave + lane; at < BB * 16; at += NW * kWave) {
       const int row = at / 16, chunk = at % 16;
       if (8 * chunk + 8 <= left) continue;
-      const uint32_t p = ring + uint32_t(i & 1) * kStage + kWBytes + uint32_t(row) * 256 + uint32_t(x_slot<G>(chunk, row)) * 16;
+      const uint32_t p = ring + uint32_t(i & 1) * kStage + uint32_t(row) * 256 + uint32_t(x_slot<G>(chunk, row)) * 16;
       st128(p, __builtin_bit_cast(uint4, __builtin_bit_cast(u32x4, ld128(p)) & tail_mask8(left - 8 * chunk)));
     }
   };
@@ -1094,7 +1108,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
       const uint32_t gi = min(g0 + g, uint32_t(groups - 1));
 #pragma unroll
       for (int t = 0; t < WI; ++t) {
-        const uint32_t row = min(uint32_t(16 * (ww * WI + t) + r), uint32_t(tw.last));
+        const uint32_t row = min(uint32_t(16 * (wave * WI + t) + r), uint32_t(tw.last));
         sn[t][g] = scale.load(gi, row);
         if (OFF) mn[t][g] = offset.load(gi, row);
       }
@@ -1108,18 +1122,34 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
   for (int i = 0; i < WI; ++i)
 #pragma unroll
     for (int j = 0; j < BJ; ++j) acc[i][j] = zero;
-  const uint32_t wat = uint32_t(ww * WI * 16 + r) * 64 + uint32_t(w_slot(q, r)) * 16;
-  const uint32_t xat = kWBytes + uint32_t(wb * BJ * 16 + r) * 256;
-  auto multiply = [&](int i, const float (&sc)[WI][GB], const float (&mc)[WI][GB]) {
-    const uint32_t base = ring + uint32_t(i & 1) * kStage;
-    bf16x8 w[WI][4];
+  // the wave's weights of a block: as they lie in memory, then decoded
+  u32x4 raw[WI];
+  bf16x8 w[WI][4];
+  auto load_weights = [&](int i) {
+    const int kb = block(i);
+#pragma unroll
+    for (int u = 0; u < LWN; ++u) {
+      const uint32_t voff = wvo[u] - (kb == nkb - 1 ? wover : 0u);
+      if (kOwn) raw[u] = buffer_load16<false>(tw.rsrc, voff, uint32_t(kb) * 64);
+      else if (LW % NW == 0 || u * NW + wave < LW)
+        stage_load<false>(tw.rsrc, voff, uint32_t(kb) * 64, ring + uint32_t(i & 1) * kStage + kX + uint32_t(u * NW + wave) * 1024);
+    }
+  };
+  auto decode = [&](int i) {
 #pragma unroll
     for (int t = 0; t < WI; ++t) {
-      u32x4 v = __builtin_bit_cast(u32x4, ld128(base + wat + uint32_t(t) * 1024));
-      if (G != 128) transpose4(v);
+      if (!kOwn) {
+        const uint32_t row = uint32_t((wave * WI + t) * 16 + r);
+        raw[t] = __builtin_bit_cast(u32x4, ld128(ring + uint32_t(i & 1) * kStage + kX + row * 64 + uint32_t(w_slot(q, r)) * 16));
+      }
+      if (G != 128) transpose4(raw[t]);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) w[t][s] = decode_q8(v[s]);
+      for (int s = 0; s < 4; ++s) w[t][s] = decode_q8(raw[t][s]);
     }
+  };
+  const uint32_t xat = uint32_t(r) * 256;
+  auto multiply = [&](int i, const float (&sc)[WI][GB], const float (&mc)[WI][GB]) {
+    const uint32_t base = ring + uint32_t(i & 1) * kStage;
     // one tile of tokens at a time: the next one's operands are read and the last one's sums are scaled while this one's
     // products run; the barriers keep the compiler from holding more tiles than that in registers
     bf16x8 x[2][4];
@@ -1168,13 +1198,17 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
   };
   if (n > 0) {
     if (LOOSE) load_first();
+    load_weights(0);
     issue(0);
     scales(0);
     if (LOOSE) store_tokens(0);
   }
   // every wave takes part in the barriers of the first group's blocks
   const int steps = (nkb + KG - 1) / KG;
-  if (w_all >= 4) __builtin_amdgcn_s_setprio(1);
+  const bool late = kOwn && w_all / 4 % 2;
+  if (late && n > 0) decode(0);
+  if (late) __builtin_amdgcn_s_setprio(2);
+  else if (kOwn || w_all >= 4) __builtin_amdgcn_s_setprio(1);
 #pragma unroll 1
   for (int i = 0; i < steps; ++i) {
     wait_vmcnt<0>();  // this wave's loads of block i (and its scales) have landed
@@ -1191,13 +1225,24 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
         sc[t][g] = scale.value(sn[t][g]);
         mc[t][g] = OFF ? offset.value(mn[t][g]) * 0.0625f : 0.f;
       }
+    // ahead of the loads, whose arrival the compiler would wait for together with the weights'
+    if (kOwn && !late && i < n) decode(i);
     if (i + 1 < n) {
+      load_weights(i + 1);
       issue(i + 1);
       scales(i + 1);
     }
     // a branch even where every group has the block: across it the compiler would hold more in registers than there are
-    if (i < n) multiply(i, sc, mc);
+    if (i < n) {
+      if (!kOwn) decode(i);
+      multiply(i, sc, mc);
+    }
     if (LOOSE && i + 1 < n) store_tokens(i + 1);
+    if (late && i + 1 < n) {
+      __builtin_amdgcn_s_setprio(0);
+      decode(i + 1);
+      __builtin_amdgcn_s_setprio(2);
+    }
   }
   __syncthreads();  // no wave reads the rings any more
   if (KG > 1) {
@@ -1222,7 +1267,7 @@ __global__ __launch_bounds__(64 * WGW * WGB * KG) void i4_stage_kernel(I4Args a,
           for (int e = 0; e < 4; ++e) acc[i][j][e] += v[e];
         }
   }
-  const int64_t n0 = row0 + 16 * ww * WI, bw0 = b0 + 16 * wb * BJ;
+  const int64_t n0 = row0 + 16 * wave * WI, bw0 = b0;
   const uint32_t out = uint32_t((KG - 1) * kPartial + wave * epilogue_bytes<WI>);
   if (a.yt == UW_F32) store_through_lds<WI, BJ, false, false>(a, n0, bw0, out, lane, acc);
   else store_through_lds<WI, BJ, true, false>(a, n0, bw0, out, lane, acc);
@@ -1294,14 +1339,14 @@ int run_deep(const I4Args& a, hipStream_t s) {
   return hip_check(hipGetLastError(), "i4_deep_kernel launch");
 }
 
-template <int G, bool OFF, bool S32, int WGW, int WGB, int WI, int BJ, int KG, bool LOOSE = false>
+template <int G, bool OFF, bool S32, int NW, int WI, int BJ, int KG, bool LOOSE = false>
 int run_stage(const I4Args& a, hipStream_t s) {
-  constexpr int BW = 16 * WI * WGW, BB = 16 * BJ * WGB, kThreads = 64 * WGW * WGB * KG;
+  constexpr int BW = 16 * WI * NW, BB = 16 * BJ, kThreads = 64 * NW * KG;
   const int64_t nw = (a.rows + BW - 1) / BW, nb = (a.batch + BB - 1) / BB;
   if (int rc = check_launch(nw, nb, kThreads)) return rc;
   const int64_t per_xcd = (nw * nb + kXcds - 1) / kXcds;
-  auto kern = i4_stage_kernel<G, OFF, S32, WGW, WGB, WI, BJ, KG, LOOSE>;
-  constexpr size_t kLds = size_t(KG) * 2 * (BW * 64 + BB * 256);
+  auto kern = i4_stage_kernel<G, OFF, S32, NW, WI, BJ, KG, LOOSE>;
+  constexpr size_t kLds = std::max(size_t(KG) * 2 * (BB * 256 + (stage_own(KG) ? 0 : BW * 64)), size_t(KG - 1) * NW * WI * BJ * 1024 + NW * epilogue_bytes<WI>);
   static_assert(kLds <= kLdsLimit, "LDS");
   allow_full_lds(kern);
   hipLaunchKernelGGL(kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), kLds, s, a, int(nw), int(nb), int(per_xcd));
@@ -1320,16 +1365,16 @@ int run_gemm(const I4Args& a, int shape, hipStream_t s) {
     case 7: return run_slice<G, OFF, S32, 2, 1, 16, 1>(a, s);
     case 8: return run_deep<G, OFF, S32, 1, 1, 8, 3>(a, s);
     case 9: return run_deep<G, OFF, S32, 2, 1, 8, 2>(a, s);
-    case 10: return run_stage<G, OFF, S32, 4, 1, 1, 1, 4>(a, s);   // 64 x 16, 4 groups
-    case 11: return run_stage<G, OFF, S32, 4, 1, 1, 2, 4>(a, s);   // 64 x 32, 4 groups
-    case 12: return run_stage<G, OFF, S32, 4, 1, 1, 4, 4>(a, s);   // 64 x 64, 4 groups
-    case 13: return run_stage<G, OFF, S32, 4, 1, 2, 4, 3>(a, s);   // 128 x 64, 3 groups
-    case 14: return run_stage<G, OFF, S32, 4, 1, 2, 8, 2>(a, s);   // 128 x 128, 2 groups
-    case 15: return run_stage<G, OFF, S32, 8, 1, 2, (OFF || G == 32 ? 12 : 16), 1>(a, s);  // 256 x 256, or 192 where registers hold no more
-    case 16: return run_stage<G, OFF, S32, 4, 1, 1, 2, 4, true>(a, s);   // 64 x 32, 4 groups
-    case 17: return run_stage<G, OFF, S32, 4, 1, 1, 4, 4, true>(a, s);   // 64 x 64, 4 groups
-    case 18: return run_stage<G, OFF, S32, 4, 1, 2, 8, 2, true>(a, s);   // 128 x 128, 2 groups
-    default: return run_stage<G, OFF, S32, 8, 1, 2, 8, 1, true>(a, s);   // 256 x 128
+    case 10: return run_stage<G, OFF, S32, 4, 1, 1, 4>(a, s);   // 64 x 16, 4 groups
+    case 11: return run_stage<G, OFF, S32, 4, 1, 2, 4>(a, s);   // 64 x 32, 4 groups
+    case 12: return run_stage<G, OFF, S32, 4, 1, 4, 4>(a, s);   // 64 x 64, 4 groups
+    case 13: return run_stage<G, OFF, S32, 4, 2, 4, 3>(a, s);   // 128 x 64, 3 groups
+    case 14: return run_stage<G, OFF, S32, 4, 2, 8, 2>(a, s);   // 128 x 128, 2 groups
+    case 15: return run_stage<G, OFF, S32, 8, 2, (OFF || G == 32 ? 12 : 16), 1>(a, s);  // 256 x 256, or 192 where registers hold no more
+    case 16: return run_stage<G, OFF, S32, 4, 1, 2, 4, true>(a, s);   // 64 x 32, 4 groups
+    case 17: return run_stage<G, OFF, S32, 4, 1, 4, 4, true>(a, s);   // 64 x 64, 4 groups
+    case 18: return run_stage<G, OFF, S32, 4, 2, 8, 2, true>(a, s);   // 128 x 128, 2 groups
+    default: return run_stage<G, OFF, S32, 8, 2, 8, 1, true>(a, s);   // 256 x 128
   }
 }
 
