@@ -199,6 +199,36 @@ def test_gemm_drawn_sizes():
                  rng.random() < 0.5, 0, True, rng.choice((0, 0, 1, 8)), rng.choice((0, 0, 3, 8)), seed=i)
 
 
+@pytest.mark.parametrize("b,rows,cols,group", [(1, 1, (1 << 21) + 5, 32), (2, 3, (1 << 21) + 40, 128)])
+def test_gemm_rows_past_32_bit_offsets(b, rows, cols, group):
+    _say(f"rows past 32-bit offsets: {b} x {rows} x {cols}")
+    run_gemm(b, rows, cols, group, True, "f32", "f32", bias=True)
+
+
+@pytest.mark.parametrize("far", ["W", "X", "scale", "offset"])
+def test_gemm_strides_past_32_bits(far):
+    """One operand at strides whose offsets pass 32 bits (or the bound below them): the same results to the bit of whole numbers."""
+    _say(f"strides past 32 bits: {far}")
+    w = Weights(40, 250, 32, True, "f32", seed=3, whole=True)
+    X = tokens(20, 250, 4, whole=True)
+    Y, y_ok = inside(20, 40, torch.float32)
+    if far == "W":
+        wide = torch.empty_strided((40, 128), (1 << 27, 1), dtype=torch.uint8, device=DEV)[:, :125]  # whole 16-byte words
+        wide.copy_(w.W)
+        w.W = wide
+    elif far == "X":
+        wide = torch.empty_strided(X.shape, (1 << 27, 1), dtype=torch.bfloat16, device=DEV)
+        wide.copy_(X)
+        X = wide
+    else:
+        wide = torch.empty_strided(w.scale.shape, ((1 << 27) + 4, 1), dtype=torch.float32, device=DEV)
+        wide.copy_(getattr(w, far))
+        setattr(w, far, wide)
+    w.run(X, Y)
+    torch.cuda.synchronize()
+    assert np.array_equal(f64(Y), w.ref(f64(X))[0]) and y_ok()
+
+
 def test_gemm_infinities_stay_in_their_token():
     for shape in SHAPES:  # 520 columns: rows on 16-byte boundaries
         for affine, b in itertools.product((False, True), (4, 16, 40)):

@@ -130,6 +130,15 @@ def test_gemm_refuses_more_tiles_than_a_launch_holds():
         assert gemm(shape=shape, **big) == UNSUP
 
 
+def test_gemm_shapes_refuse_what_does_not_fit_their_offsets():
+    long = dict(rows=1, batch=1, cols=1 << 21, ldw=1 << 20, ldx=1 << 21, lds=1, group=32, X=P + (1 << 24), scale=P + (1 << 26),
+                Y=P + (1 << 28))
+    far = dict(scale=1 << 40, lds=1 << 30, cols=128, group=32, ldw=64, ldx=128, X=1 << 38)
+    for shape in range(2, uw.uw_i4_gemm_shape_count()):
+        for k in (long, far, dict(ldw=1 << 22, X=1 << 38), dict(ldx=1 << 21, Y=1 << 38)):
+            assert gemm(shape=shape, **k) == UNSUP, (shape, k)
+
+
 def norm(**k):
     a = dict(X=P, batch=4, cols=64, ldx=64, xt=BF16, post_norm=1, post=P + 65536, pt=BF16, post_eps=1e-5, gate=P + 69632, ldg=0,
              gt=BF16, block_scale=1.0, R=P + 4096, ldr=64, rt=BF16, residual_scale=1.0, H=P + 8192, ldh=64, gain=P + 73728,
