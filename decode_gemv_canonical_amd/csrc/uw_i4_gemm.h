@@ -4,14 +4,18 @@
 //
 //   Y[b, n] = sum_g s[g, n] (sum_k q[n, k] X[b, k]) + m[g, n] (sum_k X[b, k]) (+ bias[n])
 //
-// Product: u = q + 8 as an 8-bit float code (e4m3: the codes 0 .. 15 stand for
-// 0 .. 15 times 2^-9) is converted to bf16 two at a time, exactly; its product
-// with a bf16 activation is exact too, and the matrix cores add a group's
-// products in fp32.  The sum starts from -8 times the group's sum of
-// activations, so that it ends as sum q x; it is scaled and added in fp32.
-// Nothing is rounded to fewer bits before Y.  (q itself, from
-// v_cvt_off_f32_i4 and a packing, takes 15 operations per 8 weights instead of
-// 9, and the products leave time for 2 operations each.)
+// A weight's integer becomes bf16 exactly, its product with a bf16 activation is
+// exact too, and the matrix cores add a group's products in fp32; the sum is
+// scaled and added in fp32.  Nothing is rounded to fewer bits before Y.
+// The decoding decides how far the products are from the matrix cores' rate, or
+// the weights from memory's.  Two ways:
+//   decode_u8  u = q + 8 as an 8-bit float code (e4m3: the codes 0 .. 15 stand for
+//     0 .. 15 times 2^-9), converted two at a time: 9 operations per 8 weights;
+//     the sum starts from -8 times the group's sum of activations, a product more
+//     per 16 tokens, and ends as sum q x.  All kernels but i4_stage_kernel.
+//   decode_q8  q / 16 from v_cvt_off_f32_i4 and a packing: 15 operations, and no
+//     sum of activations but where there are offsets.  i4_stage_kernel, whose
+//     waves would each form the sums of up to 256 tokens.
 // With A = 16 activation rows and B = 16 weight rows, lane (r = lane % 16, q =
 // lane / 16) holds 8 consecutive k of row r, and of the result weight row r for
 // activation rows 4 q .. 4 q + 3: one scale per lane and tile.
@@ -33,9 +37,9 @@ __device__ __forceinline__ u32x4 load16_any(const void* p) {
   return v;
 }
 
-// q / 16 of eight nibbles q + 8, in bf16, in order: 14 operations.  The odd
+// q / 16 of eight nibbles q + 8, in bf16, in order: 15 operations.  The odd
 // nibbles' word is kept apart, so that the conversions take their bytes from
-// the two words by themselves instead of shifting each (18 operations).
+// the two words by themselves instead of shifting each (19 operations).
 __device__ __forceinline__ bf16x8 decode_q8(uint32_t w) {
   w ^= 0x88888888u;  // two's complement
   uint32_t h = w >> 4;
@@ -99,7 +103,9 @@ __device__ __forceinline__ float against_eights(float m) { return m * -0.125f; }
 // A workgroup holds 16 weight rows and 16 activation rows; its KS waves split
 // k: wave w takes the blocks of 128 columns w, w + KS, ... and the partial
 // tiles are summed in LDS, wave by wave.  Everything is read straight from
-// global memory; activation rows may start at any element.
+// global memory; activation rows may start at any element.  With 64-bit offsets:
+// what the other kernels do not reach comes here (one token of 14336 x 4096: 18.5
+// us, 16 25, 4096 4321: the loads' latency, block after block).
 template <int G, bool OFF>
 __global__ __launch_bounds__(512) void i4_direct_kernel(I4Args a, int n_groups, int ny, int KS) {
   const int L = int(blockIdx.x);
@@ -204,6 +210,8 @@ struct GroupRows {
 // Loads of blocks that are not there are made all the same, from one address:
 // where a load hangs on a branch, the wait for an older one becomes a wait for
 // all.  A last block that is not whole comes at the end, by itself.
+// 16 tokens of 14336 x 4096 take 12.2 us with 64 weight rows, 77 of 1000 x 4100
+// 8.4 with 32: the first loads' latency, then the decoding.
 template <int G, bool OFF, bool S32, int WI, int BJ, int KW, int D>
 __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tiles, int nb_tiles) {
   constexpr int GB = 128 / G;  // groups of a block
@@ -369,13 +377,19 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
 // workgroup, but a block's activations are 256 bytes per token: one 4-byte load
 // of the wave (in the operand's layout it would be four of 16 bytes, most of
 // them for tokens that are not there), put in order by the wave's own corner of
-// LDS.
+// LDS.  One token of 14336 x 4096 takes 8.1 us with 32 weight rows, 3.9 TB/s of
+// weights and scales (a plain read of them 5.6 to 6.6 us with its launch), of
+// 4096 x 14336 7.6 with 16: bound by the one round of loads that a workgroup
+// makes, and the launch.
 template <int G, bool OFF, bool S32, int WI, int NB, int KW, int D>
 __global__ __launch_bounds__(64 * KW) void i4_token_kernel(I4Args a, int nw_tiles) {
   constexpr int GB = 128 / G;       // groups of a block
   constexpr uint32_t kRow = 272;    // a token's 256 bytes, 16 further into the banks than the one before
-  const int wt = int(blockIdx.x);
-  if (wt >= nw_tiles) return;
+  // workgroups are dealt to the XCDs round-robin: each XCD takes a run of tiles, since the scales of 16 rows are 32 bytes
+  // of a group and neighbours on other XCDs would fetch the rest of the line again (one token of 14336 x 4096: 8.4 -> 8.1
+  // us, of 4096 x 14336 8.1 -> 7.6; no gain for the slices, whose time has more to it)
+  const int xcd = int(blockIdx.x) % kXcds;
+  const int wt = xcd * (nw_tiles / kXcds) + min(xcd, nw_tiles % kXcds) + int(blockIdx.x) / kXcds;
   const int64_t row0 = int64_t(wt) * 16 * WI;
   const int lane = int(threadIdx.x) % kWave, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   const int r = lane % 16, q = lane / 16, batch = int(a.batch);
@@ -531,6 +545,8 @@ __global__ __launch_bounds__(64 * KW) void i4_token_kernel(I4Args a, int nw_tile
 // An activation row starts 16 bytes further into the banks than the one before
 // it; lanes of tokens that are not there read the last one's again, into
 // results that are not written.
+// 28672 x 4096 with 16 tokens: 22.2 us, the slices 26.8; 14336 x 4096 with 4: 10.3
+// (the token kernel 8.9).
 // LDS: activations; the waves' sums of two tiles, of the tokens that are there.
 template <int G, bool OFF, bool S32, int KW, int D, int U>
 __global__ __launch_bounds__(64 * KW) void i4_stream_kernel(I4Args a, int n_tiles, uint32_t pitch) {
@@ -834,7 +850,9 @@ __device__ __forceinline__ int w_slot(int chunk, int row) { return chunk ^ (-(ro
 // Few tokens, long rows: as the slices, with everything staged by direct loads
 // into the wave's own ring of D blocks in LDS, so that many blocks are in
 // flight without registers and nothing but the wave's own loads is waited for.
-// A block's weights and activations lie in LDS as in i4_stage_kernel.
+// A block's weights and activations lie in LDS where w_slot and x_slot say.
+// 16 tokens of 4096 x 14336, groups of 64 with offsets: 15.5 us, 33 MB at 2.1
+// TB/s (the wave's rounds of load, wait, decode; the slices take 20.6).
 template <int G, bool OFF, bool S32, int WI, int BJ, int KW, int D>
 __global__ __launch_bounds__(64 * KW) void i4_deep_kernel(I4Args a, int nw_tiles, int nb_tiles) {
   using Groups = StagedGroups<G, S32, WI>;

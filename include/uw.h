@@ -728,9 +728,9 @@ int uw_block_norm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int
  * as q + 8, the even column in the low half; rows start at 16-byte boundaries
  * (d_Q 16-byte aligned, ldq in bytes, a multiple of 16 and at least 16 *
  * ceil(cols / 32)), and whole 16-byte words of a row are read, whatever lies
- * past its last column, and bytes between two rows may be.  Scales and offsets lie group by group: ceil(cols /
- * group) rows of `rows` elements of st (UW_F32 or UW_BF16) with strides lds and
- * ldo.  So the weights of a row-major [rows, cols / 8] int32 matrix of unsigned
+ * past its last column, and bytes between two rows may be.  Scales and offsets
+ * lie group by group: ceil(cols / group) rows of `rows` elements of st (UW_F32
+ * or UW_BF16) with strides lds and ldo.  So the weights of a row-major [rows, cols / 8] int32 matrix of unsigned
  * nibbles u with scales s and zero points z are d_Q as it is, s, and
  * offset = s * (8 - z).
  *
@@ -748,7 +748,7 @@ int uw_block_norm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int
  * A group that holds an infinity or a NaN gets q = 0 and NaN for its scale and
  * offset.  The byte that holds the last column of an odd number has 8 in its
  * other half; nothing is written past it.
- * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (more than 2^35 - 2048 columns),
+ * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (more than 2^33 - 512 columns),
  *         UW_ERR_HIP.
  */
 int uw_i4_quantize(const void* d_X, int64_t rows, int64_t cols, int64_t ldx, int xt, int group, uint8_t* d_Q, int64_t ldq,
@@ -774,8 +774,8 @@ int uw_i4_dequantize(const uint8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq
  *         16-byte boundaries (ldx a multiple of 8) are read fastest.
  *   d_bias  rows fp32 values, or NULL.
  *   d_Y   batch rows of `rows` elements of yt (UW_F32 or UW_BF16), stride ldy.
- * Results depend on the batch and the sizes (the order of the sum), not on
- * anything else.  A token that holds an infinity or a NaN gets no finite value
+ * Results depend on the batch, the sizes, the group and how the operands lie
+ * (which choose the order of the sums), and repeat to the bit.  A token that holds an infinity or a NaN gets no finite value
  * in its row, and the others nothing of it.
  * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (more tiles than a launch holds),
  *         UW_ERR_HIP.
@@ -789,8 +789,10 @@ int uw_i4_gemm(const uint8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, int 
  * [1, uw_i4_gemm_shape_count()) picks the weight and batch rows a workgroup
  * holds and how the operands reach the matrix cores.
  * Errors: as uw_i4_gemm; UW_ERR_INVALID for an unknown shape,
- *         UW_ERR_UNSUPPORTED for a staged shape on activation rows off 16-byte
- *         boundaries (or strides of 2^22 bytes or more).
+ *         UW_ERR_UNSUPPORTED for a shape that does not take the operands:
+ *         activation rows off 16-byte boundaries, more tokens than it is for, or
+ *         rows, strides or scales whose offsets it does not hold (from 2^21
+ *         columns or elements of ldx, 2^22 bytes of ldw, 2^31 bytes of scales on).
  */
 int uw_i4_gemm_shaped(const uint8_t* d_W, int64_t rows, int64_t cols, int64_t ldw, int group, const void* d_scale,
                       int64_t lds, const void* d_offset, int64_t ldo, int st, const uint16_t* d_X, int64_t batch,
