@@ -174,10 +174,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_over(const void* p, int
                                            __builtin_amdgcn_readfirstlane(int(bytes)), 0x00020000);
 }
 
-// 16 bytes; NT: non-temporally, for weights that one workgroup reads.
-template <bool NT>
 __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, int(voff), int(soff), NT ? 2 : 0);
+  return __builtin_amdgcn_raw_buffer_load_b128(r, int(voff), int(soff), 0);
 }
 
 // Scales and offsets of the rows from row0 on (S32: fp32, else bf16), loaded as
@@ -247,7 +245,7 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
   Block ring[D];
   auto load_weights = [&](Block& b, int kb) {
 #pragma unroll
-    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16<false>(wbuf, wvo[t], uint32_t(kb) * 64);
+    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16(wbuf, wvo[t], uint32_t(kb) * 64);
 #pragma unroll
     for (int g = 0; g < GB; ++g) {
       const uint32_t gi = min(uint32_t(kb * GB + g), groups - 1);
@@ -411,7 +409,7 @@ __global__ __launch_bounds__(64 * KW) void i4_token_kernel(I4Args a, int nw_tile
   Block ring[D];
   auto load_weights = [&](Block& b, int kb) {
 #pragma unroll
-    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16<false>(wbuf, wvo[t], uint32_t(kb) * 64);
+    for (int t = 0; t < WI; ++t) b.w[t] = buffer_load16(wbuf, wvo[t], uint32_t(kb) * 64);
 #pragma unroll
     for (int g = 0; g < GB; ++g) {
       const uint32_t gi = min(uint32_t(kb * GB + g), groups - 1);
@@ -597,7 +595,7 @@ __global__ __launch_bounds__(64 * KW) void i4_stream_kernel(I4Args a, int n_tile
     const bool there = left > 0;
     const uint32_t kb = there ? uint32_t(wave + KW * lb) : 0u, tile = there ? uint32_t(lt) : 0u;
     const uint32_t row = there ? uint32_t(min(r, last_row - int(tile) * 16)) : 0u;
-    b.w = buffer_load16<false>(wbuf, row * uint32_t(a.ldw) + (there ? 16 * q : 0), tile * 16 * uint32_t(a.ldw) + kb * 64);
+    b.w = buffer_load16(wbuf, row * uint32_t(a.ldw) + (there ? 16 * q : 0), tile * 16 * uint32_t(a.ldw) + kb * 64);
 #pragma unroll
     for (int g = 0; g < GB; ++g) {
       const uint32_t gi = min(kb * GB + g, groups - 1);
@@ -702,17 +700,15 @@ __global__ __launch_bounds__(64 * KW) void i4_stream_kernel(I4Args a, int n_tile
   }
 }
 
-// 16 bytes of row b of Y from column n on: 16 / SIZE values.  NT: whole lines
-// are written, past the caches.
-template <int SIZE, bool NT>
+// 16 bytes of row b of Y from column n on: 16 / SIZE values.
+template <int SIZE>
 __device__ __forceinline__ void store_row16(const I4Args& a, int64_t b, int64_t n, const uint4& v) {
   if (b >= a.batch || n >= a.rows) return;
   char* y = a.Y + (b * a.ldy + n) * SIZE;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   const int m = int(std::min<int64_t>(16 / SIZE, a.rows - n));
   if (m == 16 / SIZE) {
-    if (NT) __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(y));
-    else __builtin_memcpy(y, w, 16);
+    __builtin_memcpy(y, w, 16);
     return;
   }
 #pragma unroll
@@ -741,7 +737,7 @@ __device__ __forceinline__ float finish(float acc, bool biased, float bias) {
 // rows at a time as the wave's 16 WI columns, so that rows go out in runs of
 // 32 WI bytes (bf16) or twice that.  out: the wave's place in LDS,
 // epilogue_bytes<WI> that nothing else uses any more.
-template <int WI, int BJ, bool YBF16, bool NT>
+template <int WI, int BJ, bool YBF16>
 __device__ __forceinline__ void store_through_lds(const I4Args& a, int64_t n0, int64_t b0, uint32_t out, int lane,
                                                   const f32x4 (&acc)[WI][BJ]) {
   constexpr int kCols = 16 * WI, kSize = YBF16 ? 2 : 4, kPitch = kCols * kSize + 16;
@@ -767,7 +763,7 @@ __device__ __forceinline__ void store_through_lds(const I4Args& a, int64_t n0, i
     for (int c0 = 0; c0 < kChunks; c0 += kWave) {
       const int at = c0 + lane, br = at / kLanes, c = at % kLanes * kPer;
       if (kChunks % kWave == 0 || at < kChunks)
-        store_row16<kSize, NT>(a, b0 + 16 * j + br, n0 + c, ld128(out + uint32_t(br) * kPitch + uint32_t(c) * kSize));
+        store_row16<kSize>(a, b0 + 16 * j + br, n0 + c, ld128(out + uint32_t(br) * kPitch + uint32_t(c) * kSize));
     }
     wave_lds_fence();
   }
@@ -1148,7 +1144,7 @@ __global__ __launch_bounds__(64 * NW * KG, G == 128 && !OFF && KG == 4 && BJ == 
 #pragma unroll
     for (int u = 0; u < LWN; ++u) {
       const uint32_t voff = wvo[u] - (kb == nkb - 1 ? wover : 0u);
-      if (kOwn) raw[u] = buffer_load16<false>(tw.rsrc, voff, uint32_t(kb) * 64);
+      if (kOwn) raw[u] = buffer_load16(tw.rsrc, voff, uint32_t(kb) * 64);
       else if (LW % NW == 0 || u * NW + wave < LW)
         stage_load<false>(tw.rsrc, voff, uint32_t(kb) * 64, ring + uint32_t(i & 1) * kStage + kX + uint32_t(u * NW + wave) * 1024);
     }
@@ -1287,8 +1283,8 @@ __global__ __launch_bounds__(64 * NW * KG, G == 128 && !OFF && KG == 4 && BJ == 
   }
   const int64_t n0 = row0 + 16 * wave * WI, bw0 = b0;
   const uint32_t out = uint32_t((KG - 1) * kPartial + wave * epilogue_bytes<WI>);
-  if (a.yt == UW_F32) store_through_lds<WI, BJ, false, false>(a, n0, bw0, out, lane, acc);
-  else store_through_lds<WI, BJ, true, false>(a, n0, bw0, out, lane, acc);
+  if (a.yt == UW_F32) store_through_lds<WI, BJ, false>(a, n0, bw0, out, lane, acc);
+  else store_through_lds<WI, BJ, true>(a, n0, bw0, out, lane, acc);
 }
 
 // A launch holds fewer than 2^32 threads.  In double: sizes below 2^40 make
