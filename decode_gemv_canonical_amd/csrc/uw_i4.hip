@@ -62,10 +62,10 @@ __device__ __forceinline__ void unpack8(const Raw8& v, float (&f)[8]) {
 // columns, a wave a row at a time with all its loads issued first, so that the
 // scales of a group go out (and come in) for 16 rows side by side: a row at a
 // time they cost as much as the matrix (14336 x 4096, groups of 32 with offsets:
-// 55 us, with these tiles 43; back 53, 34).  Bytes bound the plain forms (groups
-// of 128: 34.4 us from bf16, 4.3 TB/s; 50 from fp32, 5.3; back 29.8, 4.9), the
-// vector ALU the quantisation with offsets (three divisions, and the smallest and
-// largest value, for every 8 values).
+// 55 us, with these tiles 39; back 53, 33).  Bytes bound the plain forms (groups
+// of 128: 33.8 us from bf16, 4.3 TB/s; 49 from fp32, 5.3; back 30, 4.9), the
+// vector ALU the quantisation with offsets (a division, and the smallest and largest
+// value, for every 8 values).
 constexpr int kTileCols = 512;
 
 struct Q4Args {
@@ -174,10 +174,10 @@ __global__ __launch_bounds__(256) void quantize4_kernel(Q4Args a) {
     {
 #pragma clang fp contract(off)
       if (OFF) {
-        s = as_kept(fmaxf(most / 15.f - least / 15.f, kTiny), a.st);
+        s = as_kept(fmaxf(most * (1.f / 15.f) - least * (1.f / 15.f), kTiny), a.st);
         m = as_kept((least * 0.5f + most * 0.5f) + s * 0.5f, a.st);
       } else {
-        s = as_kept(fmaxf(bits_f32(top) / 7.f, kTiny), a.st);
+        s = as_kept(fmaxf(bits_f32(top) * (1.f / 7.f), kTiny), a.st);
       }
     }
     // where s nears the denormal range the residual would leave it: both are scaled up (t is at most 8 s)

@@ -741,10 +741,12 @@ int uw_block_norm(const void* d_X, int64_t batch, int64_t cols, int64_t ldx, int
 /*
  * uw_i4_quantize (device) - rows of xt (UW_F32 or UW_BF16) in 4 bits.  Of a
  * group p, in fp32, each step rounded:
- *   d_offset NULL: s = max(max|p| / 7, 2^-126);
- *   else: s = max(max p / 15 - min p / 15, 2^-126), m = (min p / 2 + max p / 2) + s / 2;
- * s is rounded to st before it is used, and so is m; q is the quotient p / s
- * (or (p - m) / s) rounded to nearest, ties to even, and held to -8 .. 7.
+ *   d_offset NULL: s = max(max|p| * (1 / 7), 2^-126);
+ *   else: s = max(max p * (1 / 15) - min p * (1 / 15), 2^-126),
+ *         m = (min p / 2 + max p / 2) + s / 2;
+ * 1 / 7 and 1 / 15 are rounded to fp32 too; s is rounded to st before it is
+ * used, and so is m; q is the quotient p / s (or (p - m) / s) rounded to
+ * nearest, ties to even, and held to -8 .. 7.
  * A group that holds an infinity or a NaN gets q = 0 and NaN for its scale and
  * offset.  The byte that holds the last column of an odd number has 8 in its
  * other half; nothing is written past it.

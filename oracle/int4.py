@@ -44,10 +44,10 @@ def quantize(p: np.ndarray, group: int, affine: bool, bf16_scales: bool):
             fine = np.isfinite(w).all(axis=1)
             if affine:
                 top, low = w.max(axis=1), w.min(axis=1)
-                s = _kept(np.maximum(top / f(15) - low / f(15), TINY), bf16_scales)
+                s = _kept(np.maximum(top * (f(1) / f(15)) - low * (f(1) / f(15)), TINY), bf16_scales)
                 m = _kept((low * f(0.5) + top * f(0.5)) + s * f(0.5), bf16_scales)
             else:
-                s = _kept(np.maximum(np.abs(w).max(axis=1) / f(7), TINY), bf16_scales)
+                s = _kept(np.maximum(np.abs(w).max(axis=1) * (f(1) / f(7)), TINY), bf16_scales)
                 m = np.zeros_like(s)
             t = (w - m[:, None]).astype(np.float32) if affine else w
             k = np.clip(np.rint((t / s[:, None]).astype(np.float32)), -8, 7)
