@@ -396,7 +396,7 @@ bool shape_ok(const I4Args& a, int group, int shape) {
 // x 64..28672 x 64..14336, all groups, forms and types of scales, half of them
 // with rows of X off 16 bytes, each on 3 to 8 rotated operand sets.  Only their
 // order counts: the times themselves are up to a quarter off.  On those sizes the
-// choice takes 1.03 of the best shape's time in the mean, 95 of 100 under 1.18;
+// choice takes 1.03 of the best shape's time in the mean, 95 of 100 under 1.16;
 // without any one of the shapes the best would be 0.3 to 4 percent slower in the
 // mean and up to 2.5 times in single sizes.
 float expected_us(const I4Shape& s, const I4Args& a, int group, bool aligned) {
