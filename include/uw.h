@@ -777,8 +777,12 @@ int uw_i4_dequantize(const uint8_t* d_Q, int64_t rows, int64_t cols, int64_t ldq
  *   d_bias  rows fp32 values, or NULL.
  *   d_Y   batch rows of `rows` elements of yt (UW_F32 or UW_BF16), stride ldy.
  * Results depend on the batch, the sizes, the group and how the operands lie
- * (which choose the order of the sums), and repeat to the bit.  A token that holds an infinity or a NaN gets no finite value
- * in its row, and the others nothing of it.
+ * (which choose the order of the sums), and repeat to the bit.  A token that holds
+ * an infinity or a NaN gets no finite value in its row, and the others nothing of
+ * it.  A finite token gets finite values, where the results are in the range of
+ * fp32, as long as its magnitudes in any one group add up to less than 2^129;
+ * above that the sums of a group may pass the range.  Results under 2^-115 lose
+ * the bits below 2^-138.
  * Errors: UW_ERR_INVALID, UW_ERR_UNSUPPORTED (more tiles than a launch holds),
  *         UW_ERR_HIP.
  */

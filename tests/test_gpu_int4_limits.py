@@ -1,0 +1,85 @@
+"""The 4-bit product at the ends of its operands' range: the largest finite tokens.
+
+Tolerance: that of test_gpu_int4.py for any values, 2 u (2 cols + groups + 20) of the mass.  Its count of additions holds
+at any magnitude, as long as no sum passes the fp32 range: the terms and their sums are the same up to a power of two.
+"""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import int4 as o4
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import decode_gemv_canonical_amd as uw  # noqa: E402
+from tests.test_gpu_int4 import SHAPES, Weights  # noqa: E402
+from tests.test_gpu_int8 import DEV, U, f64, inside  # noqa: E402
+
+LARGEST = (2 - 2.0 ** -7) * 2.0 ** 127  # of bf16
+FEW = range(1, 10)  # the shapes that hold up to 16 tokens: direct, token, stream, slices, deep slices
+
+
+def run(w, X, shape):
+    """The product as fp32 values checked against the oracle; False where the shape is not for so many tokens."""
+    b = X.shape[0]
+    Y, y_ok = inside(b, w.rows, torch.float32)
+    try:
+        w.run(X, Y, shape)
+    except uw.UwError as e:
+        assert e.status == uw.UW_ERR_UNSUPPORTED and shape in (2, 3, 4) and b > 4
+        return False
+    ref, mass = w.ref(f64(X))
+    got = f64(Y)
+    what = f"shape {shape} b={b} group={w.group} affine={w.m is not None}"
+    assert (np.abs(ref) < 2.0 ** 127).all(), "the results themselves are in range"
+    assert np.isfinite(got).all(), f"{what}: tokens {np.argwhere(~np.isfinite(got).all(axis=1)).ravel().tolist()} are not finite"
+    n = 2 * w.cols + o4.groups(w.cols, w.group) + 20
+    lim = 2 * U * n * mass + 2 * U * np.abs(ref)
+    assert (np.abs(got - ref) <= lim).all(), what
+    assert y_ok(), what + ": wrote outside Y"
+    return True
+
+
+def small(w, by):
+    """Scales and offsets times `by`, a power of two."""
+    w.scale.mul_(by)
+    w.s = f64(w.scale)
+    if w.offset is not None:
+        w.offset.mul_(by)
+        w.m = f64(w.offset)
+    return w
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("group,affine", list(itertools.product((32, 64, 128), (False, True))))
+def test_large_finite_tokens(group, affine, shape):
+    """Tokens whose magnitudes add up to just under 2^129 over a group."""
+    cols, ran = 520, False
+    w = small(Weights(48, cols, group, affine, "bf16", 3), 2.0 ** -8)
+    kinds = torch.zeros(5, cols)
+    kinds[0] = torch.randn(cols, generator=torch.Generator().manual_seed(4))
+    kinds[1] = 1.875 * 2.0 ** 128 / group
+    kinds[2, ::group], kinds[2, 3::group] = LARGEST, -LARGEST
+    kinds[3, ::group], kinds[3, 5::group] = LARGEST, LARGEST
+    kinds[4, 517] = -LARGEST
+    for b in (1, 4, 16, 40):
+        X, _ = inside(b, cols, torch.bfloat16, 8, 8)  # rows on 16-byte boundaries
+        X.copy_(kinds[(torch.arange(b) + 1) % 5].bfloat16())
+        ran |= run(w, X, shape)
+    assert ran
+
+
+@pytest.mark.parametrize("shape", FEW)
+@pytest.mark.parametrize("group,affine", list(itertools.product((32, 64, 128), (False, True))))
+def test_largest_finite_tokens_of_the_shapes_for_few(group, affine, shape):
+    """No finite token leaves the range in the sums of these."""
+    w = small(Weights(48, 520, group, affine, "f32", 5), 2.0 ** -16)
+    for b in (2, 4):
+        X = torch.full((b, 520), LARGEST, device=DEV).bfloat16()
+        X[1] = -X[1]
+        assert run(w, X, shape) and (b != 4 or run(w, X, 0))
