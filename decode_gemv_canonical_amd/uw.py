@@ -796,11 +796,21 @@ def i4_rows(rows: int, cols: int, device="cuda"):
 class Int4Matrix:
     """A weight matrix in 4 bits with a scale (and an offset, where the form is
     affine) per group of columns, on the current CUDA device.  An output that is
-    not passed in is allocated under `stream`."""
+    not passed in is allocated under `stream`.  cols says how many columns there
+    are where their number is odd; tokens and outputs of another width raise
+    ValueError."""
 
     def __init__(self, q, scale, offset=None, cols: int | None = None, group: int = 128):
         self.q, self.scale, self.offset, self.group = q, scale, offset, group
         self.rows, self.cols = q.shape[0], 2 * q.shape[1] if cols is None else cols
+
+    def _want_tokens(self, x, dims: int, name: str) -> None:
+        # uw_i4_gemm takes the width from its tokens; of an odd width and the next even one the packed rows are alike
+        import torch
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if x.dim() != dims or x.shape[-1] != self.cols:
+            raise ValueError(f"{name} must be {dims}-D with {self.cols} columns, got shape {tuple(x.shape)}")
 
     @classmethod
     def from_weights(cls, W, group: int = 128, affine: bool = False, scale_dtype=None) -> "Int4Matrix":
@@ -823,11 +833,16 @@ class Int4Matrix:
         import torch
         if out is None:
             out = _output((self.rows, self.cols), out_dtype or torch.bfloat16, self.q.device, stream)
+        elif not isinstance(out, torch.Tensor):
+            raise TypeError("out must be a tensor")
+        elif out.shape != (self.rows, self.cols):
+            raise ValueError(f"out must have shape ({self.rows}, {self.cols}), got {tuple(out.shape)}")
         uw_i4_dequantize(self.q, self.scale, out, self.offset, self.group, stream)
         return out
 
     def gemm(self, X, Y=None, bias=None, out_dtype=None, stream=None):
         import torch
+        self._want_tokens(X, 2, "X")
         if Y is None:
             Y = _output((X.shape[0], self.rows), out_dtype or torch.float32, X.device, stream)
         uw_i4_gemm(self.q, self.scale, X, Y, self.offset, self.group, bias, stream)
@@ -836,6 +851,7 @@ class Int4Matrix:
     def gemv(self, x, y=None, bias=None, out_dtype=None, stream=None):
         """One token: x of cols elements, y of rows elements."""
         import torch
+        self._want_tokens(x, 1, "x")
         if y is None:
             y = _output((self.rows,), out_dtype or torch.float32, x.device, stream)
         uw_i4_gemm(self.q, self.scale, x.unsqueeze(0), y.unsqueeze(0), self.offset, self.group, bias, stream)
