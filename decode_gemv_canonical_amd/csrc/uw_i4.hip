@@ -342,37 +342,38 @@ bool offsets_ok(const I4Args& a, int group) {
 // 16-byte chunks of the activations.
 bool aligned_ok(const I4Args& a) { return reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % 8 == 0; }
 
-// Shapes: weight and batch rows of a workgroup's tile (at groups of 128), and
-// the kernel (uw_i4_gemm.h).  per_cu, start, alone, shared, lead and loose are
-// for expected_us below.
+// Shapes: weight and batch rows of a workgroup's tile (at groups of 128), the
+// kernel (uw_i4_gemm.h) and the threads of a workgroup (of kDirect at most).
+// per_cu, start, alone, shared, lead and loose are for expected_us below.
 enum Kind { kDirect, kToken, kStream, kSlice, kDeep, kStage, kLoose };
 struct I4Shape {
   int bw, bb;
   Kind kind;
+  int threads;
   int per_cu;
   float start, alone, shared, lead, loose;
 };
 constexpr I4Shape kShapeList[] = {
-    {0, 0, kDirect, 1, 0, 0, 0, 0, 0},  // 0: the choice below
-    {16, 16, kDirect, 1, 0, 0, 0, 0, 0},
-    {32, 4, kToken, 1, 1.07f, 0.0718f, 0.0008f, 0.0062f, 0.0079f},
-    {16, 4, kToken, 2, 1.18f, 0.0291f, 0.0456f, 0.0112f, 0.0125f},
-    {16, 16, kStream, 4, 2.89f, 0.0192f, 0.0353f, 0.0066f, 0.0095f},
-    {64, 16, kSlice, 1, 1.84f, 0.1460f, 0.0006f, 0.0047f, 0.0109f},
-    {16, 16, kSlice, 1, 1.78f, 0.0539f, 0, 0.0040f, 0.0068f},
-    {32, 16, kSlice, 1, 1.65f, 0.0865f, 0.0508f, 0.0035f, 0.0092f},
-    {16, 16, kDeep, 1, 1.63f, 0.0711f, 0.0607f, 0.0007f, 0},
-    {32, 16, kDeep, 1, 1.73f, 0.0952f, 0.0571f, 0.0010f, 0},
-    {64, 16, kStage, 1, 2.21f, 0.2259f, 0.0001f, 0.0007f, 0},  // 4 groups of waves
-    {64, 32, kStage, 1, 2.76f, 0.2677f, 0.2120f, 0.0009f, 0},  // 4
-    {64, 64, kStage, 1, 3.65f, 0.3461f, 0.2914f, 0.0013f, 0},  // 4
-    {128, 64, kStage, 1, 3.87f, 0.5498f, 0.4785f, 0.0014f, 0},  // 3
-    {128, 128, kStage, 1, 5.22f, 0.8902f, 0.6110f, 0.0022f, 0},  // 2
-    {256, 256, kStage, 1, 6.47f, 2.7515f, 2.7968f, 0.0013f, 0},
-    {64, 32, kLoose, 1, 2.23f, 0.3020f, 0.2638f, 0.0004f, 0.0024f},  // 4
-    {64, 64, kLoose, 1, 3.33f, 0.4104f, 0.2865f, 0.0007f, 0.0036f},  // 4
-    {128, 128, kLoose, 1, 5.50f, 1.0149f, 0.3523f, 0.0015f, 0.0049f},  // 2
-    {256, 128, kLoose, 1, 4.43f, 1.6052f, 1.4308f, 0.0029f, 0.0065f},
+    {0, 0, kDirect, 0, 1, 0, 0, 0, 0, 0},  // 0: the choice below
+    {16, 16, kDirect, 512, 1, 0, 0, 0, 0, 0},
+    {32, 4, kToken, 512, 1, 1.07f, 0.0718f, 0.0008f, 0.0062f, 0.0079f},
+    {16, 4, kToken, 512, 2, 1.18f, 0.0291f, 0.0456f, 0.0112f, 0.0125f},
+    {16, 16, kStream, 512, 4, 2.89f, 0.0192f, 0.0353f, 0.0066f, 0.0095f},
+    {64, 16, kSlice, 512, 1, 1.84f, 0.1460f, 0.0006f, 0.0047f, 0.0109f},
+    {16, 16, kSlice, 1024, 1, 1.78f, 0.0539f, 0, 0.0040f, 0.0068f},
+    {32, 16, kSlice, 1024, 1, 1.65f, 0.0865f, 0.0508f, 0.0035f, 0.0092f},
+    {16, 16, kDeep, 512, 1, 1.63f, 0.0711f, 0.0607f, 0.0007f, 0},
+    {32, 16, kDeep, 512, 1, 1.73f, 0.0952f, 0.0571f, 0.0010f, 0},
+    {64, 16, kStage, 1024, 1, 2.21f, 0.2259f, 0.0001f, 0.0007f, 0},  // 4 groups of waves
+    {64, 32, kStage, 1024, 1, 2.76f, 0.2677f, 0.2120f, 0.0009f, 0},  // 4
+    {64, 64, kStage, 1024, 1, 3.65f, 0.3461f, 0.2914f, 0.0013f, 0},  // 4
+    {128, 64, kStage, 768, 1, 3.87f, 0.5498f, 0.4785f, 0.0014f, 0},  // 3
+    {128, 128, kStage, 512, 1, 5.22f, 0.8902f, 0.6110f, 0.0022f, 0},  // 2
+    {256, 256, kStage, 512, 1, 6.47f, 2.7515f, 2.7968f, 0.0013f, 0},
+    {64, 32, kLoose, 1024, 1, 2.23f, 0.3020f, 0.2638f, 0.0004f, 0.0024f},  // 4
+    {64, 64, kLoose, 1024, 1, 3.33f, 0.4104f, 0.2865f, 0.0007f, 0.0036f},  // 4
+    {128, 128, kLoose, 512, 1, 5.50f, 1.0149f, 0.3523f, 0.0015f, 0.0049f},  // 2
+    {256, 128, kLoose, 512, 1, 4.43f, 1.6052f, 1.4308f, 0.0029f, 0.0065f},
 };
 constexpr int kShapes = int(sizeof(kShapeList) / sizeof(kShapeList[0]));
 
@@ -383,6 +384,21 @@ bool shape_ok(const I4Args& a, int group, int shape) {
   if (kind == kToken) return a.batch <= 4;
   if (kind == kStream) return stream_ok(a, 8);
   return kind == kDeep || kind == kStage ? aligned_ok(a) : true;
+}
+
+// Rows and tokens of a shape's tile.
+int64_t tile_rows(const I4Shape& s, int group) { return s.kind == kSlice && s.bw == 64 && group == 32 ? 32 : s.bw; }
+int64_t tile_tokens(const I4Shape& s, const I4Args& a, int group) { return s.bb == 256 && (a.offset || group == 32) ? 192 : s.bb; }
+
+// Whether a launch holds the shape's workgroups, as their launchers check it
+// (check_launch; the stream's workgroups take many tiles each).  What is past it,
+// from 2^27 rows on, is left to shapes of larger or fewer tiles, and to the direct
+// kernel.
+bool launch_holds(const I4Shape& s, const I4Args& a, int group) {
+  if (s.kind == kStream) return true;
+  const double nw = double((a.rows + tile_rows(s, group) - 1) / tile_rows(s, group) + kXcds);
+  const double nb = double((a.batch + tile_tokens(s, a, group) - 1) / tile_tokens(s, a, group));
+  return (nw * nb + kXcds) * s.threads < 4294967296.0;
 }
 
 // What a product takes on a shape, in us: 1.6 for the launch, then rounds of
@@ -401,8 +417,7 @@ bool shape_ok(const I4Args& a, int group, int shape) {
 // mean and up to 2.5 times in single sizes.
 float expected_us(const I4Shape& s, const I4Args& a, int group, bool aligned) {
   const float blocks = float((a.cols + 127) / 128);
-  const int64_t bw = s.kind == kSlice && s.bw == 64 && group == 32 ? 32 : s.bw;
-  const int64_t bb = s.bb == 256 && (a.offset || group == 32) ? 192 : s.bb;
+  const int64_t bw = tile_rows(s, group), bb = tile_tokens(s, a, group);
   const float n = float((a.rows + bw - 1) / bw) * float((a.batch + bb - 1) / bb) / kCus;
   const float rounds = std::ceil(n / float(s.per_cu));
   const float held = n < 1.f ? n : 0.5f * (n + std::ceil(n));
@@ -418,7 +433,7 @@ int pick_shape(const I4Args& a, int group) {
   int shape = 1;
   float best = 0.f;
   for (int i = 2; i < kShapes; ++i) {
-    if (!shape_ok(a, group, i)) continue;
+    if (!shape_ok(a, group, i) || !launch_holds(kShapeList[i], a, group)) continue;
     // one shape for up to 4 tokens is always among the first two kinds, and the others' times are fitted to more tokens
     // (with all of them 1.05 of the best in the mean there, the worst 2.6; so 1.03 and 1.4)
     if (a.batch <= 4 && kShapeList[i].kind != kToken && kShapeList[i].kind != kStream) continue;

@@ -1,4 +1,4 @@
-"""The 4-bit product at the ends of its operands' range: the largest finite tokens.
+"""The 4-bit product at the ends of its operands' range: the largest finite tokens, more rows than most shapes hold.
 
 Tolerance: that of test_gpu_int4.py for any values, 2 u (2 cols + groups + 20) of the mass.  Its count of additions holds
 at any magnitude, as long as no sum passes the fp32 range: the terms and their sums are the same up to a power of two.
@@ -83,3 +83,23 @@ def test_largest_finite_tokens_of_the_shapes_for_few(group, affine, shape):
         X = torch.full((b, 520), LARGEST, device=DEV).bfloat16()
         X[1] = -X[1]
         assert run(w, X, shape) and (b != 4 or run(w, X, 0))
+
+
+@pytest.mark.parametrize("group", [32, 128])
+def test_more_rows_than_a_launch_of_the_token_shapes_holds(group):
+    """2^28 rows: a shape that holds them is taken.  Whole numbers and powers of two: exact in fp32, whatever the order."""
+    rows, cols = 1 << 28, 32
+    g = torch.Generator(device=DEV).manual_seed(7)
+    W = torch.randint(0, 256, (rows, 16), generator=g, dtype=torch.uint8, device=DEV)
+    scale = (2.0 ** torch.randint(-1, 2, (1, rows), generator=g, device=DEV)).bfloat16()
+    X = torch.randint(-4, 5, (3, cols), generator=g, device=DEV).bfloat16()
+    at = torch.cat([torch.arange(64), torch.randint(0, rows - 5000, (2000,), generator=torch.Generator().manual_seed(1)),
+                    torch.arange(rows - 5064, rows - 5000)])
+    for n, b in ((rows, 1), (rows - 4096, 1), (rows, 3)):
+        rows_at = torch.cat([at, torch.arange(n - 64, n)]).to(DEV)
+        q, s = o4.unpack(W[rows_at].cpu().numpy(), cols), f64(scale[:, rows_at])
+        Y = torch.full((b, n), float("nan"), device=DEV)
+        uw.uw_i4_gemm(W[:n], scale[:, :n], X[:b], Y, group=group)
+        assert np.array_equal(f64(Y[:, rows_at]), o4.gemm(q, s, None, group, f64(X[:b]))[0]), (n, b)
+        assert not torch.isnan(Y).any()
+        del Y
