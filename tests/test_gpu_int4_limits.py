@@ -1,4 +1,5 @@
-"""The 4-bit product at the ends of its operands' range: the largest finite tokens, more rows than most shapes hold.
+"""The 4-bit product at the ends of its operands' range: the largest finite tokens, more rows than most shapes hold;
+and which shapes refuse which operands.
 
 Tolerance: that of test_gpu_int4.py for any values, 2 u (2 cols + groups + 20) of the mass.  Its count of additions holds
 at any magnitude, as long as no sum passes the fp32 range: the terms and their sums are the same up to a power of two.
@@ -17,7 +18,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import decode_gemv_canonical_amd as uw  # noqa: E402
-from tests.test_gpu_int4 import SHAPES, Weights  # noqa: E402
+from tests.test_gpu_int4 import SHAPES, WIDTHS, Weights, tokens  # noqa: E402
 from tests.test_gpu_int8 import DEV, U, f64, inside  # noqa: E402
 
 LARGEST = (2 - 2.0 ** -7) * 2.0 ** 127  # of bf16
@@ -31,7 +32,7 @@ def run(w, X, shape):
     try:
         w.run(X, Y, shape)
     except uw.UwError as e:
-        assert e.status == uw.UW_ERR_UNSUPPORTED and shape in (2, 3, 4) and b > 4
+        assert e.status == uw.UW_ERR_UNSUPPORTED and refuses(shape, b, w.cols, X)
         return False
     ref, mass = w.ref(f64(X))
     got = f64(Y)
@@ -103,3 +104,54 @@ def test_more_rows_than_a_launch_of_the_token_shapes_holds(group):
         assert np.array_equal(f64(Y[:, rows_at]), o4.gemm(q, s, None, group, f64(X[:b]))[0]), (n, b)
         assert not torch.isnan(Y).any()
         del Y
+
+
+def refuses(shape, b, cols, X):
+    """Whether a shape is not for these tokens (at strides and scales within its offsets)."""
+    if shape in (2, 3):  # the token kernel
+        return b > 4
+    if shape == 4:  # the stream: up to 16 tokens that fit in 160 KB of LDS, with two parts of each of 8 waves
+        return b > 16 or b * ((cols + 127) // 128 * 256 + 16) + 2 * 8 * ((b + 3) // 4) * 256 > 160 * 1024
+    if 8 <= shape <= 15:  # rows in whole 16-byte chunks: deep slices and staged tiles
+        return X.data_ptr() % 16 != 0 or (b > 1 and X.stride(0) % 8 != 0)
+    return False  # the choice, direct, slices, staged tiles through registers
+
+
+def check_refusals(b, rows, cols, group, affine, pad=0, shift=0):
+    """Every shape against that rule; those that take the operands give the exact result (whole numbers)."""
+    w = Weights(rows, cols, group, affine, "bf16", cols, True)
+    X = tokens(b, cols, cols + 1, True, pad, shift)
+    want = w.ref(f64(X))[0]
+    for shape in SHAPES:
+        what = f"shape {shape}: {b} x {rows} x {cols}, stride {X.stride(0)}, address % 16 = {X.data_ptr() % 16}"
+        Y = torch.full((b, rows), float("nan"), device=DEV)
+        try:
+            w.run(X, Y, shape)
+        except uw.UwError as e:
+            assert e.status == uw.UW_ERR_UNSUPPORTED and refuses(shape, b, cols, X), f"{what}: refused"
+            continue
+        assert not refuses(shape, b, cols, X), f"{what}: not refused"
+        assert np.array_equal(f64(Y), want), what
+
+
+@pytest.mark.parametrize("cols", WIDTHS)
+def test_shapes_that_refuse_by_width(cols):
+    for (group, affine), b, rows in zip(itertools.product((32, 64, 128), (False, True)), (1, 2, 16, 17, 5, 3), (1, 15, 16, 33, 64, 70)):
+        check_refusals(b, rows, cols, group, affine)
+        check_refusals(b, rows, cols, group, affine, pad=-cols % 8)
+
+
+@pytest.mark.parametrize("b", [1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 100, 128, 129, 200, 256, 257])
+def test_shapes_that_refuse_by_batch(b):
+    check_refusals(b, 130, 520, 32, True)
+
+
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (8, 8), (1, 0), (3, 1), (4, 2), (0, 5), (16, 7)])
+def test_shapes_that_refuse_by_alignment(pad, shift):
+    for b, rows, cols, group in ((1, 40, 136, 64), (5, 100, 1001, 32), (33, 70, 300, 128), (150, 64, 129, 64)):
+        check_refusals(b, rows, cols, group, True, pad, shift)
+
+
+@pytest.mark.parametrize("b,cols", [(1, 65536), (2, 40960), (4, 14336), (5, 14336), (6, 14336), (11, 6656), (12, 6656), (16, 4096), (16, 4352), (16, 4608)])
+def test_shapes_that_refuse_by_the_stream_s_memory(b, cols):
+    check_refusals(b, 33, cols, 128, False)
