@@ -75,6 +75,35 @@ def test_large_finite_tokens(group, affine, shape):
     assert ran
 
 
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("group,affine", list(itertools.product((32, 64, 128), (False, True))))
+def test_tiny_tokens(group, affine, shape):
+    """Tokens down to 2^-126, whose sums are denormal in 2^-11 of their value.  There a step is 2^-149 whatever the value: each
+    of the 2 cols + groups + 20 additions may lose it, times 2^11 and a scale below 1."""
+    cols, ran = 520, False
+    w = Weights(48, cols, group, affine, "f32", 3)
+    assert w.s.max() < 1 and (w.m is None or np.abs(w.m).max() < 1)
+    n = 2 * cols + o4.groups(cols, group) + 20
+    for b, power in itertools.product((3, 16, 40), (-100, -112, -118, -124)):
+        X, _ = inside(b, cols, torch.bfloat16, 8, 8)
+        sign = torch.randn(b, cols, generator=torch.Generator().manual_seed(b)).sign()
+        X.copy_((sign * (1 + torch.rand(b, cols, generator=torch.Generator().manual_seed(b))) * 2.0 ** power).bfloat16())
+        Y, y_ok = inside(b, w.rows, torch.float32)
+        try:
+            w.run(X, Y, shape)
+        except uw.UwError as e:
+            assert e.status == uw.UW_ERR_UNSUPPORTED and refuses(shape, b, cols, X)
+            continue
+        ran = True
+        ref, mass = w.ref(f64(X))
+        got = f64(Y)
+        over = np.abs(got - ref) > 2 * U * n * mass + 2 * U * np.abs(ref) + n * 2.0 ** -138
+        assert not over.any() and y_ok(), f"shape {shape} b={b} 2^{power}: {over.sum()} of {over.size} off"
+        # not merely zero: the values stand well above that
+        assert power < -112 or (got != 0).all()
+    assert ran
+
+
 @pytest.mark.parametrize("shape", FEW)
 @pytest.mark.parametrize("group,affine", list(itertools.product((32, 64, 128), (False, True))))
 def test_largest_finite_tokens_of_the_shapes_for_few(group, affine, shape):
