@@ -62,10 +62,11 @@ __device__ __forceinline__ void unpack8(const Raw8& v, float (&f)[8]) {
 // columns, a wave a row at a time with all its loads issued first, so that the
 // scales of a group go out (and come in) for 16 rows side by side: a row at a
 // time they cost as much as the matrix (14336 x 4096, groups of 32 with offsets:
-// 55 us, with these tiles 39; back 53, 33).  Bytes bound the plain forms (groups
-// of 128: 33.8 us from bf16, 4.3 TB/s; 49 from fp32, 5.3; back 30, 4.9), the
-// vector ALU the quantisation with offsets (a division, and the smallest and largest
-// value, for every 8 values).
+// 55 us, with these tiles 38.4; back 53, 34.2).  Bytes bound the plain forms (groups
+// of 128: 33.6 us from bf16, 4.4 TB/s; 50 from fp32, 5.3; back 30.4, 4.9, or 23.6
+// right behind the quantisation, while the caches hold the integers), the vector
+// ALU the quantisation with offsets (the quotients, and the smallest and largest
+// value, of every 8 values).
 constexpr int kTileCols = 512;
 
 struct Q4Args {
@@ -180,7 +181,8 @@ __global__ __launch_bounds__(256) void quantize4_kernel(Q4Args a) {
         s = as_kept(fmaxf(bits_f32(top) * (1.f / 7.f), kTiny), a.st);
       }
     }
-    // where s nears the denormal range the residual would leave it: both are scaled up (t is at most 8 s)
+    // where s nears the denormal range the residual would leave it: both are scaled up (a t that this takes past the fp32
+    // range is many s, and held as an infinite one is)
     const float up = s < 0x1p-60f ? 0x1p64f : 1.f;
     const float su = s * up, inv = 1.f / su;
     uint32_t w = 0u - kNibbleBase * 0x11111111u;
@@ -408,13 +410,17 @@ bool launch_holds(const I4Shape& s, const I4Args& a, int group) {
 // its own loads; a compute unit needs `shared` per block and workgroup it holds;
 // and the operands' bytes come at 5.4 TB/s.  The three limits of the loop add as
 // fourth powers (the largest rules, a near second counts).
-// The constants were fitted to the shapes' times on 3000 sizes drawn over 1..4096
-// x 64..28672 x 64..14336, all groups, forms and types of scales, half of them
+// The constants were fitted to the shapes' times on 3000 sizes over 1..4096 x
+// 64..28672 x 64..14336 (three of ten with the rows and columns of eight usual
+// matrices, the others drawn), all groups, forms and types of scales, half of them
 // with rows of X off 16 bytes, each on 3 to 8 rotated operand sets.  Only their
-// order counts: the times themselves are up to a quarter off.  On those sizes the
-// choice takes 1.03 of the best shape's time in the mean, 95 of 100 under 1.16;
-// without any one of the shapes the best would be 0.3 to 4 percent slower in the
-// mean and up to 2.5 times in single sizes.
+// order counts: the times themselves are up to a quarter off.  On 2590 other sizes,
+// all drawn, the choice takes 1.03 of the best shape's time in the mean, 95 of 100
+// under 1.21, the worst 2.3 (on those of the fit 1.03, 1.17 and 2.8); without any
+// one of the shapes the best would be up to 2.7 percent slower in the mean, and 1.1
+// to 2.6 times in single sizes.  The stream's workgroups stay and take tile after
+// tile, which `rounds` says badly: 4 tokens of 14336 x 4096 go to it (10.3 us, the
+// token kernel 8.9), 16 of 28672 x 4096 not (slices 26.5, the stream 22.4).
 float expected_us(const I4Shape& s, const I4Args& a, int group, bool aligned) {
   const float blocks = float((a.cols + 127) / 128);
   const int64_t bw = tile_rows(s, group), bb = tile_tokens(s, a, group);
@@ -437,7 +443,9 @@ int pick_shape(const I4Args& a, int group) {
     // one shape for up to 4 tokens is always among the first two kinds, and the others' times are fitted to more tokens
     // (with all of them 1.05 of the best in the mean there, the worst 2.6; so 1.03 and 1.4)
     if (a.batch <= 4 && kShapeList[i].kind != kToken && kShapeList[i].kind != kStream) continue;
-    // a slice for each 16 tokens reads the weights as often: not past a few of them
+    // a slice for each 16 tokens reads the weights as often: not past a few of them.  (Where rows are few and off 16 bytes
+    // this loses: 81 to 256 such tokens take 1.12 of the best shape's time in the mean, up to 2.3; of all sizes 95 of 100
+    // would be under 1.18 without it, the worst 2.1)
     if (kShapeList[i].kind == kSlice && a.batch > 80) continue;
     const float us = expected_us(kShapeList[i], a, group, aligned);
     if (shape == 1 || us < best) {

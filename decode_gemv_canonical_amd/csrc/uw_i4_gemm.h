@@ -133,7 +133,7 @@ __device__ __forceinline__ void finish4(const I4Args& a, int64_t n, f32x4& v) {
 // tiles are summed in LDS, wave by wave.  Everything is read straight from
 // global memory; activation rows may start at any element.  With 64-bit offsets:
 // what the other kernels do not reach comes here (one token of 14336 x 4096: 18.5
-// us, 16 25, 4096 4321: the loads' latency, block after block).
+// us, 16 24.7, 4096 4312: the loads' latency, block after block).
 template <int G, bool OFF>
 __global__ __launch_bounds__(512) void i4_direct_kernel(I4Args a, int n_groups, int ny, int KS) {
   const int L = int(blockIdx.x);
@@ -236,8 +236,8 @@ struct GroupRows {
 // Loads of blocks that are not there are made all the same, from one address:
 // where a load hangs on a branch, the wait for an older one becomes a wait for
 // all.  A last block that is not whole comes at the end, by itself.
-// 16 tokens of 14336 x 4096 take 12.2 us with 64 weight rows, 77 of 1000 x 4100
-// 8.4 with 32: the first loads' latency, then the decoding.
+// 16 tokens of 14336 x 4096 take 12.4 us with 64 weight rows, 77 of 1000 x 4100
+// 8.3 with 32: the first loads' latency, then the decoding.
 template <int G, bool OFF, bool S32, int WI, int BJ, int KW, int D>
 __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tiles, int nb_tiles) {
   constexpr int GB = 128 / G;  // groups of a block
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(64 * KW) void i4_slice_kernel(I4Args a, int nw_tile
 // workgroup, but a block's activations are 256 bytes per token: one 4-byte load
 // of the wave (in the operand's layout it would be four of 16 bytes, most of
 // them for tokens that are not there), put in order by the wave's own corner of
-// LDS.  One token of 14336 x 4096 takes 8.1 us with 32 weight rows, 3.9 TB/s of
+// LDS.  One token of 14336 x 4096 takes 8.0 us with 32 weight rows, 3.8 TB/s of
 // weights and scales (a plain read of them 5.6 to 6.6 us with its launch), of
 // 4096 x 14336 7.6 with 16: bound by the one round of loads that a workgroup
 // makes, and the launch.
@@ -563,8 +563,8 @@ __global__ __launch_bounds__(64 * KW) void i4_token_kernel(I4Args a, int nw_tile
 // An activation row starts 16 bytes further into the banks than the one before
 // it; lanes of tokens that are not there read the last one's again, into
 // results that are not written.
-// 28672 x 4096 with 16 tokens: 22.2 us, the slices 26.8; 14336 x 4096 with 4: 10.3
-// (the token kernel 8.9).
+// 28672 x 4096 with 16 tokens, groups of 64 with offsets: 22.4 us, the slices 26.5;
+// 14336 x 4096 with 4 tokens: 10.3 (the token kernel 8.9).
 // LDS: activations; the waves' sums of two tiles, of the tokens that are there.
 template <int G, bool OFF, bool S32, int KW, int D, int U>
 __global__ __launch_bounds__(64 * KW) void i4_stream_kernel(I4Args a, int n_tiles, uint32_t pitch) {
@@ -804,7 +804,7 @@ __device__ __forceinline__ u32x4 tail_mask8(int left) {
 // row's value on (bf16 values need not start at a word).
 template <int G, bool S32, int WI>
 struct StagedGroups {
-  static constexpr int GB = 128 / G, kLanes = 16 * WI, kLoads = (GB * kLanes + 63) / 64, kBytes = GB * kLanes * 4;
+  static constexpr int GB = 128 / G, kLanes = 16 * WI, kLoads = (GB * kLanes + 63) / 64;
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t start, step;  // bytes to row0's value of group 0, and between groups
   uint32_t groups, rows;
@@ -856,8 +856,10 @@ __device__ __forceinline__ int w_slot(int chunk, int row) { return chunk ^ (-(ro
 // into the wave's own ring of D blocks in LDS, so that many blocks are in
 // flight without registers and nothing but the wave's own loads is waited for.
 // A block's weights and activations lie in LDS where w_slot and x_slot say.
-// 16 tokens of 4096 x 14336, groups of 64 with offsets: 15.5 us, 33 MB at 2.1
-// TB/s (the wave's rounds of load, wait, decode; the slices take 20.6).
+// 16 tokens of 4096 x 14336, groups of 64 with offsets: 15.5 us (the slices take
+// 20.3), 33 MB of weights at 2.1 TB/s.  Each of the 256 workgroups of 16 weight rows
+// takes all tokens' whole rows into LDS, 117 MB through the L2s together, four bytes of X
+// for one of W; that, and the waves' rounds of load, wait and decode.
 template <int G, bool OFF, bool S32, int WI, int BJ, int KW, int D>
 __global__ __launch_bounds__(64 * KW) void i4_deep_kernel(I4Args a, int nw_tiles, int nb_tiles) {
   using Groups = StagedGroups<G, S32, WI>;
@@ -1014,8 +1016,9 @@ __global__ __launch_bounds__(64 * KW) void i4_deep_kernel(I4Args a, int nw_tiles
 // about two; and the decoding is kept beside other waves' products: with up to
 // 3 groups a wave reads its packed rows straight into registers, and half of
 // the waves decode the next block behind their products, under the barrier that
-// the others decode after (14336 x 4096, 4096 tokens: 422 us, 1.14 PF/s; all of
-// them after it 437; every wave at one priority 468).  Four groups are four
+// the others decode after (14336 x 4096, 4096 tokens: 438 us, 1.10 PF/s; on a
+// faster card 422, where all of them after it took 437, every wave at one priority
+// 468).  Four groups are four
 // waves to a SIMD, which cover each other without that, and their packed rows
 // come faster through LDS, by direct loads (64 x 64 tiles: 867 us against 987).
 //

@@ -576,8 +576,9 @@ template <int XT, int RT, bool I8, int NT, int VPT>
 __global__ __launch_bounds__(NT == kWave ? 256 : NT) void block_kernel(BlockArgs a) {
   constexpr int kRowsPer = NT == kWave ? 4 : 1;
   constexpr int kXs = XT == kF32 ? 4 : 2, kRs = RT == kF32 ? 4 : 2;
-  // one chunk a thread: gains and gates are loaded with x and r, before the first sum.  With more chunks the registers
-  // that they take cost more waves than the latency behind the sum (2048 x 8192, bf16: 30.5 us late, 33.5 early)
+  // one chunk a thread: gains and gates are loaded with x and r, before the first sum (1111 x 8192, fp32 stream: 29.2 us
+  // early, 30.2 late).  With more chunks the registers that they take cost more waves than the latency behind the sum
+  // (1024 x 16384, bf16: 32.6 us late, 39.4 early)
   constexpr bool kEarly = VPT == 1;
   const int t = int(threadIdx.x) % NT;
   const int64_t row = int64_t(blockIdx.x) * kRowsPer + (NT == kWave ? int(threadIdx.x) / kWave : 0);
@@ -667,7 +668,8 @@ __global__ __launch_bounds__(NT == kWave ? 256 : NT) void block_kernel(BlockArgs
 
 // Rows past the register form's 32768 values: a pass for the first norm's sum,
 // one that writes h, and one for y, which reads h back where it was kept and
-// computes it again where not.
+// computes it again where not.  512 x 65536, bf16, h kept: 87 us; of the 12 bytes a
+// value that it moves (x twice, r, h out and back, y), 4.6 TB/s, the operator needs 8.
 template <int XT, int RT, bool I8>
 __global__ __launch_bounds__(1024) void long_block_kernel(BlockArgs a) {
   constexpr int NT = 1024;
@@ -771,8 +773,9 @@ int run_block(const BlockRows& b, hipStream_t s) {
     }
     return int(UW_OK);
   };
-  // the norm's threads and chunks (run_rows), but one chunk a thread up to 4096 columns whatever the rows: two chunks
-  // take 2048 x 4096 in 15.9 us, one in 15.2
+  // the norm's threads and chunks (run_rows), but one chunk a thread up to 4096 columns whatever the rows: 256 x 4096 take
+  // 4.8 us (5.8 with two), 1200 11.3 (11.5).  From there on two would gain a little: 2048 x 4096, bf16 16.4 to 17.9 us
+  // with one, by how much the caches hold, 15.8 to 16.4 with two; 2048 x 8192 33 and 30
   if (chunks <= 64) return go(block_kernel<XT, RT, I8, 64, 1>, 256, 4);
   if (chunks <= 128) return go(block_kernel<XT, RT, I8, 64, 2>, 256, 4);
   if (chunks <= 256) return go(block_kernel<XT, RT, I8, 256, 1>, 256, 1);
